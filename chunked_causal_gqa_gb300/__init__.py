@@ -22,8 +22,14 @@ import torch
 
 from . import _binding
 from ._binding import PFA_BF16, PFA_F32, PfaError
+from .q8 import (Q8Cache, cache_read_q8, cache_write_q8, decode_attention_q8,
+                 decode_workspace_bytes_q8, prefill_attention_q8, prefill_workspace_bytes_q8,
+                 q8_cache, qk_norm_rope)
 
 __all__ = ["prefill_attention", "prefill_attention_cache", "prefill_attention_graph",
+           "Q8Cache", "q8_cache", "qk_norm_rope", "cache_write_q8", "cache_read_q8",
+           "decode_attention_q8", "decode_workspace_bytes_q8", "prefill_attention_q8",
+           "prefill_workspace_bytes_q8",
            "workspace_bytes", "schedule", "release_host_buffers",
            "last_device_error", "status_string", "version", "debug_configure", "PfaError",
            "PFA_F32", "PFA_BF16"]

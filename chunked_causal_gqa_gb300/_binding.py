@@ -28,7 +28,10 @@ EXPORTS = ("pfa_prefill_attention", "pfa_prefill_attention_ws", "pfa_workspace_b
            "pfa_prefill_attention_host", "pfa_host_buffer_bytes",
            "pfa_status_string",
            "pfa_last_device_error", "pfa_version", "pfa_debug_configure",
-           "pfa_debug_check_schedule", "pfa_debug_check_schedule_d512")
+           "pfa_debug_check_schedule", "pfa_debug_check_schedule_d512",
+           "pfa_qk_norm_rope", "pfa_cache_write_q8", "pfa_cache_read_q8",
+           "pfa_decode_attention_q8", "pfa_decode_workspace_bytes_q8",
+           "pfa_prefill_attention_q8", "pfa_prefill_workspace_bytes_q8")
 
 _lock = threading.Lock()
 _lib = None
@@ -98,6 +101,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.pfa_debug_check_schedule.restype = i32
         lib.pfa_debug_check_schedule_d512.argtypes = [i64, i64, i32, i32, i32, i32, ip, ip, ip]
         lib.pfa_debug_check_schedule_d512.restype = i32
+        f32 = ctypes.c_float
+        lib.pfa_qk_norm_rope.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, i32, i32, vp, vp,
+                                         f32, f32, vp, i32, i32, i32, i64, i64, i64, i64, i64, vp]
+        lib.pfa_cache_write_q8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, i32, i32,
+                                           i64, i32, i32, i64, i64, vp]
+        lib.pfa_cache_read_q8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i64, i32,
+                                          i32, i64, vp]
+        lib.pfa_decode_attention_q8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, i32,
+                                                i32, i32, f32, i32, i64, i64, i64, i32, vp, sz, vp]
+        lib.pfa_decode_workspace_bytes_q8.argtypes = [i64, i64, i32, i32, i32, i32,
+                                                      ctypes.POINTER(sz)]
+        lib.pfa_prefill_attention_q8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32,
+                                                 i32, f32, i32, i64, i64, i32, vp, sz, vp]
+        lib.pfa_prefill_workspace_bytes_q8.argtypes = [i64, i64, i32, i32, i32, i32, i32,
+                                                       ctypes.POINTER(sz)]
+        for name in EXPORTS[-7:]:
+            getattr(lib, name).restype = i32
         if path is None:
             _lib = lib
         return lib

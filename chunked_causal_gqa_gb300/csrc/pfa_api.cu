@@ -85,6 +85,19 @@ int device_state(int* dev_out, DeviceState** st_out) {
   return s.status;
 }
 
+}  // namespace
+
+int current_device(DeviceInfo* d) {
+  int dev = -1;
+  DeviceState* st = nullptr;
+  const int ds = device_state(&dev, &st);
+  if (ds != kOk) return ds;
+  d->device = dev;
+  d->num_sms = st->num_sms;
+  d->err = st->err;
+  return kOk;
+}
+
 // A pointer the GPU can read: device memory or managed memory of this device.
 bool device_accessible(const void* p, int dev) {
   cudaPointerAttributes a;
@@ -100,6 +113,8 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
+
+namespace {
 
 // ------------------------------------------------------------------ TMA maps
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,

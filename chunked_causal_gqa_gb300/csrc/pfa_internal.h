@@ -2,6 +2,7 @@
 // the kernel translation units.  Not part of the public interface.
 #pragma once
 #include <atomic>
+#include <cstddef>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -84,6 +85,18 @@ class DeviceOnce {
   std::atomic<int> state_[kDevices];  // 0 not done, 1 ok, -1 failed
 };
 
+// The current device, checked and set up on first use (pfa_api.cu).
+struct DeviceInfo {
+  int device;
+  int num_sms;
+  unsigned* err;  // device error word
+};
+int current_device(DeviceInfo* d);
+// Whether kernels on device `dev` can use p (device or managed memory).
+bool device_accessible(const void* p, int dev);
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
+bool overlaps(const void* a, size_t na, const void* b, size_t nb);
+
 // Encodes a 3-D tiled bf16 tensor map (innermost dimension first).
 // Returns 0 on success.  Results are cached by all arguments.
 int encode_tmap_bf16_3d(CUtensorMap* out, const void* base, const uint64_t dims[3],
@@ -126,5 +139,80 @@ inline size_t workspace_bytes_bf16(const Call& c, int* schedule = nullptr) {
 int check_schedule_bf16_d128(const Call& c, int sms, int* schedule, int* ctas);
 // The same for the head_dim-512 path (pfa_debug_check_schedule_d512).
 int check_schedule_bf16_d512(const Call& c, int sms, int* schedule, int* ctas);
+
+// ---- operators around the 8-bit cache (checked by pfa_q8_api.cu)
+
+// Where the new rows of B sequences of T tokens sit: token t of sequence b is
+// at position lengths[b] - T + t, or start_pos + t when lengths is null.
+struct Span {
+  int64_t B, T, start_pos;
+  const int64_t* lengths;
+};
+
+struct NormRopeCall {
+  const void *q, *k;
+  void *q_out, *k_out;
+  Span span;
+  int H, Hkv, D;
+  const void *q_weight, *k_weight;  // null: no norm
+  float eps, weight_offset;
+  const double* inv_freq;           // null: no rotation
+  int rot_dim, interleaved, dtype;
+  // elements from one token's row to the next, and from one head to the next of k_out
+  int64_t q_row, k_row, q_out_row, k_out_row, k_out_head;
+  int num_sms;
+  cudaStream_t stream;
+};
+int launch_norm_rope(const NormRopeCall& c);
+
+// An 8-bit cache: e4m3 codes [B][Hkv][max_seq_len][D] and fp32 scales
+// [B][Hkv][max_seq_len / block] for K and for V.
+struct CacheQ8 {
+  void *k8, *v8;
+  float *k_scale, *v_scale;
+  int64_t max_seq_len;
+  int block;
+};
+
+struct WriteQ8Call {
+  const void *k, *v;
+  CacheQ8 cache;
+  Span span;
+  int Hkv, D, dtype;
+  int64_t k_row, v_row;
+  unsigned* err;
+  int num_sms;
+  cudaStream_t stream;
+};
+int launch_cache_write_q8(const WriteQ8Call& c);
+
+struct ReadQ8Call {
+  CacheQ8 cache;
+  void *k_out, *v_out;
+  int64_t heads, start, rows;       // heads: B * Hkv blocks of max_seq_len rows
+  int64_t out_head;                 // elements from one head's rows to the next in the outputs
+  int D, dtype;
+  int num_sms;
+  cudaStream_t stream;
+};
+int launch_cache_read_q8(const ReadQ8Call& c);
+
+struct DecodeQ8Call {
+  const void* q;
+  void* out;
+  CacheQ8 cache;
+  Span span;
+  int H, Hkv, D, window, dtype;
+  float scale;
+  int64_t q_row, out_row;
+  unsigned* err;
+  int num_sms;
+  int device;
+  void* ws;
+  cudaStream_t stream;
+};
+// Workspace bytes of launch_decode_q8 for B sequences of T tokens.
+size_t decode_q8_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int num_sms);
+int launch_decode_q8(const DecodeQ8Call& c);
 
 }  // namespace pfa

@@ -1,0 +1,442 @@
+// pfa_q8_api.cu -- the C entry points of the operators around the 8-bit cache
+// (declared in include/pfa.h): argument checks and dispatch.  Checks that need
+// no device come first, so that a bad call is refused on any machine.
+#include "pfa_internal.h"
+
+#include "../../include/pfa.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace pfa {
+namespace {
+
+constexpr int64_t kMaxLen = ((int64_t)1 << 31) - 4096;  // positions and row counts
+
+size_t elem(int dtype) { return dtype == PFA_F32 ? 4 : 2; }
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) & (a - 1); }
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// n rows of `width` bytes, `pitch` bytes apart.
+struct Rows {
+  const void* p;
+  int64_t n;
+  size_t pitch, width;
+  size_t span() const { return (size_t)(n - 1) * pitch + width; }
+};
+
+// Whether two sets of rows share a byte.  Columns of one buffer (the same
+// pitch) are told apart by their column ranges; anything else by its span.
+bool share(const Rows& a, const Rows& b) {
+  if (!overlaps(a.p, a.span(), b.p, b.span())) return false;
+  if (a.pitch != b.pitch) return true;
+  const int64_t pitch = (int64_t)a.pitch;
+  int64_t d = ((int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p))) % pitch;
+  if (d < 0) d += pitch;  // b's first column in a's rows
+  return d < (int64_t)a.width || d + (int64_t)b.width > pitch;
+}
+
+int check_span(int64_t B, int64_t T, int64_t start_pos, const int64_t* lengths) {
+  if (B < 0 || T < 0 || B > kMaxLen || T > kMaxLen || B * T > kMaxLen) return PFA_ERR_SHAPE;
+  if (lengths) return misaligned(lengths, 8) ? PFA_ERR_ALIGNMENT : PFA_OK;
+  // without lengths: one sequence, its position known to the host
+  if (B > 1 || start_pos < 0 || start_pos > kMaxLen || start_pos + T > kMaxLen)
+    return PFA_ERR_SHAPE;
+  return PFA_OK;
+}
+
+// The shape of an 8-bit cache of `heads` blocks of rows.
+int check_cache(int64_t heads, int head_dim, int64_t cap, int block) {
+  if (heads < 0 || head_dim <= 0 || head_dim > 512 || head_dim % 16 != 0) return PFA_ERR_SHAPE;
+  if (block != 16 && block != 32 && block != 64 && block != 128) return PFA_ERR_SHAPE;
+  if (cap <= 0 || cap > kMaxLen || cap % block != 0) return PFA_ERR_SHAPE;
+  // sizes in bytes and work counts stay far inside 64 bits
+  if (heads > ((int64_t)1 << 50) / (cap * head_dim)) return PFA_ERR_SHAPE;
+  return PFA_OK;
+}
+int check_cache_pointers(const CacheQ8& c) {
+  if (!c.k8 || !c.v8 || !c.k_scale || !c.v_scale) return PFA_ERR_NULL;
+  if (misaligned(c.k8, 16) || misaligned(c.v8, 16) || misaligned(c.k_scale, 4) ||
+      misaligned(c.v_scale, 4))
+    return PFA_ERR_ALIGNMENT;
+  return PFA_OK;
+}
+bool cache_shares(const CacheQ8& c, int64_t heads, int head_dim, const void* p, size_t n) {
+  const size_t codes = (size_t)heads * c.max_seq_len * head_dim;
+  const size_t scales = (size_t)heads * (c.max_seq_len / c.block) * sizeof(float);
+  return overlaps(p, n, c.k8, codes) || overlaps(p, n, c.v8, codes) ||
+         overlaps(p, n, c.k_scale, scales) || overlaps(p, n, c.v_scale, scales);
+}
+bool accessible(const CacheQ8& c, int dev) {
+  return device_accessible(c.k8, dev) && device_accessible(c.v8, dev) &&
+         device_accessible(c.k_scale, dev) && device_accessible(c.v_scale, dev);
+}
+
+CacheQ8 cache_of(const void* k8, const void* v8, const float* k_scale, const float* v_scale,
+                 int64_t cap, int block) {
+  return CacheQ8{const_cast<void*>(k8), const_cast<void*>(v8), const_cast<float*>(k_scale),
+                 const_cast<float*>(v_scale), cap, block};
+}
+
+// Shapes of the attention entries.
+int check_attention(int64_t B, int64_t T, int H, int Hkv, int D, float scale, int dtype) {
+  if (dtype != PFA_F32 && dtype != PFA_BF16) return PFA_ERR_DTYPE;
+  if (B < 0 || T < 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || H / Hkv > 128) return PFA_ERR_SHAPE;
+  if (D != 128 && D != 512) return PFA_ERR_SHAPE;
+  if (!std::isfinite(scale)) return PFA_ERR_VALUE;
+  return PFA_OK;
+}
+
+// How a chunk of one sequence runs: its few rows straight from the codes, or
+// the visible cache rows read back into the workspace and the 16/32-bit
+// kernels on them.
+struct PrefillPlan {
+  bool direct;
+  int64_t lo, rows;       // cache rows [lo, lo + rows) are visible
+  size_t v_at, ws_at, total;
+  Call call;              // on the read-back rows
+};
+
+bool prefill_direct(int64_t T, int group) { return T * group <= 64; }
+
+int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window, float scale,
+                 int dtype, int64_t qkv_dim, int num_sms, void* stream, PrefillPlan* p) {
+  p->direct = prefill_direct(T, H / Hkv);
+  if (p->direct) {
+    p->total = decode_q8_workspace(1, T, H, Hkv, D, dtype, num_sms);
+    return PFA_OK;
+  }
+  p->lo = window > 0 ? std::max<int64_t>(0, start_pos - window + 1) : 0;
+  p->rows = start_pos + T - p->lo;
+  const size_t kv = round256((size_t)Hkv * p->rows * D * elem(dtype));
+  // causal and window masks depend on differences of positions only
+  const int rc = prepare_layout(nullptr, nullptr, nullptr, nullptr, T, start_pos - p->lo, H, Hkv,
+                                D, window, scale, dtype, qkv_dim, p->rows, 0, stream, false,
+                                &p->call);
+  if (rc != PFA_OK) return rc;
+  p->v_at = kv;
+  p->ws_at = 2 * kv;
+  p->call.ws_bytes = dtype == PFA_BF16 ? workspace_bytes_bf16(p->call) : 0;
+  p->total = p->ws_at + round256(p->call.ws_bytes);
+  return PFA_OK;
+}
+
+}  // namespace
+}  // namespace pfa
+
+using namespace pfa;
+
+extern "C" {
+
+int pfa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int64_t B, int64_t T,
+                     int64_t start_pos, const int64_t* lengths, int num_heads, int num_kv_heads,
+                     int head_dim, const void* q_weight, const void* k_weight, float eps,
+                     float weight_offset, const double* inv_freq, int rot_dim, int interleaved,
+                     int dtype, int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                     int64_t k_out_stride, int64_t k_out_head_stride, void* stream) {
+  if (dtype != PFA_F32 && dtype != PFA_BF16) return PFA_ERR_DTYPE;
+  if (num_heads <= 0 || num_kv_heads <= 0 || num_heads > 65536 || num_kv_heads > 65536)
+    return PFA_ERR_SHAPE;
+  if (head_dim <= 0 || head_dim > 512 || head_dim % 16 != 0) return PFA_ERR_SHAPE;
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0) return PFA_ERR_SHAPE;
+  int rc = check_span(B, T, start_pos, lengths);
+  if (rc != PFA_OK) return rc;
+  if (!std::isfinite(eps) || eps < 0.f || !std::isfinite(weight_offset)) return PFA_ERR_VALUE;
+  if (B == 0 || T == 0) return PFA_OK;
+  if (!q || !k || !q_out || !k_out || (rot_dim > 0 && !inv_freq)) return PFA_ERR_NULL;
+  const int64_t n = B * T, es = (int64_t)elem(dtype), D = head_dim;
+  const int64_t wq = num_heads * D, wk = num_kv_heads * D;
+  if (q_stride < wq || k_stride < wk || q_out_stride < wq || k_out_head_stride < D)
+    return PFA_ERR_SHAPE;
+  // k_out: heads inside a token's row, or tokens inside a head's rows (a cache)
+  const bool k_token_major = k_out_stride >= (num_kv_heads - 1) * k_out_head_stride + D;
+  const bool k_head_major = k_out_stride >= D && k_out_head_stride >= (n - 1) * k_out_stride + D;
+  if (!k_token_major && !k_head_major) return PFA_ERR_SHAPE;
+  if ((q_stride * es) % 16 || (k_stride * es) % 16 || (q_out_stride * es) % 16 ||
+      (k_out_stride * es) % 16 || (k_out_head_stride * es) % 16)
+    return PFA_ERR_ALIGNMENT;
+  if (misaligned(q, 16) || misaligned(k, 16) || misaligned(q_out, 16) || misaligned(k_out, 16) ||
+      misaligned(q_weight, 16) || misaligned(k_weight, 16) || misaligned(inv_freq, 8))
+    return PFA_ERR_ALIGNMENT;
+  const Rows rq{q, n, (size_t)(q_stride * es), (size_t)(wq * es)};
+  const Rows rk{k, n, (size_t)(k_stride * es), (size_t)(wk * es)};
+  const Rows oq{q_out, n, (size_t)(q_out_stride * es), (size_t)(wq * es)};
+  Rows ok{k_out, n, (size_t)(k_out_stride * es), (size_t)(wk * es)};
+  const bool k_rows = k_out_head_stride == D && k_token_major;
+  if (!k_rows) {  // one span over all of it
+    ok.n = 1;
+    ok.width = (size_t)(((num_kv_heads - 1) * k_out_head_stride + (n - 1) * k_out_stride + D) * es);
+    ok.pitch = ok.width;
+  }
+  const bool q_in_place = q_out == q && q_out_stride == q_stride;
+  const bool k_in_place = k_out == k && k_rows && k_out_stride == k_stride;
+  if ((!q_in_place && share(oq, rq)) || share(oq, rk) || share(oq, ok) ||
+      (!k_in_place && share(ok, rk)) || share(ok, rq))
+    return PFA_ERR_ALIAS;
+  const size_t wbytes = (size_t)(D * es), fbytes = (size_t)rot_dim / 2 * sizeof(double);
+  const Rows outs[] = {oq, ok};
+  for (const Rows& o : outs)
+    if ((q_weight && overlaps(o.p, o.span(), q_weight, wbytes)) ||
+        (k_weight && overlaps(o.p, o.span(), k_weight, wbytes)) ||
+        (rot_dim && overlaps(o.p, o.span(), inv_freq, fbytes)) ||
+        (lengths && overlaps(o.p, o.span(), lengths, (size_t)B * 8)))
+      return PFA_ERR_ALIAS;
+  DeviceInfo d;
+  if ((rc = current_device(&d)) != kOk) return rc;
+  const void* used[] = {q, k, q_out, k_out, q_weight, k_weight, rot_dim ? inv_freq : nullptr,
+                        lengths};
+  for (const void* p : used)
+    if (p && !device_accessible(p, d.device)) return PFA_ERR_DEVICE;
+  NormRopeCall c;
+  c.q = q; c.k = k; c.q_out = q_out; c.k_out = k_out;
+  c.span = Span{B, T, start_pos, lengths};
+  c.H = num_heads; c.Hkv = num_kv_heads; c.D = head_dim;
+  c.q_weight = q_weight; c.k_weight = k_weight;
+  c.eps = eps; c.weight_offset = weight_offset;
+  c.inv_freq = inv_freq; c.rot_dim = rot_dim; c.interleaved = interleaved ? 1 : 0;
+  c.dtype = dtype;
+  c.q_row = q_stride; c.k_row = k_stride; c.q_out_row = q_out_stride;
+  c.k_out_row = k_out_stride; c.k_out_head = k_out_head_stride;
+  c.num_sms = d.num_sms;
+  c.stream = static_cast<cudaStream_t>(stream);
+  return launch_norm_rope(c);
+}
+
+int pfa_cache_write_q8(const void* k, const void* v, void* k8, void* v8, float* k_scale,
+                       float* v_scale, int64_t B, int64_t T, int64_t start_pos,
+                       const int64_t* lengths, int num_kv_heads, int head_dim,
+                       int64_t max_seq_len, int block, int dtype, int64_t k_stride,
+                       int64_t v_stride, void* stream) {
+  if (dtype != PFA_F32 && dtype != PFA_BF16) return PFA_ERR_DTYPE;
+  if (num_kv_heads <= 0 || num_kv_heads > 65536) return PFA_ERR_SHAPE;
+  int rc = check_span(B, T, start_pos, lengths);
+  if (rc != PFA_OK) return rc;
+  if ((rc = check_cache(B * num_kv_heads, head_dim, max_seq_len, block)) != PFA_OK) return rc;
+  if (T > max_seq_len || (!lengths && start_pos + T > max_seq_len)) return PFA_ERR_SHAPE;
+  if (B == 0 || T == 0) return PFA_OK;
+  if (!k || !v) return PFA_ERR_NULL;
+  WriteQ8Call c;
+  c.cache = CacheQ8{k8, v8, k_scale, v_scale, max_seq_len, block};
+  if ((rc = check_cache_pointers(c.cache)) != PFA_OK) return rc;
+  const int64_t es = (int64_t)elem(dtype), width = (int64_t)num_kv_heads * head_dim;
+  if (k_stride < width || v_stride < width) return PFA_ERR_SHAPE;
+  if ((k_stride * es) % 16 || (v_stride * es) % 16 || misaligned(k, 16) || misaligned(v, 16))
+    return PFA_ERR_ALIGNMENT;
+  const int64_t heads = B * num_kv_heads;
+  const size_t codes = (size_t)heads * max_seq_len * head_dim;
+  const size_t scales = (size_t)heads * (max_seq_len / block) * sizeof(float);
+  const Rows rk{k, B * T, (size_t)(k_stride * es), (size_t)(width * es)};
+  const Rows rv{v, B * T, (size_t)(v_stride * es), (size_t)(width * es)};
+  if (cache_shares(c.cache, heads, head_dim, k, rk.span()) ||
+      cache_shares(c.cache, heads, head_dim, v, rv.span()) || overlaps(k8, codes, v8, codes) ||
+      overlaps(k8, codes, k_scale, scales) || overlaps(k8, codes, v_scale, scales) ||
+      overlaps(v8, codes, k_scale, scales) || overlaps(v8, codes, v_scale, scales) ||
+      overlaps(k_scale, scales, v_scale, scales) ||
+      (lengths && cache_shares(c.cache, heads, head_dim, lengths, (size_t)B * 8)))
+    return PFA_ERR_ALIAS;
+  DeviceInfo d;
+  if ((rc = current_device(&d)) != kOk) return rc;
+  if (!device_accessible(k, d.device) || !device_accessible(v, d.device) ||
+      !accessible(c.cache, d.device) || (lengths && !device_accessible(lengths, d.device)))
+    return PFA_ERR_DEVICE;
+  c.k = k; c.v = v;
+  c.span = Span{B, T, start_pos, lengths};
+  c.Hkv = num_kv_heads; c.D = head_dim; c.dtype = dtype;
+  c.k_row = k_stride; c.v_row = v_stride;
+  c.err = d.err; c.num_sms = d.num_sms;
+  c.stream = static_cast<cudaStream_t>(stream);
+  return launch_cache_write_q8(c);
+}
+
+int pfa_cache_read_q8(const void* k8, const void* v8, const float* k_scale, const float* v_scale,
+                      void* k_out, void* v_out, int64_t heads, int64_t start, int64_t rows,
+                      int head_dim, int64_t max_seq_len, int block, int dtype,
+                      int64_t out_head_stride, void* stream) {
+  if (dtype != PFA_F32 && dtype != PFA_BF16) return PFA_ERR_DTYPE;
+  int rc = check_cache(heads, head_dim, max_seq_len, block);
+  if (rc != PFA_OK) return rc;
+  if (heads > kMaxLen || start < 0 || rows < 0 || start > max_seq_len ||
+      rows > max_seq_len - start)
+    return PFA_ERR_SHAPE;
+  if (heads == 0 || rows == 0) return PFA_OK;
+  ReadQ8Call c;
+  c.cache = cache_of(k8, v8, k_scale, v_scale, max_seq_len, block);
+  if ((rc = check_cache_pointers(c.cache)) != PFA_OK) return rc;
+  if (!k_out || !v_out) return PFA_ERR_NULL;
+  const int64_t es = (int64_t)elem(dtype), width = rows * head_dim;
+  if (out_head_stride < width) return PFA_ERR_SHAPE;
+  if ((out_head_stride * es) % 16 || misaligned(k_out, 16) || misaligned(v_out, 16))
+    return PFA_ERR_ALIGNMENT;
+  const Rows ok{k_out, heads, (size_t)(out_head_stride * es), (size_t)(width * es)};
+  const Rows ov{v_out, heads, (size_t)(out_head_stride * es), (size_t)(width * es)};
+  if (share(ok, ov) || cache_shares(c.cache, heads, head_dim, k_out, ok.span()) ||
+      cache_shares(c.cache, heads, head_dim, v_out, ov.span()))
+    return PFA_ERR_ALIAS;
+  DeviceInfo d;
+  if ((rc = current_device(&d)) != kOk) return rc;
+  if (!accessible(c.cache, d.device) || !device_accessible(k_out, d.device) ||
+      !device_accessible(v_out, d.device))
+    return PFA_ERR_DEVICE;
+  c.k_out = k_out; c.v_out = v_out;
+  c.heads = heads; c.start = start; c.rows = rows; c.out_head = out_head_stride;
+  c.D = head_dim; c.dtype = dtype;
+  c.num_sms = d.num_sms;
+  c.stream = static_cast<cudaStream_t>(stream);
+  return launch_cache_read_q8(c);
+}
+
+int pfa_decode_workspace_bytes_q8(int64_t B, int64_t T, int num_heads, int num_kv_heads,
+                                  int head_dim, int dtype, size_t* bytes) {
+  if (!bytes) return PFA_ERR_NULL;
+  *bytes = 0;
+  int rc = check_attention(B, T, num_heads, num_kv_heads, head_dim, 1.f, dtype);
+  if (rc != PFA_OK) return rc;
+  if (B > kMaxLen || T > kMaxLen || T * (num_heads / num_kv_heads) > PFA_DECODE_MAX_ROWS)
+    return PFA_ERR_SHAPE;
+  if (B == 0 || T == 0) return PFA_OK;
+  DeviceInfo d;
+  if ((rc = current_device(&d)) != kOk) return rc;
+  *bytes = decode_q8_workspace(B, T, num_heads, num_kv_heads, head_dim, dtype, d.num_sms);
+  return PFA_OK;
+}
+
+int pfa_decode_attention_q8(const void* q, const void* k8, const void* v8, const float* k_scale,
+                            const float* v_scale, void* out, int64_t B, int64_t T,
+                            const int64_t* lengths, int num_heads, int num_kv_heads, int head_dim,
+                            int window, float scale, int dtype, int64_t q_stride,
+                            int64_t out_stride, int64_t max_seq_len, int block, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  int rc = check_attention(B, T, num_heads, num_kv_heads, head_dim, scale, dtype);
+  if (rc != PFA_OK) return rc;
+  if (B > kMaxLen || T > kMaxLen || T * (num_heads / num_kv_heads) > PFA_DECODE_MAX_ROWS)
+    return PFA_ERR_SHAPE;
+  if ((rc = check_cache(B * num_kv_heads, head_dim, max_seq_len, block)) != PFA_OK) return rc;
+  if (B == 0 || T == 0) return PFA_OK;
+  if (!lengths) return PFA_ERR_NULL;
+  if ((rc = check_span(B, T, 0, lengths)) != PFA_OK) return rc;
+  DecodeQ8Call c;
+  c.cache = cache_of(k8, v8, k_scale, v_scale, max_seq_len, block);
+  if ((rc = check_cache_pointers(c.cache)) != PFA_OK) return rc;
+  if (!q || !out) return PFA_ERR_NULL;
+  const int64_t es = (int64_t)elem(dtype), width = (int64_t)num_heads * head_dim;
+  if (q_stride < width || out_stride < width) return PFA_ERR_SHAPE;
+  if ((q_stride * es) % 16 || (out_stride * es) % 16 || misaligned(q, 16) || misaligned(out, 16) ||
+      misaligned(workspace, 256))
+    return PFA_ERR_ALIGNMENT;
+  const int64_t heads = B * num_kv_heads;
+  const Rows rq{q, B * T, (size_t)(q_stride * es), (size_t)(width * es)};
+  const Rows ro{out, B * T, (size_t)(out_stride * es), (size_t)(width * es)};
+  if (share(ro, rq) || cache_shares(c.cache, heads, head_dim, out, ro.span()) ||
+      overlaps(out, ro.span(), lengths, (size_t)B * 8))
+    return PFA_ERR_ALIAS;
+  DeviceInfo d;
+  if ((rc = current_device(&d)) != kOk) return rc;
+  const size_t need =
+      decode_q8_workspace(B, T, num_heads, num_kv_heads, head_dim, dtype, d.num_sms);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return PFA_ERR_SCRATCH;
+    if (overlaps(workspace, need, q, rq.span()) || overlaps(workspace, need, out, ro.span()) ||
+        overlaps(workspace, need, lengths, (size_t)B * 8) ||
+        cache_shares(c.cache, heads, head_dim, workspace, need))
+      return PFA_ERR_ALIAS;
+    if (!device_accessible(workspace, d.device)) return PFA_ERR_DEVICE;
+  }
+  if (!device_accessible(q, d.device) || !device_accessible(out, d.device) ||
+      !device_accessible(lengths, d.device) || !accessible(c.cache, d.device))
+    return PFA_ERR_DEVICE;
+  c.q = q; c.out = out;
+  c.span = Span{B, T, 0, lengths};
+  c.H = num_heads; c.Hkv = num_kv_heads; c.D = head_dim;
+  c.window = window > 0 ? window : 0; c.dtype = dtype; c.scale = scale;
+  c.q_row = q_stride; c.out_row = out_stride;
+  c.err = d.err; c.num_sms = d.num_sms; c.device = d.device;
+  c.ws = workspace;
+  c.stream = static_cast<cudaStream_t>(stream);
+  return launch_decode_q8(c);
+}
+
+int pfa_prefill_workspace_bytes_q8(int64_t T, int64_t start_pos, int num_heads, int num_kv_heads,
+                                   int head_dim, int window, int dtype, size_t* bytes) {
+  if (!bytes) return PFA_ERR_NULL;
+  *bytes = 0;
+  int rc = check_attention(1, T, num_heads, num_kv_heads, head_dim, 1.f, dtype);
+  if (rc != PFA_OK) return rc;
+  if ((rc = check_span(1, T, start_pos, nullptr)) != PFA_OK) return rc;
+  if (T == 0) return PFA_OK;
+  DeviceInfo d;
+  if ((rc = current_device(&d)) != kOk) return rc;
+  PrefillPlan plan;
+  rc = prefill_plan(T, start_pos, num_heads, num_kv_heads, head_dim, window, 1.f, dtype,
+                    (int64_t)num_heads * head_dim, d.num_sms, nullptr, &plan);
+  if (rc == PFA_OK) *bytes = plan.total;
+  return rc;
+}
+
+int pfa_prefill_attention_q8(const void* q, const void* k8, const void* v8, const float* k_scale,
+                             const float* v_scale, void* out, int64_t T, int64_t start_pos,
+                             int num_heads, int num_kv_heads, int head_dim, int window,
+                             float scale, int dtype, int64_t qkv_dim, int64_t max_seq_len,
+                             int block, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_attention(1, T, num_heads, num_kv_heads, head_dim, scale, dtype);
+  if (rc != PFA_OK) return rc;
+  if ((rc = check_span(1, T, start_pos, nullptr)) != PFA_OK) return rc;
+  if ((rc = check_cache(num_kv_heads, head_dim, max_seq_len, block)) != PFA_OK) return rc;
+  if (start_pos + T > max_seq_len) return PFA_ERR_SHAPE;
+  if (T == 0) return PFA_OK;
+  const CacheQ8 cache = cache_of(k8, v8, k_scale, v_scale, max_seq_len, block);
+  if ((rc = check_cache_pointers(cache)) != PFA_OK) return rc;
+  if (!q || !out) return PFA_ERR_NULL;
+  const int64_t es = (int64_t)elem(dtype), width = (int64_t)num_heads * head_dim;
+  if (qkv_dim < width) return PFA_ERR_SHAPE;
+  if ((qkv_dim * es) % 16 || misaligned(q, 16) || misaligned(out, 16) ||
+      misaligned(workspace, 256))
+    return PFA_ERR_ALIGNMENT;
+  const Rows rq{q, T, (size_t)(qkv_dim * es), (size_t)(width * es)};
+  const Rows ro{out, T, (size_t)(qkv_dim * es), (size_t)(width * es)};
+  if (share(ro, rq) || cache_shares(cache, num_kv_heads, head_dim, out, ro.span()))
+    return PFA_ERR_ALIAS;
+  DeviceInfo d;
+  if ((rc = current_device(&d)) != kOk) return rc;
+  PrefillPlan plan;
+  rc = prefill_plan(T, start_pos, num_heads, num_kv_heads, head_dim, window, scale, dtype, qkv_dim,
+                    d.num_sms, stream, &plan);
+  if (rc != PFA_OK) return rc;
+  if (plan.total > 0) {
+    if (!workspace || workspace_bytes < plan.total) return PFA_ERR_SCRATCH;
+    if (overlaps(workspace, plan.total, q, rq.span()) ||
+        overlaps(workspace, plan.total, out, ro.span()) ||
+        cache_shares(cache, num_kv_heads, head_dim, workspace, plan.total))
+      return PFA_ERR_ALIAS;
+    if (!device_accessible(workspace, d.device)) return PFA_ERR_DEVICE;
+  }
+  if (!device_accessible(q, d.device) || !device_accessible(out, d.device) ||
+      !accessible(cache, d.device))
+    return PFA_ERR_DEVICE;
+  if (plan.direct) {
+    DecodeQ8Call c;
+    c.q = q; c.out = out; c.cache = cache;
+    c.span = Span{1, T, start_pos, nullptr};
+    c.H = num_heads; c.Hkv = num_kv_heads; c.D = head_dim;
+    c.window = window > 0 ? window : 0; c.dtype = dtype; c.scale = scale;
+    c.q_row = qkv_dim; c.out_row = qkv_dim;
+    c.err = d.err; c.num_sms = d.num_sms; c.device = d.device;
+    c.ws = workspace;
+    c.stream = static_cast<cudaStream_t>(stream);
+    return launch_decode_q8(c);
+  }
+  char* base = static_cast<char*>(workspace);
+  ReadQ8Call r;
+  r.cache = cache;
+  r.k_out = base; r.v_out = base + plan.v_at;
+  r.heads = num_kv_heads; r.start = plan.lo; r.rows = plan.rows;
+  r.out_head = plan.rows * head_dim;
+  r.D = head_dim; r.dtype = dtype; r.num_sms = d.num_sms;
+  r.stream = static_cast<cudaStream_t>(stream);
+  if ((rc = launch_cache_read_q8(r)) != kOk) return rc;
+  plan.call.q = q; plan.call.out = out;
+  plan.call.k = r.k_out; plan.call.v = r.v_out;
+  plan.call.ws = plan.call.ws_bytes ? base + plan.ws_at : nullptr;
+  return dispatch(plan.call, dtype);
+}
+
+}  // extern "C"

@@ -62,9 +62,11 @@ typedef enum {
     PFA_ERR_VALUE = -8,      /* scale is not a finite number                        */
     PFA_ERR_ALIAS = -9,      /* out overlaps q, k_cache or v_cache                  */
     PFA_ERR_SCRATCH = -10,   /* the shape needs more scratch than
-                                pfa_prefill_attention_noalloc holds                 */
-    PFA_ERR_LENGTHS = -11    /* pfa_prefill_attention_graph: the {T, start_pos} read
-                                on the device did not fit its capacities (reported
+                                pfa_prefill_attention_noalloc holds, or than the
+                                workspace given to an 8-bit cache's attention       */
+    PFA_ERR_LENGTHS = -11    /* lengths read on the device ({T, start_pos} of
+                                pfa_prefill_attention_graph, the 8-bit cache's
+                                lengths) did not fit the capacities (reported
                                 after a sync by pfa_last_device_error)              */
 } pfa_status;
 
@@ -384,6 +386,155 @@ PFA_API int pfa_prefill_attention_noalloc(const void *q, const void *k_cache,
                                           int head_dim, int window, float scale, int dtype,
                                           void *stream);
 
+/*
+ * Operators around an 8-bit KV cache
+ * ==================================
+ *
+ * The 8-bit cache of B sequences holds, for K and for V,
+ *   codes   [B][num_kv_heads][max_seq_len][head_dim] e4m3 (1 byte an element)
+ *   scales  [B][num_kv_heads][max_seq_len / block] fp32, one for each head and
+ *           block of `block` consecutive rows (16, 32, 64 or 128; max_seq_len is
+ *           a multiple of it)
+ * and stands for code * scale.  Scales are powers of two as
+ * pfa_cache_write_q8 makes them (0 for a block of zeros).  Key j of a sequence
+ * is in row j; one sequence's part (a slot) is itself a cache with B = 1.
+ * Code pointers are 16-byte aligned, max_seq_len * head_dim may pass 2^31.
+ *
+ * Where new tokens sit: with `lengths` (device pointer, B int64, read when the
+ * kernel runs, so that a captured graph replays for other lengths) sequence b
+ * has lengths[b] tokens after the call's T and its token t is at position
+ * lengths[b] - T + t; without (NULL) there is one sequence and token t is at
+ * start_pos + t.  lengths[b] < T pads the sequence in front: its first
+ * T - lengths[b] tokens have negative positions; lengths[b] = 0 is an empty
+ * slot.  lengths[b] < 0 or > max_seq_len: nothing of that sequence is written and
+ * PFA_ERR_LENGTHS is recorded for pfa_last_device_error.
+ *
+ * Row b * T + t of a token-major array starts at (b * T + t) * its stride
+ * (elements; stride * element size a multiple of 16 bytes), heads and elements
+ * dense inside it, so columns of one projection buffer can be passed.
+ *
+ * All calls are asynchronous on `stream`, allocate nothing, and give
+ * results that are a deterministic function of their inputs.  As for
+ * pfa_prefill_attention_graph, the first call on a device must not be under
+ * capture.  Argument errors are returned before anything is enqueued.
+ */
+
+/*
+ * pfa_qk_norm_rope -- RMS norm of each query and key head and rotation of its
+ * position, one pass.  fp32 arithmetic, one rounding at the end.
+ *
+ *   q, k           [B * T] rows of num_heads (num_kv_heads) heads of head_dim
+ *                  elements, q_stride (k_stride) elements apart.
+ *   q_out, k_out   the same shapes.  q_out may be q with the same stride, and
+ *                  k_out k; any other overlap is PFA_ERR_ALIAS.  Head h of
+ *                  row r of k_out is at r * k_out_stride + h * k_out_head_stride, so
+ *                  it can be rows of a 16/32-bit cache [num_kv_heads][max_seq_len][head_dim]
+ *                  (k_out_stride = head_dim, k_out_head_stride = max_seq_len * head_dim).
+ *   q_weight, k_weight  [head_dim] of the same dtype, or NULL: no norm.
+ *                  y = x * rsqrt(mean(x^2) + eps) * (weight + weight_offset).
+ *   inv_freq       device, rot_dim / 2 doubles: radians a position (not NULL
+ *                  unless rot_dim is 0).  The angle position * inv_freq is reduced
+ *                  to a fraction of a turn in 64 bits.
+ *   rot_dim        elements of each head that are rotated, from its start; a
+ *                  multiple of 16, <= head_dim.  Pairs (i, i + rot_dim / 2), or
+ *                  (2 i, 2 i + 1) when interleaved != 0.
+ *   head_dim       a multiple of 16 up to 512.
+ * Rows at negative positions (padding) are written as zeros.
+ */
+PFA_API int pfa_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int64_t B,
+                             int64_t T, int64_t start_pos, const int64_t *lengths, int num_heads,
+                             int num_kv_heads, int head_dim, const void *q_weight,
+                             const void *k_weight, float eps, float weight_offset,
+                             const double *inv_freq, int rot_dim, int interleaved, int dtype,
+                             int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                             int64_t k_out_stride, int64_t k_out_head_stride, void *stream);
+
+/*
+ * pfa_cache_write_q8 -- quantise T new tokens of each sequence into its cache.
+ *
+ *   k, v    [B * T] rows of num_kv_heads heads of head_dim elements (dtype),
+ *           k_stride (v_stride) elements apart.
+ *   k8, v8, k_scale, v_scale   the cache; written in place.
+ *   head_dim  a multiple of 16 up to 512.
+ * For each head and block that new rows touch, with low the first new position:
+ *   s_old = the block's scale if it starts below low, else 0
+ *   s_new = max(s_old, the smallest power of two s >= 2^-126 with a / s <= 448)
+ *           a = the largest magnitude of the block's new finite elements (0: s_old)
+ *   rows below low:  code <- e4m3(code * s_old / s_new)
+ *   new rows:        code <- e4m3(x / s_new), NaN for an x that is not finite
+ * (e4m3(): nearest, ties to even).  Rows behind the new ones keep their codes;
+ * they belong to no token.  Writing the same tokens again gives the same cache.
+ */
+PFA_API int pfa_cache_write_q8(const void *k, const void *v, void *k8, void *v8, float *k_scale,
+                               float *v_scale, int64_t B, int64_t T, int64_t start_pos,
+                               const int64_t *lengths, int num_kv_heads, int head_dim,
+                               int64_t max_seq_len, int block, int dtype, int64_t k_stride,
+                               int64_t v_stride, void *stream);
+
+/*
+ * pfa_cache_read_q8 -- rows start .. start + rows - 1 of every head as dtype:
+ * k_out, v_out [heads] blocks of [rows][head_dim] elements, out_head_stride
+ * elements apart; heads = B * num_kv_heads.  code * scale is rounded once
+ * (exact for power-of-two scales within the type's range).
+ */
+PFA_API int pfa_cache_read_q8(const void *k8, const void *v8, const float *k_scale,
+                              const float *v_scale, void *k_out, void *v_out, int64_t heads,
+                              int64_t start, int64_t rows, int head_dim, int64_t max_seq_len,
+                              int block, int dtype, int64_t out_head_stride, void *stream);
+
+/* Most rows T * num_heads / num_kv_heads of pfa_decode_attention_q8. */
+#define PFA_DECODE_MAX_ROWS 1024
+
+/*
+ * pfa_decode_attention_q8 -- attention of the T newest tokens of each of B
+ * sequences over its 8-bit cache: the operation of pfa_prefill_attention (GQA,
+ * causal, optional window, softmax) with K and V = code * scale.
+ *
+ *   q, out    [B * T] rows of num_heads heads, q_stride / out_stride apart; out
+ *             overlaps nothing else.  Only its num_heads * head_dim elements a row
+ *             are written.
+ *   lengths   device, B int64 (required).  Rows at negative positions (padding
+ *             and empty slots) are zeros.
+ *   head_dim  128 or 512; num_heads / num_kv_heads <= 128;
+ *             T * num_heads / num_kv_heads <= PFA_DECODE_MAX_ROWS.
+ *   workspace device, 256-byte aligned, of pfa_decode_workspace_bytes_q8 bytes
+ *             (PFA_ERR_SCRATCH if it is NULL or smaller).  Its contents on entry do
+ *             not matter.  Calls that can run at the same time (two captured
+ *             graphs among them) must not share one.
+ * Cache rows that no row of the sequence's T tokens sees are not read into the
+ * result, whatever they hold.  A key that some of the T tokens see and others do
+ * not must be finite (its weight is zero for the others, and zero times NaN is NaN).
+ */
+PFA_API int pfa_decode_attention_q8(const void *q, const void *k8, const void *v8,
+                                    const float *k_scale, const float *v_scale, void *out,
+                                    int64_t B, int64_t T, const int64_t *lengths, int num_heads,
+                                    int num_kv_heads, int head_dim, int window, float scale,
+                                    int dtype, int64_t q_stride, int64_t out_stride,
+                                    int64_t max_seq_len, int block, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+PFA_API int pfa_decode_workspace_bytes_q8(int64_t B, int64_t T, int num_heads, int num_kv_heads,
+                                          int head_dim, int dtype, size_t *bytes);
+
+/*
+ * pfa_prefill_attention_q8 -- pfa_prefill_attention_cache (linear) on one
+ * sequence's 8-bit cache: T tokens at start_pos .., whose own rows have been
+ * written.  q and out rows are qkv_dim elements apart.  A chunk of few rows runs
+ * on the codes; a longer one reads the visible rows back into the workspace and
+ * runs the 16/32-bit kernels on them (the softmax weights are then rounded as
+ * those kernels round them).  workspace: pfa_prefill_workspace_bytes_q8 bytes
+ * (PFA_ERR_SCRATCH otherwise), 256-byte aligned, not shared by calls that can run
+ * at the same time.  head_dim and heads as for pfa_decode_attention_q8.
+ */
+PFA_API int pfa_prefill_attention_q8(const void *q, const void *k8, const void *v8,
+                                     const float *k_scale, const float *v_scale, void *out,
+                                     int64_t T, int64_t start_pos, int num_heads,
+                                     int num_kv_heads, int head_dim, int window, float scale,
+                                     int dtype, int64_t qkv_dim, int64_t max_seq_len, int block,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+PFA_API int pfa_prefill_workspace_bytes_q8(int64_t T, int64_t start_pos, int num_heads,
+                                           int num_kv_heads, int head_dim, int window, int dtype,
+                                           size_t *bytes);
+
 /* Human-readable name of a pfa_status value (static storage, never NULL). */
 PFA_API const char *pfa_status_string(int status);
 
@@ -391,8 +542,8 @@ PFA_API const char *pfa_status_string(int status);
  * pfa_last_device_error -- synchronise `stream`, then return and clear the
  * device-side error word of the current device: PFA_OK, PFA_ERR_TIMEOUT if
  * a kernel launched since the last call gave up on a wait, or
- * PFA_ERR_LENGTHS if a pfa_prefill_attention_graph launch found its
- * run-time lengths out of range (timeouts take precedence).  Returns
+ * PFA_ERR_LENGTHS if a pfa_prefill_attention_graph launch, or a launch of an
+ * operator of the 8-bit cache, found its run-time lengths out of range (timeouts take precedence).  Returns
  * PFA_ERR_DEVICE if the stream cannot be synchronised (the CUDA error is then
  * the runtime's).
  */
