@@ -1,23 +1,56 @@
 // pfa_decode_q8.cu -- attention of few tokens of a batch of sequences over
-// their 8-bit caches.
+// their 8-bit caches, on the tensor cores.
 //
-// One block per (sequence, token, query head): tiles of 128 keys, a thread
-// scores one key, the block takes the tile's maximum and sum, then each thread
-// accumulates its columns of P.V (running maximum and sum, fp32).
+// For each sequence and kv head the T * group query rows form tiles of 16 rows
+// (fp32: 8), and for each tile
+//   s_j = scale * ks_j * <q, k8_j>,  out = sum_j 2^(s_j log2 e - m) vs_j v8_j / sum_j 2^(s_j log2 e - m)
+// with the running maximum m, the sum and the output in fp32.  A cache byte is
+// read once for all rows of a tile, so with up to 16 rows HBM's bytes bound it.
+//
+// Products: mma.sync m16n8k16 on halves.  e4m3 is exact in half; q is scaled
+// to 2^13..2^14 by a power of two for each row, which makes bf16 q exact but for
+// elements 2^27 below the row's largest; the weights, times their block's scale
+// over the largest seen so far and 2^14, are rounded to half (2^-11, finer
+// than the bf16 output).  For fp32, q and the weights are a high and a low half:
+// the tile's rows 8-15 hold the low halves of rows 0-7, so the same instructions
+// give 21 bits.  tcgen05 would need 128 rows or K and V staged as its operands;
+// the tensor work of these shapes is a third of the time of the bytes.
+//
+// Fragments straight from the rows: the contraction's order is free as long as
+// both operands agree, so a lane reads 16-byte pieces of a K row and takes each
+// word of four elements as its part of one k16 step; likewise output columns, so
+// a lane reads 16 bytes of four V rows and pairs the rows' bytes with prmt.
+//
+// Work split: tiles of 32 keys ("units") of all sequences, heads and row tiles
+// form one list, cut into equal runs, one for each block (one block an SM).
+// Eight warps take the run's units in turn, each with its own ring of three
+// stages filled by cp.async (no barrier in the loop); their sums join in shared
+// memory where a run leaves a head.  What covers a head alone is stored as
+// output, what covers part of it goes to the workspace, and a second kernel,
+// launched so that its start overlaps, joins the parts in order.
+//
+// head_dim 512: four warps share a unit, each with 128 columns of K and V; the
+// scores' four partial sums are exchanged through shared memory.
 #include "pfa_internal.h"
 #include "pfa_ptx.cuh"
 #include "pfa_q8.cuh"
 
 #include "../../include/pfa.h"
 
+#include <algorithm>
 #include <cmath>
-#include <cuda_fp8.h>
 
 namespace pfa {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kMaxD = 512;
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kUnit = 32;                      // keys of a unit
+constexpr int kStages = 3;
+constexpr int kHalf = kUnit * 128;             // bytes of a warp's K (or V) part of a stage
+constexpr int kStageBytes = 2 * kHalf;
+constexpr int kMaxEntries = 4096;              // (sequence, row tile) pairs of one launch
+constexpr int kJoinBytes = 32768;              // joins: 8 row sums of 128 floats for each warp
+constexpr float kWeightScale = 16384.f;
 
 struct Params {
   const void* q;
@@ -25,88 +58,642 @@ struct Params {
   const uint8_t *k8, *v8;
   const float *k_scale, *v_scale;
   const int64_t* lengths;
-  int64_t B, T, start_pos, cap, q_row, out_row;
-  int H, Hkv, D, window, block;
+  int64_t T, start_pos, q_row, out_row;
+  int64_t b0;                 // first sequence of this launch
+  int cap, H, Hkv, group, window, block_shift;
+  int rows, tiles, entries;   // T * group, row tiles of a sequence, entries of this launch
   float scale_log2;
   unsigned* err;
+  int64_t* prefix;            // workspace: units before each entry
+  float* parts;               // workspace: slots of partial sums
 };
 
-__device__ __forceinline__ float get(const float* p) { return *p; }
-__device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+// A tile of rows of one sequence and the keys that they see.
+struct Entry {
+  int64_t b;
+  int end, r0, nr;    // sequence length; first row of the tile, rows
+  int lo, hi;         // keys [lo, hi] are seen by some row
+  int u0, n;          // units u0 .. u0 + n - 1 hold them
+  bool bad;
+};
+
+template <int RM>
+__device__ __forceinline__ Entry entry_of(const Params& p, int e) {
+  Entry x;
+  x.b = p.b0 + e / p.tiles;
+  x.r0 = e % p.tiles * RM;
+  x.nr = min(RM, p.rows - x.r0);
+  const int64_t end = p.lengths ? p.lengths[x.b] : p.start_pos + p.T;
+  x.bad = end < 0 || end > p.cap;
+  x.end = x.bad ? 0 : (int)end;
+  const int first = x.end - (int)p.T;
+  x.hi = first + (x.r0 + x.nr - 1) / p.group;
+  x.lo = p.window > 0 ? max(0, first + x.r0 / p.group - p.window + 1) : 0;
+  x.u0 = x.lo / kUnit;
+  x.n = x.bad || x.hi < 0 ? 0 : x.hi / kUnit - x.u0 + 1;
+  return x;
+}
+
+// The run of block c of w: [c * U / w, (c + 1) * U / w).
+__device__ __forceinline__ int64_t run_start(int64_t c, int64_t U, int64_t w) { return c * U / w; }
+// The block whose run holds unit x.
+__device__ __forceinline__ int64_t run_of(int64_t x, int64_t U, int64_t w) {
+  return ((x + 1) * w - 1) / U;
+}
+// Blocks that get a run: enough units for each of a block's teams.
+template <int TEAMS>
+__device__ __forceinline__ int64_t runs(int64_t U, int64_t blocks) {
+  return min(blocks, (U + TEAMS - 1) / TEAMS);
+}
+
+// Floats of a partial-sum slot: rows of output, then {m, l} of each row.
+template <int RM, int D>
+__host__ __device__ constexpr int slot_floats() { return RM * D + RM * 2; }
+
+// Pieces of 16 bytes of a row are permuted by its place in a group of eight, so
+// that K fragments (two rows, four pieces) and V fragments (every other row, two
+// pieces) of eight lanes fall in distinct banks.
+__device__ __forceinline__ int swizzle(int r) {
+  return (((r ^ (r >> 1)) & 1) << 2) | ((r >> 1) & 2) | ((r >> 1) & 1);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+               :: "r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// a, b -> high halves and what they leave out.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = half2_of(a - f.x, b - f.y);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Walks the units of a run that belong to one team.
+template <int RM, int TEAMS>
+struct Cursor {
+  const Params& p;
+  int64_t at, stop;    // units of the run from the current piece on: [at, stop)
+  int e, h;            // entry and kv head of the piece
+  Entry x;
+  int k, kend;         // the team's unit inside the head, end of the piece
+  int k_first;         // first unit of the piece
+  __device__ Cursor(const Params& p, int64_t at, int64_t stop, int e, int64_t into, int team)
+      : p(p), at(at), stop(stop), e(e) {
+    x = entry_of<RM>(p, e);
+    h = x.n > 0 ? (int)(into / x.n) : 0;
+    piece(x.n > 0 ? (int)(into % x.n) : 0, team);
+  }
+  __device__ void piece(int first, int team) {
+    k_first = first;
+    const int64_t left = stop - at;
+    kend = left < x.n - first ? first + (int)left : x.n;
+    k = first + team;
+  }
+  __device__ bool done() const { return at >= stop; }
+  __device__ void next_piece(int team) {
+    at += kend - k_first;
+    if (at >= stop) return;
+    if (++h == p.Hkv) {
+      h = 0;
+      do {
+        if (++e >= p.entries) {  // only if the lengths changed under the kernel
+          at = stop;
+          return;
+        }
+        x = entry_of<RM>(p, e);
+      } while (x.n == 0);
+    }
+    piece(0, team);
+  }
+};
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const Params p) {
-  __shared__ float sq[kMaxD], sp[kThreads], sr[kThreads / 32], ss[kThreads];
-  const int h = blockIdx.x % p.H;
-  const int64_t bt = blockIdx.x / p.H, b = bt / p.T, t = bt % p.T;
-  const int64_t end = p.lengths ? p.lengths[b] : p.start_pos + p.T;
-  if (end < 0 || end > p.cap) {
-    if (t == 0 && h == 0 && threadIdx.x == 0) atomicOr(p.err, kErrLengths);
+__device__ __forceinline__ void store_row4(E* o, float4 v) {
+  if constexpr (sizeof(E) == 4) {
+    *reinterpret_cast<float4*>(o) = v;
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                              *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+struct Shared {
+  alignas(128) uint8_t ring[kWarps][kStages][kStageBytes];
+  alignas(16) uint8_t join[kJoinBytes];   // also: entry prefix at the start, score exchange
+  float scales[kWarps][kStages][4];       // K and V scales of a unit's two halves
+  float2 ml[kWarps][16];                  // a warp's {m, l} of each row
+  float vref[kWarps];
+  int64_t sums[kWarps];
+  int64_t total;
+  int first_entry;
+  int64_t into;
+};
+
+template <typename E, int NW>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Params p) {
+  constexpr int D = NW * 128, TEAMS = kWarps / NW;
+  constexpr bool F32 = sizeof(E) == 4;
+  constexpr int RM = F32 ? 8 : 16;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, qd = lane & 3;
+  const int team = warp / NW, part = warp % NW;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // ---- units before each entry, and where this block's run starts
+  int64_t* pre = reinterpret_cast<int64_t*>(sm.join);
+  const int per = (p.entries + kThreads - 1) / kThreads;
+  {
+    int64_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
+      if (e >= p.entries) break;
+      const Entry x = entry_of<RM>(p, e);
+      pre[e] = mine;
+      mine += (int64_t)x.n * p.Hkv;
+      if (x.bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
+    }
+    int64_t up = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += v;
+    }
+    if (lane == 31) sm.sums[warp] = up;
+    __syncthreads();
+    int64_t base = up - mine, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) base += sm.sums[w];
+      total += sm.sums[w];
+    }
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
+      if (e >= p.entries) break;
+      pre[e] += base;
+      if (blockIdx.x == 0) p.prefix[e] = pre[e];
+    }
+    if (tid == 0) {
+      sm.total = total;
+      if (blockIdx.x == 0) p.prefix[p.entries] = total;
+    }
+  }
+  __syncthreads();
+  const int64_t U = sm.total, W = runs<TEAMS>(U, gridDim.x);
+  if (blockIdx.x >= W) return;
+  const int64_t at = run_start(blockIdx.x, U, W), stop = run_start(blockIdx.x + 1, U, W);
+  for (int e = tid; e < p.entries; e += kThreads) {
+    const int64_t a = pre[e], b = e + 1 < p.entries ? pre[e + 1] : U;
+    if (a <= at && at < b) {
+      sm.first_entry = e;
+      sm.into = at - a;
+    }
+  }
+  __syncthreads();
+
+  Cursor<RM, TEAMS> in(p, at, stop, sm.first_entry, sm.into, team);   // copies
+  Cursor<RM, TEAMS> cu = in;                                          // products
+
+  const uint32_t ring = smem_u32(sm.ring[warp]);
+  const uint32_t scales = smem_u32(sm.scales[warp]);
+  // copy c of 8: row 4 c + lane / 8, piece lane % 8
+  const uint32_t dst0 = (lane >> 3) * 128 + (((lane & 7) ^ swizzle(lane >> 3)) << 4);
+  const uint32_t dst1 = (4 + (lane >> 3)) * 128 + (((lane & 7) ^ swizzle(4 + (lane >> 3))) << 4);
+  auto copy_unit = [&](int stage) {
+    while (!in.done() && in.k >= in.kend) in.next_piece(team);
+    if (!in.done()) {
+      const Entry& x = in.x;
+      const int key0 = (x.u0 + in.k) * kUnit;
+      const int64_t head = x.b * p.Hkv + in.h;
+      const int64_t row0 = head * p.cap;
+      const uint32_t dst = ring + stage * kStageBytes;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int key = key0 + 4 * c + (lane >> 3);
+        const bool on = key >= x.lo && key <= x.hi;
+        const int64_t off = (row0 + (on ? key : x.lo)) * D + part * 128 + (lane & 7) * 16;
+        const uint32_t d = dst + (c >> 1) * 1024 + (c & 1 ? dst1 : dst0);
+        copy16(d, p.k8 + off, on);
+        copy16(d + kHalf, p.v8 + off, on);
+      }
+      if (lane < 4) {
+        const int key = key0 + (lane & 1) * 16;
+        const bool on = key + 15 >= x.lo && key <= x.hi;
+        const int64_t off = head * (p.cap >> p.block_shift) + ((on ? key : x.lo) >> p.block_shift);
+        copy4(scales + (stage * 4 + lane) * 4, (lane < 2 ? p.k_scale : p.v_scale) + off, on);
+      }
+      in.k += TEAMS;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) copy_unit(s);
+
+  const uint32_t k_at = g * 128 + ((qd ^ swizzle(g)) << 4);             // first piece; second: ^ 64
+  const uint32_t v_at0 = (2 * qd) * 128 + ((g ^ swizzle(2 * qd)) << 4);
+  const uint32_t v_at1 = (2 * qd + 1) * 128 + ((g ^ swizzle(2 * qd + 1)) << 4);
+  int stage = 0, swap = 0;
+
+  while (!cu.done()) {
+    const Entry x = cu.x;
+    // ---- the piece's query rows, scaled by a power of two each
+    uint32_t qf[8][4];
+    float srow[2];
+    int hi[2], lo[2];
+#pragma unroll
+    for (int i = 0; i < (F32 ? 1 : 2); ++i) {
+      const int r = x.r0 + min(g + 8 * i, x.nr - 1);   // rows past the tile repeat its last one
+      const int t = r / p.group;
+      const E* row = (const E*)p.q + (x.b * p.T + t) * p.q_row +
+                     ((int64_t)cu.h * p.group + r % p.group) * D;
+      float amax = 0.f;
+      if (NW > 1) {
+#pragma unroll 4
+        for (int d = qd * 8; d < D; d += 32) {
+          float f[8];
+          load8(row + d, f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+        }
+      }
+      float f[32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load8(row + part * 128 + (j >> 1) * 64 + qd * 16 + (j & 1) * 8, f + 8 * j);
+      if (NW == 1) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(f[j]));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      int ex = 13 + 127 - (int)(__float_as_uint(amax) >> 23);
+      if (amax == 0.f || !(amax <= 3.402823466e38f)) ex = 0;
+      ex = min(ex, 120);
+      const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+      srow[i] = __uint_as_float((uint32_t)(127 - ex) << 23) * p.scale_log2;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float* w = f + 4 * s;
+        if constexpr (F32) {
+          split2(w[0] * up, w[1] * up, qf[s][0], qf[s][1]);
+          split2(w[2] * up, w[3] * up, qf[s][2], qf[s][3]);
+        } else {
+          qf[s][i] = half2_of(w[0] * up, w[1] * up);
+          qf[s][2 + i] = half2_of(w[2] * up, w[3] * up);
+        }
+      }
+      hi[i] = x.end - (int)p.T + t;
+      lo[i] = p.window > 0 ? hi[i] - p.window + 1 : 0;
+    }
+    if constexpr (F32) { srow[1] = srow[0]; hi[1] = hi[0]; lo[1] = lo[0]; }
+    // keys that every row of the tile sees need no mask
+    const int all_hi = x.end - (int)p.T + x.r0 / p.group;
+    const int all_lo = p.window > 0 ? x.hi - p.window + 1 : 0;
+
+    float o[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0x1p-100f;
+
+    for (; cu.k < cu.kend; cu.k += TEAMS) {
+      asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
+      __syncwarp();
+      copy_unit(stage == 0 ? kStages - 1 : stage - 1);   // what the last turn used
+      const uint32_t kb = ring + stage * kStageBytes, vb = kb + kHalf;
+      const float4 sc = *reinterpret_cast<const float4*>(sm.scales[warp][stage]);
+      // ---- scores
+      float s[4][4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        const uint4 a = lds16(kb + nt * 1024 + k_at), b = lds16(kb + nt * 1024 + (k_at ^ 64));
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t b0, b1;
+          e4m3x4_to_half(w[k], b0, b1);
+          mma(s[nt], qf[k], b0, b1);
+        }
+      }
+      if constexpr (NW > 1) {
+        // the team's partial scores, summed in the same order by each warp
+        float4* ex = reinterpret_cast<float4*>(sm.join) + ((team * 2 + swap) * NW) * 128;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+          ex[part * 128 + nt * 32 + lane] = make_float4(s[nt][0], s[nt][1], s[nt][2], s[nt][3]);
+        asm volatile("bar.sync %0, %1;" :: "r"(1 + team), "n"(NW * 32) : "memory");
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          float4 t = ex[nt * 32 + lane];
+#pragma unroll
+          for (int w = 1; w < NW; ++w) {
+            const float4 v = ex[w * 128 + nt * 32 + lane];
+            t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+          }
+          s[nt][0] = t.x; s[nt][1] = t.y; s[nt][2] = t.z; s[nt][3] = t.w;
+        }
+        swap ^= 1;
+      }
+      if constexpr (F32) {
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) { s[nt][0] += s[nt][2]; s[nt][1] += s[nt][3]; }
+      }
+      constexpr int NR = F32 ? 1 : 2;  // rows of a lane
+      const float ksc[2] = {sc.x, sc.y};
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const float f0 = srow[i] * ksc[0], f1 = srow[i] * ksc[1];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          s[nt][2 * i] *= nt < 2 ? f0 : f1;
+          s[nt][2 * i + 1] *= nt < 2 ? f0 : f1;
+        }
+      }
+      const int key0 = (x.u0 + cu.k) * kUnit;
+      if (key0 < all_lo || key0 + kUnit - 1 > all_hi) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int key = key0 + nt * 8 + 2 * qd + c;
+              if (key < lo[i] || key > hi[i]) s[nt][2 * i + c] = -INFINITY;
+            }
+      }
+      // ---- running maximum, weights, sums
+      const float nv = fmaxf(vref, fmaxf(sc.z, sc.w));
+      const float inv = kWeightScale / nv;
+      const float vf0 = sc.z * inv, vf1 = sc.w * inv;
+      const float shrink = vref / nv;
+      vref = nv;
+      float alpha[2];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        float mx = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
+#pragma unroll
+        for (int nt = 1; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * i], s[nt][2 * i + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        mx = fmaxf(mx, m[i]);
+        const float base = mx == -INFINITY ? 0.f : mx;
+        const float a = exp2_fast(m[i] - base);
+        m[i] = mx;
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float e = exp2_fast(s[nt][2 * i + c] - base);
+            sum += e;
+            s[nt][2 * i + c] = e * (nt < 2 ? vf0 : vf1);
+          }
+        l[i] = l[i] * a + sum;
+        alpha[i] = a * shrink;
+      }
+      if constexpr (F32) alpha[1] = alpha[0];
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          o[i][0] *= alpha[0]; o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1]; o[i][3] *= alpha[1];
+        }
+      }
+      // ---- weighted sum of V
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t a[4];
+        if constexpr (F32) {
+          split2(s[2 * j][0], s[2 * j][1], a[0], a[1]);
+          split2(s[2 * j + 1][0], s[2 * j + 1][1], a[2], a[3]);
+        } else {
+          a[0] = half2_of(s[2 * j][0], s[2 * j][1]);
+          a[1] = half2_of(s[2 * j][2], s[2 * j][3]);
+          a[2] = half2_of(s[2 * j + 1][0], s[2 * j + 1][1]);
+          a[3] = half2_of(s[2 * j + 1][2], s[2 * j + 1][3]);
+        }
+        const uint4 r0 = lds16(vb + j * 2048 + v_at0), r1 = lds16(vb + j * 2048 + v_at1);
+        const uint4 r2 = lds16(vb + j * 2048 + 1024 + v_at0), r3 = lds16(vb + j * 2048 + 1024 + v_at1);
+        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+        const uint32_t w2[4] = {r2.x, r2.y, r2.z, r2.w}, w3[4] = {r3.x, r3.y, r3.z, r3.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t b[8];
+          e4m3x4_to_half(__byte_perm(w0[w], w1[w], 0x5140), b[0], b[1]);
+          e4m3x4_to_half(__byte_perm(w0[w], w1[w], 0x7362), b[2], b[3]);
+          e4m3x4_to_half(__byte_perm(w2[w], w3[w], 0x5140), b[4], b[5]);
+          e4m3x4_to_half(__byte_perm(w2[w], w3[w], 0x7362), b[6], b[7]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma(o[4 * w + i], a, b[i], b[4 + i]);
+        }
+      }
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    }
+
+    // ---- join the block's teams, rows in rounds of eight
+    constexpr int NR = F32 ? 1 : 2;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (qd == 0) sm.ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
+    }
+    const bool whole = cu.k_first == 0 && cu.kend == x.n;
+    float* slot = p.parts + (int64_t)(2 * blockIdx.x + (cu.at == at ? 0 : 1)) * slot_floats<RM, D>();
+    float* join = reinterpret_cast<float*>(sm.join);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      if (8 * i >= x.nr) break;
+      __syncthreads();   // ml is complete; what used the join area before is done
+      const bool on = g + 8 * i < x.nr;
+      if (on) {
+        float mx = -INFINITY;
+        for (int w = 0; w < TEAMS; ++w) mx = fmaxf(mx, sm.ml[w * NW][g + 8 * i].x);
+        const float f = exp2_fast(m[i] - (mx == -INFINITY ? 0.f : mx)) * vref / kWeightScale;
+        float* to = join + (team * 8 + g) * D + part * 128 + qd * 32;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int d = 0; d < 16; d += 4) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[j] = (F32 ? o[d + j][c] + o[d + j][c + 2] : o[d + j][2 * i + c]) * f;
+            *reinterpret_cast<float4*>(to + c * 16 + d) = make_float4(v[0], v[1], v[2], v[3]);
+          }
+      }
+      __syncthreads();
+      const int rows = min(8, x.nr - 8 * i);
+      for (int c = tid; c < rows * (D / 4); c += kThreads) {
+        const int rr = c / (D / 4), d = c % (D / 4) * 4, r = rr + 8 * i;
+        float4 sum = *reinterpret_cast<const float4*>(join + rr * D + d);
+        for (int w = 1; w < TEAMS; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(join + (w * 8 + rr) * D + d);
+          sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+        }
+        float mx = -INFINITY, ls = 0.f;
+        for (int w = 0; w < TEAMS; ++w) mx = fmaxf(mx, sm.ml[w * NW][r].x);
+        for (int w = 0; w < TEAMS; ++w)
+          ls += sm.ml[w * NW][r].y * exp2_fast(sm.ml[w * NW][r].x - (mx == -INFINITY ? 0.f : mx));
+        if (whole) {
+          const float n = ls == 0.f ? 0.f : 1.f / ls;
+          const int q = x.r0 + r;
+          E* to = (E*)p.out + (x.b * p.T + q / p.group) * p.out_row +
+                  ((int64_t)cu.h * p.group + q % p.group) * D + d;
+          store_row4(to, make_float4(sum.x * n, sum.y * n, sum.z * n, sum.w * n));
+        } else {
+          *reinterpret_cast<float4*>(slot + r * D + d) = sum;
+          if (d == 0) *reinterpret_cast<float2*>(slot + RM * D + 2 * r) = make_float2(mx, ls);
+        }
+      }
+    }
+    __syncthreads();   // the join area and ml are free again
+    cu.next_piece(team);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// One block for each row: joins the parts of its head in the order of the
+// blocks that left them, and writes the zeros of rows that see nothing.
+template <typename E, int NW>
+__global__ void __launch_bounds__(128) join_kernel(const Params p, int blocks) {
+  constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = sizeof(E) == 4 ? 8 : 16;
+  constexpr int V = D / 4, GROUPS = 128 / V;
+  __shared__ float4 s_sum[128];
+  __shared__ float s_l[GROUPS > 0 ? GROUPS : 1];
+  const int per = min(RM, p.rows);
+  int64_t id = blockIdx.x;
+  const int r = (int)(id % per);
+  id /= per;
+  const int h = (int)(id % p.Hkv), e = (int)(id / p.Hkv);
+  const Entry x = entry_of<RM>(p, e);
+  if (r >= x.nr || x.bad) return;
+  const int d = threadIdx.x % V * 4, grp = threadIdx.x / V;
+  const int q = x.r0 + r;
+  E* to = (E*)p.out + (x.b * p.T + q / p.group) * p.out_row +
+          ((int64_t)h * p.group + q % p.group) * D + d;
+  if (x.n == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (grp == 0) store_row4(to, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
   }
-  const int64_t pos = end - p.T + t;
-  const int64_t lo = p.window > 0 ? max((int64_t)0, pos - p.window + 1) : 0;
-  const int64_t head = b * p.Hkv + h / (p.H / p.Hkv);
-  const uint8_t* k8 = p.k8 + head * p.cap * p.D;
-  const uint8_t* v8 = p.v8 + head * p.cap * p.D;
-  const float* ks = p.k_scale + head * (p.cap / p.block);
-  const float* vs = p.v_scale + head * (p.cap / p.block);
-  const int tid = threadIdx.x;
-  for (int d = tid; d < p.D; d += kThreads)
-    sq[d] = get((const E*)p.q + bt * p.q_row + (int64_t)h * p.D + d);
-  float o[kMaxD / kThreads] = {};
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j0 = lo; j0 <= pos; j0 += kThreads) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t U = p.prefix[p.entries], W = runs<TEAMS>(U, blocks);
+  const int64_t s0 = p.prefix[e] + (int64_t)h * x.n;
+  const int64_t c0 = run_of(s0, U, W), c1 = run_of(s0 + x.n - 1, U, W);
+  if (c0 == c1) return;
+  auto slot = [&](int64_t c) {
+    const int64_t which = 2 * c + (run_start(c, U, W) >= s0 ? 0 : 1);
+    return p.parts + which * slot_floats<RM, D>();
+  };
+  float mx = -INFINITY;
+  for (int64_t c = c0; c <= c1; ++c) mx = fmaxf(mx, slot(c)[RM * D + 2 * r]);
+  const float base = mx == -INFINITY ? 0.f : mx;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int64_t c = c0 + grp; c <= c1; c += GROUPS) {
+    const float* s = slot(c);
+    const float2 ml = *reinterpret_cast<const float2*>(s + RM * D + 2 * r);
+    const float4 v = *reinterpret_cast<const float4*>(s + r * D + d);
+    const float f = exp2_fast(ml.x - base);
+    sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
+    sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
+    l = fmaf(ml.y, f, l);
+  }
+  if (GROUPS > 1) {
+    s_sum[threadIdx.x] = sum;
+    if (d == 0) s_l[grp] = l;
     __syncthreads();
-    const int64_t j = j0 + tid;
-    float s = -INFINITY;
-    if (j <= pos) {
-      float acc = 0.f;
-      for (int d = 0; d < p.D; d += 4) {
-        float x[4];
-        e4m3x4_to_float(*reinterpret_cast<const uint32_t*>(k8 + j * p.D + d), x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc = fmaf(x[i], sq[d + i], acc);
-      }
-      s = acc * ks[j / p.block] * p.scale_log2;
-    }
-    float tm = s;
-    for (int w = 16; w > 0; w >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, w));
-    if (tid % 32 == 0) sr[tid / 32] = tm;
-    __syncthreads();
-    float nm = m;
-    for (int w = 0; w < kThreads / 32; ++w) nm = fmaxf(nm, sr[w]);
-    const float base = nm == -INFINITY ? 0.f : nm;
-    const float e = exp2f(s - base), alpha = exp2f(m - base);
-    m = nm;
-    l = l * alpha + e;
-    sp[tid] = j <= pos ? e * vs[j / p.block] : 0.f;
-    __syncthreads();
-    const int n = (int)min((int64_t)kThreads, pos + 1 - j0);
-    for (int c = 0; c * kThreads + tid < p.D; ++c) {
-      const int d = c * kThreads + tid;
-      float acc = o[c] * alpha;
-      for (int i = 0; i < n; ++i) {
-        const __half_raw r = __nv_cvt_fp8_to_halfraw(v8[(j0 + i) * p.D + d], __NV_E4M3);
-        acc = fmaf(sp[i], __half2float(__half(r)), acc);
-      }
-      o[c] = acc;
+    if (grp > 0) return;
+    for (int w = 1; w < GROUPS; ++w) {
+      const float4 v = s_sum[w * V + threadIdx.x];
+      sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+      l += s_l[w];
     }
   }
-  ss[tid] = l;
-  __syncthreads();
-  float sum = 0.f;
-  for (int i = 0; i < kThreads; ++i) sum += ss[i];
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int c = 0; c * kThreads + tid < p.D; ++c)
-    put((E*)p.out + bt * p.out_row + (int64_t)h * p.D + c * kThreads + tid, o[c] * inv);
+  const float n = l == 0.f ? 0.f : 1.f / l;
+  store_row4(to, make_float4(sum.x * n, sum.y * n, sum.z * n, sum.w * n));
+}
+
+template <typename E, int NW>
+int launch(Params p, const DecodeQ8Call& c, int64_t B) {
+  constexpr int RM = sizeof(E) == 4 ? 8 : 16;
+  static DeviceOnce once;
+  const int rc = once.run(c.device, [] {
+    return cudaFuncSetAttribute(decode_kernel<E, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(Shared)) == cudaSuccess ? kOk : kErrLaunch;
+  });
+  if (rc != kOk) return rc;
+  const int64_t at_once = std::max<int64_t>(1, kMaxEntries / p.tiles);   // sequences of a launch
+  char* ws = static_cast<char*>(c.ws);
+  p.prefix = reinterpret_cast<int64_t*>(ws);
+  p.parts = reinterpret_cast<float*>(
+      ws + (((size_t)(std::min(B, at_once) * p.tiles + 1) * 8 + 255) & ~(size_t)255));
+  for (int64_t b = 0; b < B; b += at_once) {
+    p.b0 = b;
+    p.entries = (int)(std::min(at_once, B - b) * p.tiles);
+    decode_kernel<E, NW><<<c.num_sms, kThreads, sizeof(Shared), c.stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return kErrLaunch;
+    cudaLaunchConfig_t cfg = {};
+    const int64_t grid = (int64_t)p.entries * p.Hkv * std::min(RM, p.rows);
+    if (grid > 0x7fffffff) return kErrShape;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(128);
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, join_kernel<E, NW>, (const Params)p, c.num_sms) != cudaSuccess) {
+      cudaGetLastError();
+      return kErrLaunch;
+    }
+  }
+  return kOk;
+}
+
+int tiles_of(int64_t T, int H, int Hkv, int dtype) {
+  const int rm = dtype == PFA_F32 ? 8 : 16;
+  return (int)((T * (H / Hkv) + rm - 1) / rm);
 }
 
 }  // namespace
 
-size_t decode_q8_workspace(int64_t, int64_t, int, int, int, int, int) { return 0; }
+size_t decode_q8_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int num_sms) {
+  const int64_t tiles = tiles_of(T, H, Hkv, dtype);
+  const int64_t entries = std::min(B, std::max<int64_t>(1, kMaxEntries / tiles)) * tiles;
+  const int rm = dtype == PFA_F32 ? 8 : 16;
+  const size_t slot = (size_t)(rm * D + rm * 2) * sizeof(float);
+  return (((size_t)(entries + 1) * 8 + 255) & ~(size_t)255) + 2 * (size_t)num_sms * slot;
+}
 
 int launch_decode_q8(const DecodeQ8Call& c) {
   Params p;
@@ -114,18 +701,19 @@ int launch_decode_q8(const DecodeQ8Call& c) {
   p.k8 = (const uint8_t*)c.cache.k8; p.v8 = (const uint8_t*)c.cache.v8;
   p.k_scale = c.cache.k_scale; p.v_scale = c.cache.v_scale;
   p.lengths = c.span.lengths;
-  p.B = c.span.B; p.T = c.span.T; p.start_pos = c.span.start_pos;
-  p.cap = c.cache.max_seq_len; p.q_row = c.q_row; p.out_row = c.out_row;
-  p.H = c.H; p.Hkv = c.Hkv; p.D = c.D; p.window = c.window; p.block = c.cache.block;
+  p.T = c.span.T; p.start_pos = c.span.start_pos;
+  p.q_row = c.q_row; p.out_row = c.out_row;
+  p.cap = (int)c.cache.max_seq_len;
+  p.H = c.H; p.Hkv = c.Hkv; p.group = c.H / c.Hkv; p.window = c.window;
+  p.block_shift = c.cache.block == 16 ? 4 : c.cache.block == 32 ? 5 : c.cache.block == 64 ? 6 : 7;
+  p.rows = (int)(p.T * p.group);
+  p.tiles = tiles_of(p.T, c.H, c.Hkv, c.dtype);
   p.scale_log2 = c.scale * 1.4426950408889634f;
   p.err = c.err;
-  const int64_t grid = p.B * p.T * p.H;
-  if (grid > 0x7fffffff) return kErrShape;
+  const int64_t B = c.span.B;
   if (c.dtype == PFA_F32)
-    decode_kernel<float><<<(unsigned)grid, kThreads, 0, c.stream>>>(p);
-  else
-    decode_kernel<__nv_bfloat16><<<(unsigned)grid, kThreads, 0, c.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? kOk : kErrLaunch;
+    return c.D == 128 ? launch<float, 1>(p, c, B) : launch<float, 4>(p, c, B);
+  return c.D == 128 ? launch<__nv_bfloat16, 1>(p, c, B) : launch<__nv_bfloat16, 4>(p, c, B);
 }
 
 }  // namespace pfa

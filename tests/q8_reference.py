@@ -88,9 +88,15 @@ def attention(q, cache, n, window, scale, dtype):
       - the scores: q is exact (bf16) or off by 2^-21 (fp32, a high and a low half), and
         D / 16 products of 16 are added in fp32, at most 2^-22 of the terms' size each;
         an error d of a score is one of 2 d of every weight;
-      - the sum over keys: 2^-22 for each 16 of them.
+      - the sum over keys: 2^-22 for each 16 of them;
+      - small weights: a half (the low half at fp32) below 2^-14 is a multiple of 2^-24, so off by up to 2^-25
+        whatever its size.  It stands for e_j vs_j / vmax * 2^14 with e_j = 2^(s_j - m), vmax the
+        largest V scale seen: undone, 2^-39 vmax / vs_j of weight, that is 2^-39 vmax |code_j| of
+        the sum, which is divided by sum e_j >= 1 (the largest e_j is 1).  It shows only where all
+        weights of size meet V values of zero.
     """
     T, H, D = q.shape
+    blk = cache[0].shape[-2] // cache[2].shape[-1]
     k, v = values(cache[0], cache[2]), values(cache[1], cache[3])
     out = torch.zeros(T, H, D, dtype=torch.float64, device=q.device)
     tol = torch.zeros_like(out)
@@ -110,10 +116,12 @@ def attention(q, cache, n, window, scale, dtype):
         p = torch.softmax(s, -1)
         o = p @ vv
         a = p @ vv.abs()
+        codes = cache[1][h // (H // k.shape[0]), lo:n].double().abs()
+        vs = cache[3][h // (H // k.shape[0]), lo // blk:(n - 1) // blk + 1].double().max()
         c = (2.0 ** -21 if f32 else 2.0 ** -11) + (n - lo + 16) / 16 * 2.0 ** -22 \
             + 2 * size * ((D / 16 + 2) * 2.0 ** -22 + (2.0 ** -21 if f32 else 0.0))
         out[T - (n - first):, h] = o
-        tol[T - (n - first):, h] = HALF[dtype] * o.abs() + (1 + HALF[dtype]) * c * a
+        tol[T - (n - first):, h] = HALF[dtype] * o.abs() + (1 + HALF[dtype]) * (c * a + 2.0 ** -39 * vs * codes.sum(0))
     return out, tol
 
 
