@@ -22,10 +22,10 @@
 // a lane reads 16 bytes of four V rows and pairs the rows' bytes with prmt.
 //
 // Work split: tiles of 32 keys ("units") of all sequences, heads and row tiles
-// form one list, cut into equal runs, one for each block (one block an SM).
-// Eight warps take the run's units in turn, each with its own ring of three
+// form one list, cut into equal runs, one for each block (two blocks an SM).
+// Four warps take the run's units in turn, each with its own ring of three
 // stages filled by cp.async (no barrier in the loop); their sums join in shared
-// memory where a run leaves a head.  What covers a head alone is stored as
+// memory where a run leaves a head, while the SM's other block streams on.  What covers a head alone is stored as
 // output, what covers part of it goes to the workspace, and a second kernel,
 // launched so that its start overlaps, joins the parts in order.
 //
@@ -43,13 +43,14 @@
 namespace pfa {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kBlocksPerSm = 2;
 constexpr int kUnit = 32;                      // keys of a unit
 constexpr int kStages = 3;
 constexpr int kHalf = kUnit * 128;             // bytes of a warp's K (or V) part of a stage
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kMaxEntries = 4096;              // (sequence, row tile) pairs of one launch
-constexpr int kJoinBytes = 32768;              // joins: 8 row sums of 128 floats for each warp
+constexpr int kMaxEntries = 2048;              // (sequence, row tile) pairs of one launch
+constexpr int kJoinBytes = kWarps * 8 * 128 * 4;  // joins: 8 row sums of 128 floats for each warp
 constexpr float kWeightScale = 16384.f;
 
 struct Params {
@@ -94,16 +95,23 @@ __device__ __forceinline__ Entry entry_of(const Params& p, int e) {
   return x;
 }
 
+// a / b; 64-bit division takes hundreds of cycles, and numbers above 2^32 are rare.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
+  return (int64_t)((uint32_t)a / (uint32_t)b);
+}
 // The run of block c of w: [c * U / w, (c + 1) * U / w).
-__device__ __forceinline__ int64_t run_start(int64_t c, int64_t U, int64_t w) { return c * U / w; }
+__device__ __forceinline__ int64_t run_start(int64_t c, int64_t U, int64_t w) {
+  return quotient(c * U, w);
+}
 // The block whose run holds unit x.
 __device__ __forceinline__ int64_t run_of(int64_t x, int64_t U, int64_t w) {
-  return ((x + 1) * w - 1) / U;
+  return quotient((x + 1) * w - 1, U);
 }
 // Blocks that get a run: enough units for each of a block's teams.
 template <int TEAMS>
 __device__ __forceinline__ int64_t runs(int64_t U, int64_t blocks) {
-  return min(blocks, (U + TEAMS - 1) / TEAMS);
+  return min(blocks, (U + TEAMS - 1) / TEAMS);  // TEAMS: a power of two
 }
 
 // Floats of a partial-sum slot: rows of output, then {m, l} of each row.
@@ -166,8 +174,8 @@ struct Cursor {
   __device__ Cursor(const Params& p, int64_t at, int64_t stop, int e, int64_t into, int team)
       : p(p), at(at), stop(stop), e(e) {
     x = entry_of<RM>(p, e);
-    h = x.n > 0 ? (int)(into / x.n) : 0;
-    piece(x.n > 0 ? (int)(into % x.n) : 0, team);
+    h = x.n > 0 ? (int)quotient(into, x.n) : 0;
+    piece(x.n > 0 ? (int)(into - (int64_t)h * x.n) : 0, team);
   }
   __device__ void piece(int first, int team) {
     k_first = first;
@@ -216,8 +224,11 @@ struct Shared {
   int64_t into;
 };
 
+static_assert(kBlocksPerSm * (sizeof(Shared) + 1024) <= 228 * 1024, "shared memory of an SM");
+static_assert(kMaxEntries * 8 <= kJoinBytes, "the prefix sums use the join area");
+
 template <typename E, int NW>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Params p) {
   constexpr int D = NW * 128, TEAMS = kWarps / NW;
   constexpr bool F32 = sizeof(E) == 4;
   constexpr int RM = F32 ? 8 : 16;
@@ -286,35 +297,60 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Params p) {
   // copy c of 8: row 4 c + lane / 8, piece lane % 8
   const uint32_t dst0 = (lane >> 3) * 128 + (((lane & 7) ^ swizzle(lane >> 3)) << 4);
   const uint32_t dst1 = (4 + (lane >> 3)) * 128 + (((lane & 7) ^ swizzle(4 + (lane >> 3))) << 4);
-  auto copy_unit = [&](int stage) {
-    while (!in.done() && in.k >= in.kend) in.next_piece(team);
-    if (!in.done()) {
-      const Entry& x = in.x;
-      const int key0 = (x.u0 + in.k) * kUnit;
-      const int64_t head = x.b * p.Hkv + in.h;
-      const int64_t row0 = head * p.cap;
-      const uint32_t dst = ring + stage * kStageBytes;
+  // Copies come in halves of a unit, K then V, each a group of its own: K's place is
+  // free for the unit after next but one when its scores are done, V's when its sum is.
+  struct Source {
+    const uint8_t* v;      // the V row of key0 (or of the first key seen), this lane's piece
+    int key0, lo, hi;      // on: hi >= lo
+    bool inner;            // all keys of the unit are seen by some row
+  } src = {};
+  auto copy_rows = [&](uint32_t dst, const uint8_t* from) {
+    if (src.inner) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        copy16(dst + (c >> 1) * 1024 + (c & 1 ? dst1 : dst0), from + c * 4 * D, true);
+    } else {
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const int key = key0 + 4 * c + (lane >> 3);
-        const bool on = key >= x.lo && key <= x.hi;
-        const int64_t off = (row0 + (on ? key : x.lo)) * D + part * 128 + (lane & 7) * 16;
-        const uint32_t d = dst + (c >> 1) * 1024 + (c & 1 ? dst1 : dst0);
-        copy16(d, p.k8 + off, on);
-        copy16(d + kHalf, p.v8 + off, on);
+        const int key = src.key0 + 4 * c + (lane >> 3);
+        const bool on = key >= src.lo && key <= src.hi;
+        copy16(dst + (c >> 1) * 1024 + (c & 1 ? dst1 : dst0), on ? from + c * 4 * D : p.k8, on);
       }
+    }
+  };
+  auto copy_k = [&](int stage) {
+    while (!in.done() && in.k >= in.kend) in.next_piece(team);
+    src.lo = 0;
+    src.hi = -1;
+    if (!in.done()) {
+      const Entry& x = in.x;
+      src.key0 = (x.u0 + in.k) * kUnit;
+      src.lo = x.lo;
+      src.hi = x.hi;
+      src.inner = src.key0 >= x.lo && src.key0 + kUnit - 1 <= x.hi;
+      const int64_t head = x.b * p.Hkv + in.h;
+      const int64_t off = (head * p.cap + src.key0 + (lane >> 3)) * D + part * 128 + (lane & 7) * 16;
+      src.v = p.v8 + off;
+      copy_rows(ring + stage * kStageBytes, p.k8 + off);
       if (lane < 4) {
-        const int key = key0 + (lane & 1) * 16;
+        const int key = src.key0 + (lane & 1) * 16;
         const bool on = key + 15 >= x.lo && key <= x.hi;
-        const int64_t off = head * (p.cap >> p.block_shift) + ((on ? key : x.lo) >> p.block_shift);
-        copy4(scales + (stage * 4 + lane) * 4, (lane < 2 ? p.k_scale : p.v_scale) + off, on);
+        const int64_t at = head * (p.cap >> p.block_shift) + ((on ? key : x.lo) >> p.block_shift);
+        copy4(scales + (stage * 4 + lane) * 4, (lane < 2 ? p.k_scale : p.v_scale) + at, on);
       }
       in.k += TEAMS;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  auto copy_v = [&](int stage) {
+    if (src.hi >= src.lo) copy_rows(ring + stage * kStageBytes + kHalf, src.v);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) copy_unit(s);
+  for (int s = 0; s < kStages; ++s) {
+    copy_k(s);
+    copy_v(s);
+  }
 
   const uint32_t k_at = g * 128 + ((qd ^ swizzle(g)) << 4);             // first piece; second: ^ 64
   const uint32_t v_at0 = (2 * qd) * 128 + ((g ^ swizzle(2 * qd)) << 4);
@@ -382,9 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Params p) {
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0x1p-100f;
 
     for (; cu.k < cu.kend; cu.k += TEAMS) {
-      asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
+      asm volatile("cp.async.wait_group %0;" :: "n"(2 * kStages - 1) : "memory");
       __syncwarp();
-      copy_unit(stage == 0 ? kStages - 1 : stage - 1);   // what the last turn used
       const uint32_t kb = ring + stage * kStageBytes, vb = kb + kHalf;
       const float4 sc = *reinterpret_cast<const float4*>(sm.scales[warp][stage]);
       // ---- scores
@@ -401,6 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Params p) {
           mma(s[nt], qf[k], b0, b1);
         }
       }
+      __syncwarp();
+      copy_k(stage);
       if constexpr (NW > 1) {
         // the team's partial scores, summed in the same order by each warp
         float4* ex = reinterpret_cast<float4*>(sm.join) + ((team * 2 + swap) * NW) * 128;
@@ -486,6 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Params p) {
         }
       }
       // ---- weighted sum of V
+      asm volatile("cp.async.wait_group %0;" :: "n"(2 * kStages - 1) : "memory");
+      __syncwarp();
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t a[4];
@@ -513,6 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Params p) {
           for (int i = 0; i < 4; ++i) mma(o[4 * w + i], a, b[i], b[4 + i]);
         }
       }
+      __syncwarp();
+      copy_v(stage);
       stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 
@@ -581,65 +622,84 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Params p) {
 
 // One block for each row: joins the parts of its head in the order of the
 // blocks that left them, and writes the zeros of rows that see nothing.
+constexpr int kJoinThreads = 128;
+
 template <typename E, int NW>
-__global__ void __launch_bounds__(128) join_kernel(const Params p, int blocks) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int blocks) {
   constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = sizeof(E) == 4 ? 8 : 16;
-  constexpr int V = D / 4, GROUPS = 128 / V;
-  __shared__ float4 s_sum[128];
-  __shared__ float s_l[GROUPS > 0 ? GROUPS : 1];
+  constexpr int V = D / 4, GROUPS = kJoinThreads / V;
+  __shared__ float4 s_sum[kJoinThreads];
+  __shared__ float s_f[kJoinThreads], s_w[kJoinThreads / 32];
   const int per = min(RM, p.rows);
-  int64_t id = blockIdx.x;
-  const int r = (int)(id % per);
-  id /= per;
-  const int h = (int)(id % p.Hkv), e = (int)(id / p.Hkv);
+  const int id = blockIdx.x, r = id % per, h = id / per % p.Hkv, e = id / per / p.Hkv;
   const Entry x = entry_of<RM>(p, e);
   if (r >= x.nr || x.bad) return;
-  const int d = threadIdx.x % V * 4, grp = threadIdx.x / V;
+  const int tid = threadIdx.x, d = tid % V * 4, grp = tid / V;
   const int q = x.r0 + r;
   E* to = (E*)p.out + (x.b * p.T + q / p.group) * p.out_row +
           ((int64_t)h * p.group + q % p.group) * D + d;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (x.n == 0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (grp == 0) store_row4(to, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t U = p.prefix[p.entries], W = runs<TEAMS>(U, blocks);
   const int64_t s0 = p.prefix[e] + (int64_t)h * x.n;
-  const int64_t c0 = run_of(s0, U, W), c1 = run_of(s0 + x.n - 1, U, W);
-  if (c0 == c1) return;
-  auto slot = [&](int64_t c) {
-    const int64_t which = 2 * c + (run_start(c, U, W) >= s0 ? 0 : 1);
-    return p.parts + which * slot_floats<RM, D>();
+  const int c0 = (int)run_of(s0, U, W), n = (int)run_of(s0 + x.n - 1, U, W) - c0 + 1;
+  if (n == 1) return;
+  // the first block's part is its run's last piece unless its run starts here
+  const int first = run_start(c0, U, W) == s0 ? 0 : 1;
+  auto slot = [&](int i) {
+    return p.parts + (int64_t)(2 * (c0 + i) + (i == 0 ? first : 0)) * slot_floats<RM, D>();
+  };
+  auto block_max = [&](float v) {
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (tid % 32 == 0) s_w[tid / 32] = v;
+    __syncthreads();
+    v = s_w[0];
+    for (int w = 1; w < kJoinThreads / 32; ++w) v = fmaxf(v, s_w[w]);
+    return v;
   };
   float mx = -INFINITY;
-  for (int64_t c = c0; c <= c1; ++c) mx = fmaxf(mx, slot(c)[RM * D + 2 * r]);
+  for (int i = tid; i < n; i += kJoinThreads) mx = fmaxf(mx, slot(i)[RM * D + 2 * r]);
+  mx = block_max(mx);
   const float base = mx == -INFINITY ? 0.f : mx;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-#pragma unroll 4
-  for (int64_t c = c0 + grp; c <= c1; c += GROUPS) {
-    const float* s = slot(c);
-    const float2 ml = *reinterpret_cast<const float2*>(s + RM * D + 2 * r);
-    const float4 v = *reinterpret_cast<const float4*>(s + r * D + d);
-    const float f = exp2_fast(ml.x - base);
-    sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
-    sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
-    l = fmaf(ml.y, f, l);
+  for (int i0 = 0; i0 < n; i0 += kJoinThreads) {
+    const int here = min(kJoinThreads, n - i0);
+    float lp = 0.f;
+    if (tid < here) {
+      const float2 ml = *reinterpret_cast<const float2*>(slot(i0 + tid) + RM * D + 2 * r);
+      const float f = exp2_fast(ml.x - base);
+      s_f[tid] = f;
+      lp = ml.y * f;
+    }
+    for (int o = 16; o > 0; o >>= 1) lp += __shfl_xor_sync(0xffffffffu, lp, o);
+    __syncthreads();   // s_w is read
+    if (tid % 32 == 0) s_w[tid / 32] = lp;
+    __syncthreads();
+    for (int w = 0; w < kJoinThreads / 32; ++w) l += s_w[w];
+#pragma unroll 8
+    for (int i = grp; i < here; i += GROUPS) {
+      const float4 v = *reinterpret_cast<const float4*>(slot(i0 + i) + r * D + d);
+      const float f = s_f[i];
+      sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
+      sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
+    }
+    __syncthreads();   // s_f is read
   }
   if (GROUPS > 1) {
-    s_sum[threadIdx.x] = sum;
-    if (d == 0) s_l[grp] = l;
+    s_sum[tid] = sum;
     __syncthreads();
     if (grp > 0) return;
     for (int w = 1; w < GROUPS; ++w) {
-      const float4 v = s_sum[w * V + threadIdx.x];
+      const float4 v = s_sum[w * V + tid];
       sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
-      l += s_l[w];
     }
   }
-  const float n = l == 0.f ? 0.f : 1.f / l;
-  store_row4(to, make_float4(sum.x * n, sum.y * n, sum.z * n, sum.w * n));
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  store_row4(to, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
 }
 
 template <typename E, int NW>
@@ -659,20 +719,21 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
   for (int64_t b = 0; b < B; b += at_once) {
     p.b0 = b;
     p.entries = (int)(std::min(at_once, B - b) * p.tiles);
-    decode_kernel<E, NW><<<c.num_sms, kThreads, sizeof(Shared), c.stream>>>(p);
+    decode_kernel<E, NW><<<c.num_sms * kBlocksPerSm, kThreads, sizeof(Shared), c.stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return kErrLaunch;
     cudaLaunchConfig_t cfg = {};
     const int64_t grid = (int64_t)p.entries * p.Hkv * std::min(RM, p.rows);
     if (grid > 0x7fffffff) return kErrShape;
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = c.stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<E, NW>, (const Params)p, c.num_sms) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, join_kernel<E, NW>, (const Params)p, c.num_sms * kBlocksPerSm) !=
+        cudaSuccess) {
       cudaGetLastError();
       return kErrLaunch;
     }
@@ -692,7 +753,7 @@ size_t decode_q8_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtyp
   const int64_t entries = std::min(B, std::max<int64_t>(1, kMaxEntries / tiles)) * tiles;
   const int rm = dtype == PFA_F32 ? 8 : 16;
   const size_t slot = (size_t)(rm * D + rm * 2) * sizeof(float);
-  return (((size_t)(entries + 1) * 8 + 255) & ~(size_t)255) + 2 * (size_t)num_sms * slot;
+  return (((size_t)(entries + 1) * 8 + 255) & ~(size_t)255) + 2 * (size_t)num_sms * kBlocksPerSm * slot;
 }
 
 int launch_decode_q8(const DecodeQ8Call& c) {
