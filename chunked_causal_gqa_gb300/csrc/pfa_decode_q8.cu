@@ -51,6 +51,8 @@ constexpr int kHalf = kUnit * 128;             // bytes of a warp's K (or V) par
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kMaxEntries = 2048;              // (sequence, row tile) pairs of one launch
 constexpr int kJoinBytes = kWarps * 8 * 128 * 4;  // joins: 8 row sums of 128 floats for each warp
+// What the start and end of a head cost a block, in units: its query rows, the join.
+constexpr int kHeadCost = 4;
 constexpr float kWeightScale = 16384.f;
 
 struct Params {
@@ -65,7 +67,6 @@ struct Params {
   int rows, tiles, entries;   // T * group, row tiles of a sequence, entries of this launch
   float scale_log2;
   unsigned* err;
-  int64_t* prefix;            // workspace: units before each entry
   float* parts;               // workspace: slots of partial sums
 };
 
@@ -76,6 +77,8 @@ struct Entry {
   int lo, hi;         // keys [lo, hi] are seen by some row
   int u0, n;          // units u0 .. u0 + n - 1 hold them
   bool bad;
+  // Units of a head in the list of all: its own and its start's cost.
+  __device__ int listed() const { return n > 0 ? n + kHeadCost : 0; }
 };
 
 template <int RM>
@@ -162,42 +165,50 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Walks the units of a run that belong to one team.
+// Walks the units of a run that belong to one team, piece by piece: the part of
+// a head that lies in the run.  A head's list starts with kHeadCost units of no work.
 template <int RM, int TEAMS>
 struct Cursor {
-  const Params& p;
-  int64_t at, stop;    // units of the run from the current piece on: [at, stop)
+  int64_t at, stop;    // the run from the current piece on: [at, stop)
   int e, h;            // entry and kv head of the piece
   Entry x;
-  int k, kend;         // the team's unit inside the head, end of the piece
-  int k_first;         // first unit of the piece
-  __device__ Cursor(const Params& p, int64_t at, int64_t stop, int e, int64_t into, int team)
-      : p(p), at(at), stop(stop), e(e) {
+  int listed;          // listed units of the piece
+  int k0, kend;        // the head's units k0 .. kend - 1 are in the piece
+  int k;               // the team's current one
+  __device__ __forceinline__ void start(const Params& p, int64_t at_, int64_t stop_, int e_,
+                                        int64_t into, int team) {
+    at = at_;
+    stop = stop_;
+    e = e_;
     x = entry_of<RM>(p, e);
-    h = x.n > 0 ? (int)quotient(into, x.n) : 0;
-    piece(x.n > 0 ? (int)(into - (int64_t)h * x.n) : 0, team);
+    h = (int)quotient(into, max(x.listed(), 1));
+    piece((int)(into - (int64_t)h * x.listed()), team);
+    if (kend <= k0) next_piece(p, team);
   }
-  __device__ void piece(int first, int team) {
-    k_first = first;
+  __device__ __forceinline__ void piece(int first, int team) {
     const int64_t left = stop - at;
-    kend = left < x.n - first ? first + (int)left : x.n;
-    k = first + team;
+    listed = left < x.listed() - first ? (int)left : x.listed() - first;
+    k0 = max(first - kHeadCost, 0);
+    kend = first + listed - kHeadCost;
+    k = k0 + team;
   }
-  __device__ bool done() const { return at >= stop; }
-  __device__ void next_piece(int team) {
-    at += kend - k_first;
-    if (at >= stop) return;
-    if (++h == p.Hkv) {
-      h = 0;
-      do {
-        if (++e >= p.entries) {  // only if the lengths changed under the kernel
-          at = stop;
-          return;
-        }
-        x = entry_of<RM>(p, e);
-      } while (x.n == 0);
-    }
-    piece(0, team);
+  __device__ __forceinline__ bool done() const { return at >= stop; }
+  __device__ __forceinline__ void next_piece(const Params& p, int team) {
+    do {
+      at += listed;
+      if (at >= stop) return;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {
+          if (++e >= p.entries) {  // only if the lengths changed under the kernel
+            at = stop;
+            return;
+          }
+          x = entry_of<RM>(p, e);
+        } while (x.n == 0);
+      }
+      piece(0, team);
+    } while (kend <= k0);
   }
 };
 
@@ -239,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   const int team = warp / NW, part = warp % NW;
 
   asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before has written its results
 
   // ---- units before each entry, and where this block's run starts
   int64_t* pre = reinterpret_cast<int64_t*>(sm.join);
@@ -250,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
       if (e >= p.entries) break;
       const Entry x = entry_of<RM>(p, e);
       pre[e] = mine;
-      mine += (int64_t)x.n * p.Hkv;
+      mine += (int64_t)x.listed() * p.Hkv;
       if (x.bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
     }
     int64_t up = mine;
@@ -269,12 +281,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
       const int e = tid * per + i;
       if (e >= p.entries) break;
       pre[e] += base;
-      if (blockIdx.x == 0) p.prefix[e] = pre[e];
     }
-    if (tid == 0) {
-      sm.total = total;
-      if (blockIdx.x == 0) p.prefix[p.entries] = total;
-    }
+    if (tid == 0) sm.total = total;
   }
   __syncthreads();
   const int64_t U = sm.total, W = runs<TEAMS>(U, gridDim.x);
@@ -289,8 +297,28 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   }
   __syncthreads();
 
-  Cursor<RM, TEAMS> in(p, at, stop, sm.first_entry, sm.into, team);   // copies
-  Cursor<RM, TEAMS> cu = in;                                          // products
+  Cursor<RM, TEAMS> in, cu;   // copies, products
+  in.start(p, at, stop, sm.first_entry, sm.into, team);
+  cu = in;
+
+  // Query rows of a piece as they are stored, this warp's columns: the lane's 32
+  // elements of rows g and g + 8 (fp32: of row g).  Rows past the tile repeat its last.
+  constexpr int NR = F32 ? 1 : 2;  // rows of a lane
+  uint4 raw[8];
+  auto load_q = [&]() {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int r = cu.x.r0 + min(g + 8 * i, cu.x.nr - 1);
+      const int t = r / p.group;
+      const E* row = (const E*)p.q + (cu.x.b * p.T + t) * p.q_row +
+                     ((int64_t)cu.h * p.group + r - t * p.group) * D + part * 128 + qd * 16;
+#pragma unroll
+      for (int j = 0; j < 8 / NR; ++j)
+        raw[i * (8 / NR) + j] = *reinterpret_cast<const uint4*>(
+            row + (j >= 4 / NR ? 64 : 0) + (j % (4 / NR)) * (16 / (int)sizeof(E)));
+    }
+  };
+  if (!cu.done()) load_q();
 
   const uint32_t ring = smem_u32(sm.ring[warp]);
   const uint32_t scales = smem_u32(sm.scales[warp]);
@@ -319,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
     }
   };
   auto copy_k = [&](int stage) {
-    while (!in.done() && in.k >= in.kend) in.next_piece(team);
+    while (!in.done() && in.k >= in.kend) in.next_piece(p, team);
     src.lo = 0;
     src.hi = -1;
     if (!in.done()) {
@@ -346,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
     if (src.hi >= src.lo) copy_rows(ring + stage * kStageBytes + kHalf, src.v);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < kStages; ++s) {
     copy_k(s);
     copy_v(s);
@@ -363,48 +391,53 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
     uint32_t qf[8][4];
     float srow[2];
     int hi[2], lo[2];
-#pragma unroll
-    for (int i = 0; i < (F32 ? 1 : 2); ++i) {
-      const int r = x.r0 + min(g + 8 * i, x.nr - 1);   // rows past the tile repeat its last one
-      const int t = r / p.group;
-      const E* row = (const E*)p.q + (x.b * p.T + t) * p.q_row +
-                     ((int64_t)cu.h * p.group + r % p.group) * D;
-      float amax = 0.f;
-      if (NW > 1) {
-#pragma unroll 4
-        for (int d = qd * 8; d < D; d += 32) {
-          float f[8];
-          load8(row + d, f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
-        }
+    auto raw_at = [&](int i, int j) -> float {   // element j of the lane's 32 of row i
+      if constexpr (F32) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+        return __uint_as_float(w[j]);
+      } else {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(raw)[i * 16 + j / 2];
+        return __uint_as_float(j % 2 ? w & 0xffff0000u : w << 16);
       }
-      float f[32];
+    };
+    float amax[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) load8(row + part * 128 + (j >> 1) * 64 + qd * 16 + (j & 1) * 8, f + 8 * j);
-      if (NW == 1) {
+    for (int i = 0; i < NR; ++i) {
+      float a = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(f[j]));
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      int ex = 13 + 127 - (int)(__float_as_uint(amax) >> 23);
-      if (amax == 0.f || !(amax <= 3.402823466e38f)) ex = 0;
+      for (int j = 0; j < 32; ++j) a = fmaxf(a, fabsf(raw_at(i, j)));
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      amax[i] = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      if (NW > 1 && qd == 0) sm.ml[warp][g + 8 * i].x = amax[i];
+    }
+    if constexpr (NW > 1) {   // over the team's columns
+      asm volatile("bar.sync %0, %1;" :: "r"(1 + team), "n"(NW * 32) : "memory");
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int w = 0; w < NW; ++w) amax[i] = fmaxf(amax[i], sm.ml[team * NW + w][g + 8 * i].x);
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      int ex = 13 + 127 - (int)(__float_as_uint(amax[i]) >> 23);
+      if (amax[i] == 0.f || !(amax[i] <= 3.402823466e38f)) ex = 0;
       ex = min(ex, 120);
       const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
       srow[i] = __uint_as_float((uint32_t)(127 - ex) << 23) * p.scale_log2;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        const float* w = f + 4 * s;
+        const float w0 = raw_at(i, 4 * s) * up, w1 = raw_at(i, 4 * s + 1) * up;
+        const float w2 = raw_at(i, 4 * s + 2) * up, w3 = raw_at(i, 4 * s + 3) * up;
         if constexpr (F32) {
-          split2(w[0] * up, w[1] * up, qf[s][0], qf[s][1]);
-          split2(w[2] * up, w[3] * up, qf[s][2], qf[s][3]);
+          split2(w0, w1, qf[s][0], qf[s][1]);
+          split2(w2, w3, qf[s][2], qf[s][3]);
         } else {
-          qf[s][i] = half2_of(w[0] * up, w[1] * up);
-          qf[s][2 + i] = half2_of(w[2] * up, w[3] * up);
+          qf[s][i] = half2_of(w0, w1);
+          qf[s][2 + i] = half2_of(w2, w3);
         }
       }
-      hi[i] = x.end - (int)p.T + t;
+      const int r = x.r0 + min(g + 8 * i, x.nr - 1);
+      hi[i] = x.end - (int)p.T + r / p.group;
       lo[i] = p.window > 0 ? hi[i] - p.window + 1 : 0;
     }
     if constexpr (F32) { srow[1] = srow[0]; hi[1] = hi[0]; lo[1] = lo[0]; }
@@ -461,7 +494,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) { s[nt][0] += s[nt][2]; s[nt][1] += s[nt][3]; }
       }
-      constexpr int NR = F32 ? 1 : 2;  // rows of a lane
       const float ksc[2] = {sc.x, sc.y};
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
@@ -558,15 +590,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
     }
 
     // ---- join the block's teams, rows in rounds of eight
-    constexpr int NR = F32 ? 1 : 2;
+    const bool whole = cu.k0 == 0 && cu.kend == x.n;
+    float* slot = p.parts + (int64_t)(2 * blockIdx.x + (cu.at == at ? 0 : 1)) * slot_floats<RM, D>();
+    const int h = cu.h;
+    cu.next_piece(p, team);
+    if (!cu.done()) load_q();   // arrives while the join runs
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if (qd == 0) sm.ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
     }
-    const bool whole = cu.k_first == 0 && cu.kend == x.n;
-    float* slot = p.parts + (int64_t)(2 * blockIdx.x + (cu.at == at ? 0 : 1)) * slot_floats<RM, D>();
     float* join = reinterpret_cast<float*>(sm.join);
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
@@ -606,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
           const float n = ls == 0.f ? 0.f : 1.f / ls;
           const int q = x.r0 + r;
           E* to = (E*)p.out + (x.b * p.T + q / p.group) * p.out_row +
-                  ((int64_t)cu.h * p.group + q % p.group) * D + d;
+                  ((int64_t)h * p.group + q % p.group) * D + d;
           store_row4(to, make_float4(sum.x * n, sum.y * n, sum.z * n, sum.w * n));
         } else {
           *reinterpret_cast<float4*>(slot + r * D + d) = sum;
@@ -615,88 +649,118 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
       }
     }
     __syncthreads();   // the join area and ml are free again
-    cu.next_piece(team);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// One block for each row: joins the parts of its head in the order of the
-// blocks that left them, and writes the zeros of rows that see nothing.
+// One block for each row and 128 columns: joins the parts of its head, and
+// writes the zeros of rows that see nothing.  Four groups of threads take every
+// fourth part in the blocks' order, each with a running maximum.
 constexpr int kJoinThreads = 128;
 
 template <typename E, int NW>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int blocks) {
   constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = sizeof(E) == 4 ? 8 : 16;
-  constexpr int V = D / 4, GROUPS = kJoinThreads / V;
-  __shared__ float4 s_sum[kJoinThreads];
-  __shared__ float s_f[kJoinThreads], s_w[kJoinThreads / 32];
+  __shared__ float4 s_sum[3][32];
+  __shared__ float2 s_ml[4];
+  __shared__ int64_t s_units[4][2];
+  const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
   const int per = min(RM, p.rows);
-  const int id = blockIdx.x, r = id % per, h = id / per % p.Hkv, e = id / per / p.Hkv;
+  int id = blockIdx.x;
+  const int d = id % NW * 128 + lane * 4;
+  id /= NW;
+  const int r = id % per, h = id / per % p.Hkv, e = id / per / p.Hkv;
+  asm volatile("griddepcontrol.launch_dependents;");
+  // the list of units, as the first kernel counts it
+  int64_t before = 0, total = 0;
+  for (int i = tid; i < p.entries; i += kJoinThreads) {
+    const int64_t n = (int64_t)entry_of<RM>(p, i).listed() * p.Hkv;
+    total += n;
+    if (i < e) before += n;
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (lane == 0) {
+    s_units[grp][0] = before;
+    s_units[grp][1] = total;
+  }
+  __syncthreads();
+  before = s_units[0][0] + s_units[1][0] + s_units[2][0] + s_units[3][0];
+  total = s_units[0][1] + s_units[1][1] + s_units[2][1] + s_units[3][1];
   const Entry x = entry_of<RM>(p, e);
-  if (r >= x.nr || x.bad) return;
-  const int tid = threadIdx.x, d = tid % V * 4, grp = tid / V;
+  const int64_t W = runs<TEAMS>(total, blocks);
+  const int64_t s0 = before + (int64_t)h * x.listed();
+  int c0 = 0, n = 0, first = 0;
+  if (x.n > 0) {
+    c0 = (int)run_of(s0 + kHeadCost, total, W);
+    n = (int)run_of(s0 + x.listed() - 1, total, W) - c0 + 1;
+    // the first block's part is its run's last piece unless its run starts in this head
+    first = run_start(c0, total, W) >= s0 ? 0 : 1;
+  }
+  // Every block waits, also one with nothing to do: this grid must not end before the first.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (r >= x.nr || x.bad || n == 1) return;   // n 1: stored whole
   const int q = x.r0 + r;
   E* to = (E*)p.out + (x.b * p.T + q / p.group) * p.out_row +
           ((int64_t)h * p.group + q % p.group) * D + d;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (x.n == 0) {
+  if (n == 0) {
     if (grp == 0) store_row4(to, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
   }
-  const int64_t U = p.prefix[p.entries], W = runs<TEAMS>(U, blocks);
-  const int64_t s0 = p.prefix[e] + (int64_t)h * x.n;
-  const int c0 = (int)run_of(s0, U, W), n = (int)run_of(s0 + x.n - 1, U, W) - c0 + 1;
-  if (n == 1) return;
-  // the first block's part is its run's last piece unless its run starts here
-  const int first = run_start(c0, U, W) == s0 ? 0 : 1;
-  auto slot = [&](int i) {
-    return p.parts + (int64_t)(2 * (c0 + i) + (i == 0 ? first : 0)) * slot_floats<RM, D>();
-  };
-  auto block_max = [&](float v) {
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (tid % 32 == 0) s_w[tid / 32] = v;
-    __syncthreads();
-    v = s_w[0];
-    for (int w = 1; w < kJoinThreads / 32; ++w) v = fmaxf(v, s_w[w]);
-    return v;
-  };
-  float mx = -INFINITY;
-  for (int i = tid; i < n; i += kJoinThreads) mx = fmaxf(mx, slot(i)[RM * D + 2 * r]);
-  mx = block_max(mx);
-  const float base = mx == -INFINITY ? 0.f : mx;
+  float mx = -INFINITY, l = 0.f;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int i0 = 0; i0 < n; i0 += kJoinThreads) {
-    const int here = min(kJoinThreads, n - i0);
-    float lp = 0.f;
-    if (tid < here) {
-      const float2 ml = *reinterpret_cast<const float2*>(slot(i0 + tid) + RM * D + 2 * r);
-      const float f = exp2_fast(ml.x - base);
-      s_f[tid] = f;
-      lp = ml.y * f;
+#pragma unroll 1
+  for (int i0 = grp; i0 < n; i0 += 32) {
+    float4 v[8];
+    float2 ml[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + 4 * j;
+      ml[j] = make_float2(-INFINITY, 0.f);
+      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const float* slot =
+            p.parts + (int64_t)(2 * (c0 + i) + (i == 0 ? first : 0)) * slot_floats<RM, D>();
+        ml[j] = *reinterpret_cast<const float2*>(slot + RM * D + 2 * r);
+        v[j] = *reinterpret_cast<const float4*>(slot + r * D + d);
+      }
     }
-    for (int o = 16; o > 0; o >>= 1) lp += __shfl_xor_sync(0xffffffffu, lp, o);
-    __syncthreads();   // s_w is read
-    if (tid % 32 == 0) s_w[tid / 32] = lp;
-    __syncthreads();
-    for (int w = 0; w < kJoinThreads / 32; ++w) l += s_w[w];
-#pragma unroll 8
-    for (int i = grp; i < here; i += GROUPS) {
-      const float4 v = *reinterpret_cast<const float4*>(slot(i0 + i) + r * D + d);
-      const float f = s_f[i];
-      sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
-      sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
+    float m = mx;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, ml[j].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    const float a = exp2_fast(mx - base);
+    mx = m;
+    l *= a;
+    sum.x *= a; sum.y *= a; sum.z *= a; sum.w *= a;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = exp2_fast(ml[j].x - base);
+      l = fmaf(ml[j].y, f, l);
+      sum.x = fmaf(v[j].x, f, sum.x); sum.y = fmaf(v[j].y, f, sum.y);
+      sum.z = fmaf(v[j].z, f, sum.z); sum.w = fmaf(v[j].w, f, sum.w);
     }
-    __syncthreads();   // s_f is read
   }
-  if (GROUPS > 1) {
-    s_sum[tid] = sum;
-    __syncthreads();
-    if (grp > 0) return;
-    for (int w = 1; w < GROUPS; ++w) {
-      const float4 v = s_sum[w * V + tid];
-      sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
-    }
+  if (grp > 0) s_sum[grp - 1][lane] = sum;
+  if (lane == 0) s_ml[grp] = make_float2(mx, l);
+  __syncthreads();
+  if (grp > 0) return;
+  float m = mx;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) m = fmaxf(m, s_ml[w].x);
+  const float base = m == -INFINITY ? 0.f : m;
+  const float a = exp2_fast(mx - base);
+  l *= a;
+  sum.x *= a; sum.y *= a; sum.z *= a; sum.w *= a;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) {
+    const float f = exp2_fast(s_ml[w].x - base);
+    const float4 v = s_sum[w - 1][lane];
+    l = fmaf(s_ml[w].y, f, l);
+    sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
+    sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   store_row4(to, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
@@ -712,28 +776,33 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
   });
   if (rc != kOk) return rc;
   const int64_t at_once = std::max<int64_t>(1, kMaxEntries / p.tiles);   // sequences of a launch
-  char* ws = static_cast<char*>(c.ws);
-  p.prefix = reinterpret_cast<int64_t*>(ws);
-  p.parts = reinterpret_cast<float*>(
-      ws + (((size_t)(std::min(B, at_once) * p.tiles + 1) * 8 + 255) & ~(size_t)255));
+  p.parts = static_cast<float*>(c.ws);
+  // Both kernels may be launched before what is in front of them has ended: they
+  // wait (griddepcontrol) before they read what it writes.
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = c.stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const int blocks = c.num_sms * kBlocksPerSm;
   for (int64_t b = 0; b < B; b += at_once) {
     p.b0 = b;
     p.entries = (int)(std::min(at_once, B - b) * p.tiles);
-    decode_kernel<E, NW><<<c.num_sms * kBlocksPerSm, kThreads, sizeof(Shared), c.stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return kErrLaunch;
-    cudaLaunchConfig_t cfg = {};
-    const int64_t grid = (int64_t)p.entries * p.Hkv * std::min(RM, p.rows);
-    if (grid > 0x7fffffff) return kErrShape;
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = c.stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<E, NW>, (const Params)p, c.num_sms * kBlocksPerSm) !=
-        cudaSuccess) {
+    const int64_t joins = (int64_t)p.entries * p.Hkv * std::min(RM, p.rows) * NW;
+    if (joins > 0x7fffffff) return kErrShape;
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
+    cudaError_t err = cudaLaunchKernelEx(&cfg, decode_kernel<E, NW>, (const Params)p);
+    if (err == cudaSuccess) {
+      cfg.gridDim = dim3((unsigned)joins);
+      cfg.blockDim = dim3(kJoinThreads);
+      cfg.dynamicSmemBytes = 0;
+      err = cudaLaunchKernelEx(&cfg, join_kernel<E, NW>, (const Params)p, blocks);
+    }
+    if (err != cudaSuccess) {
       cudaGetLastError();
       return kErrLaunch;
     }
@@ -748,12 +817,9 @@ int tiles_of(int64_t T, int H, int Hkv, int dtype) {
 
 }  // namespace
 
-size_t decode_q8_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int num_sms) {
-  const int64_t tiles = tiles_of(T, H, Hkv, dtype);
-  const int64_t entries = std::min(B, std::max<int64_t>(1, kMaxEntries / tiles)) * tiles;
-  const int rm = dtype == PFA_F32 ? 8 : 16;
-  const size_t slot = (size_t)(rm * D + rm * 2) * sizeof(float);
-  return (((size_t)(entries + 1) * 8 + 255) & ~(size_t)255) + 2 * (size_t)num_sms * kBlocksPerSm * slot;
+size_t decode_q8_workspace(int64_t, int64_t, int, int, int D, int dtype, int num_sms) {
+  const int rm = dtype == PFA_F32 ? 8 : 16;   // two slots for each block's run
+  return 2 * (size_t)num_sms * kBlocksPerSm * (rm * D + rm * 2) * sizeof(float);
 }
 
 int launch_decode_q8(const DecodeQ8Call& c) {
