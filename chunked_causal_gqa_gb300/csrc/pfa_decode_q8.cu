@@ -49,11 +49,28 @@ constexpr int kUnit = 32;                      // keys of a unit
 constexpr int kStages = 3;
 constexpr int kHalf = kUnit * 128;             // bytes of a warp's K (or V) part of a stage
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kMaxEntries = 2048;              // (sequence, row tile) pairs of one launch
+constexpr int kMaxEntries = 1 << 14;           // (sequence, row tile) pairs of one launch
+constexpr int64_t kMaxUnits = 1 << 30;         // units that a launch can list
 constexpr int kJoinBytes = kWarps * 8 * 128 * 4;  // joins: 8 row sums of 128 floats for each warp
 // What the start and end of a head cost a block, in units: its query rows, the join.
 constexpr int kHeadCost = 4;
 constexpr float kWeightScale = 16384.f;
+
+// Division of 0 <= n < 2^31 by a number that the host knows: a 64-bit product and a
+// shift, where / takes some thirty instructions (the kernels' code is mostly run
+// once a launch, and fetching it is a good part of their start).
+struct Divisor {
+  uint32_t by, m;
+  int shift;
+};
+Divisor divisor(uint32_t by) {
+  int s = 0;
+  while ((1u << s) < by) ++s;
+  return Divisor{by, (uint32_t)(((uint64_t)1 << (31 + s)) / by + 1), 31 + s};
+}
+__device__ __forceinline__ int operator/(int n, const Divisor& d) {
+  return (int)(((uint64_t)(uint32_t)n * d.m) >> d.shift);
+}
 
 struct Params {
   const void* q;
@@ -62,9 +79,12 @@ struct Params {
   const float *k_scale, *v_scale;
   const int64_t* lengths;
   int64_t T, start_pos, q_row, out_row;
-  int64_t b0;                 // first sequence of this launch
-  int cap, H, Hkv, group, window, block_shift;
-  int rows, tiles, entries;   // T * group, row tiles of a sequence, entries of this launch
+  int64_t b0;                 // first sequence and row tile of this launch
+  int tile0;
+  int cap, Hkv, window, block_shift;
+  int rows, entries;          // T * group; entries of this launch
+  Divisor group, tiles;       // H / Hkv; row tiles of a sequence in this launch
+  Divisor heads, joined;      // Hkv and min(RM, rows), for the second kernel's grid
   float scale_log2;
   unsigned* err;
   float* parts;               // workspace: slots of partial sums
@@ -84,8 +104,9 @@ struct Entry {
 template <int RM>
 __device__ __forceinline__ Entry entry_of(const Params& p, int e) {
   Entry x;
-  x.b = p.b0 + e / p.tiles;
-  x.r0 = e % p.tiles * RM;
+  const int s = e / p.tiles;
+  x.b = p.b0 + s;
+  x.r0 = (p.tile0 + e - s * (int)p.tiles.by) * RM;
   x.nr = min(RM, p.rows - x.r0);
   const int64_t end = p.lengths ? p.lengths[x.b] : p.start_pos + p.T;
   x.bad = end < 0 || end > p.cap;
@@ -98,23 +119,11 @@ __device__ __forceinline__ Entry entry_of(const Params& p, int e) {
   return x;
 }
 
-// a / b; 64-bit division takes hundreds of cycles, and numbers above 2^32 are rare.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
-  return (int64_t)((uint32_t)a / (uint32_t)b);
-}
-// The run of block c of w: [c * U / w, (c + 1) * U / w).
-__device__ __forceinline__ int64_t run_start(int64_t c, int64_t U, int64_t w) {
-  return quotient(c * U, w);
-}
-// The block whose run holds unit x.
-__device__ __forceinline__ int64_t run_of(int64_t x, int64_t U, int64_t w) {
-  return quotient((x + 1) * w - 1, U);
-}
-// Blocks that get a run: enough units for each of a block's teams.
+// Units of a run: those of all heads over the blocks, at least one for each of
+// a block's teams.  Block c has the list's units [c * run, (c + 1) * run).
 template <int TEAMS>
-__device__ __forceinline__ int64_t runs(int64_t U, int64_t blocks) {
-  return min(blocks, (U + TEAMS - 1) / TEAMS);  // TEAMS: a power of two
+__device__ __forceinline__ int run_of(int total, int blocks) {
+  return max((int)((uint32_t)(total + blocks - 1) / (uint32_t)blocks), TEAMS);
 }
 
 // Floats of a partial-sum slot: rows of output, then {m, l} of each row.
@@ -169,36 +178,37 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // a head that lies in the run.  A head's list starts with kHeadCost units of no work.
 template <int RM, int TEAMS>
 struct Cursor {
-  int64_t at, stop;    // the run from the current piece on: [at, stop)
+  int at, stop;        // the run from the current piece on: [at, stop)
   int e, h;            // entry and kv head of the piece
   Entry x;
   int listed;          // listed units of the piece
   int k0, kend;        // the head's units k0 .. kend - 1 are in the piece
   int k;               // the team's current one
-  __device__ __forceinline__ void start(const Params& p, int64_t at_, int64_t stop_, int e_,
-                                        int64_t into, int team) {
+  __device__ __forceinline__ void start(const Params& p, int at_, int stop_, int e_, int into,
+                                        int team) {
     at = at_;
     stop = stop_;
     e = e_;
     x = entry_of<RM>(p, e);
-    h = (int)quotient(into, max(x.listed(), 1));
-    piece((int)(into - (int64_t)h * x.listed()), team);
+    h = (int)((uint32_t)into / (uint32_t)max(x.listed(), 1));
+    piece(into - h * x.listed(), team);
     if (kend <= k0) next_piece(p, team);
   }
   __device__ __forceinline__ void piece(int first, int team) {
-    const int64_t left = stop - at;
-    listed = left < x.listed() - first ? (int)left : x.listed() - first;
+    listed = min(stop - at, x.listed() - first);
     k0 = max(first - kHeadCost, 0);
     kend = first + listed - kHeadCost;
     k = k0 + team;
   }
   __device__ __forceinline__ bool done() const { return at >= stop; }
   __device__ __forceinline__ void next_piece(const Params& p, int team) {
+#pragma unroll 1
     do {
       at += listed;
       if (at >= stop) return;
       if (++h == p.Hkv) {
         h = 0;
+#pragma unroll 1
         do {
           if (++e >= p.entries) {  // only if the lengths changed under the kernel
             at = stop;
@@ -225,18 +235,15 @@ __device__ __forceinline__ void store_row4(E* o, float4 v) {
 
 struct Shared {
   alignas(128) uint8_t ring[kWarps][kStages][kStageBytes];
-  alignas(16) uint8_t join[kJoinBytes];   // also: entry prefix at the start, score exchange
+  alignas(16) uint8_t join[kJoinBytes];   // also: score exchange
   float scales[kWarps][kStages][4];       // K and V scales of a unit's two halves
   float2 ml[kWarps][16];                  // a warp's {m, l} of each row
   float vref[kWarps];
-  int64_t sums[kWarps];
-  int64_t total;
-  int first_entry;
-  int64_t into;
+  int sums[kWarps];
+  int first_entry, into;
 };
 
 static_assert(kBlocksPerSm * (sizeof(Shared) + 1024) <= 228 * 1024, "shared memory of an SM");
-static_assert(kMaxEntries * 8 <= kJoinBytes, "the prefix sums use the join area");
 
 template <typename E, int NW>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Params p) {
@@ -252,48 +259,42 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before has written its results
 
-  // ---- units before each entry, and where this block's run starts
-  int64_t* pre = reinterpret_cast<int64_t*>(sm.join);
+  // ---- the list of units, and where this block's run starts in it: thread i has
+  // the entries [i * per, (i + 1) * per)
   const int per = (p.entries + kThreads - 1) / kThreads;
-  {
-    int64_t mine = 0;
-    for (int i = 0; i < per; ++i) {
-      const int e = tid * per + i;
-      if (e >= p.entries) break;
-      const Entry x = entry_of<RM>(p, e);
-      pre[e] = mine;
-      mine += (int64_t)x.listed() * p.Hkv;
-      if (x.bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
-    }
-    int64_t up = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
-      if (lane >= o) up += v;
-    }
-    if (lane == 31) sm.sums[warp] = up;
-    __syncthreads();
-    int64_t base = up - mine, total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) base += sm.sums[w];
-      total += sm.sums[w];
-    }
-    for (int i = 0; i < per; ++i) {
-      const int e = tid * per + i;
-      if (e >= p.entries) break;
-      pre[e] += base;
-    }
-    if (tid == 0) sm.total = total;
+  int mine = 0;
+#pragma unroll 1
+  for (int e = tid * per; e < min(p.entries, (tid + 1) * per); ++e) {
+    const Entry x = entry_of<RM>(p, e);
+    mine += x.listed() * p.Hkv;
+    if (x.bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
   }
+  int up = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += v;
+  }
+  if (lane == 31) sm.sums[warp] = up;
   __syncthreads();
-  const int64_t U = sm.total, W = runs<TEAMS>(U, gridDim.x);
-  if (blockIdx.x >= W) return;
-  const int64_t at = run_start(blockIdx.x, U, W), stop = run_start(blockIdx.x + 1, U, W);
-  for (int e = tid; e < p.entries; e += kThreads) {
-    const int64_t a = pre[e], b = e + 1 < p.entries ? pre[e + 1] : U;
-    if (a <= at && at < b) {
-      sm.first_entry = e;
-      sm.into = at - a;
+  int before = up - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sm.sums[w];
+    total += sm.sums[w];
+  }
+  const int run = run_of<TEAMS>(total, gridDim.x);
+  const int at = blockIdx.x * run, stop = min(total, at + run);
+  if (at >= total) return;
+  if (before <= at && at < before + mine) {   // one thread
+    int e = tid * per, into = at - before;
+#pragma unroll 1
+    for (;; ++e) {
+      const int n = entry_of<RM>(p, e).listed() * p.Hkv;
+      if (into < n || e + 1 >= min(p.entries, (tid + 1) * per)) break;
+      into -= n;
     }
+    sm.first_entry = e;
+    sm.into = into;
   }
   __syncthreads();
 
@@ -309,9 +310,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       const int r = cu.x.r0 + min(g + 8 * i, cu.x.nr - 1);
-      const int t = r / p.group;
+      const int t = r / p.group;   // its token
       const E* row = (const E*)p.q + (cu.x.b * p.T + t) * p.q_row +
-                     ((int64_t)cu.h * p.group + r - t * p.group) * D + part * 128 + qd * 16;
+                     (int64_t)(cu.h * (int)p.group.by + r - t * (int)p.group.by) * D + part * 128 + qd * 16;
 #pragma unroll
       for (int j = 0; j < 8 / NR; ++j)
         raw[i * (8 / NR) + j] = *reinterpret_cast<const uint4*>(
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
     for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0x1p-100f;
 
+#pragma unroll 1
     for (; cu.k < cu.kend; cu.k += TEAMS) {
       asm volatile("cp.async.wait_group %0;" :: "n"(2 * kStages - 1) : "memory");
       __syncwarp();
@@ -625,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
       }
       __syncthreads();
       const int rows = min(8, x.nr - 8 * i);
+#pragma unroll 1
       for (int c = tid; c < rows * (D / 4); c += kThreads) {
         const int rr = c / (D / 4), d = c % (D / 4) * 4, r = rr + 8 * i;
         float4 sum = *reinterpret_cast<const float4*>(join + rr * D + d);
@@ -638,9 +641,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
           ls += sm.ml[w * NW][r].y * exp2_fast(sm.ml[w * NW][r].x - (mx == -INFINITY ? 0.f : mx));
         if (whole) {
           const float n = ls == 0.f ? 0.f : 1.f / ls;
-          const int q = x.r0 + r;
-          E* to = (E*)p.out + (x.b * p.T + q / p.group) * p.out_row +
-                  ((int64_t)h * p.group + q % p.group) * D + d;
+          const int q = x.r0 + r, t = q / p.group;
+          E* to = (E*)p.out + (x.b * p.T + t) * p.out_row +
+                  (int64_t)(h * (int)p.group.by + q - t * (int)p.group.by) * D + d;
           store_row4(to, make_float4(sum.x * n, sum.y * n, sum.z * n, sum.w * n));
         } else {
           *reinterpret_cast<float4*>(slot + r * D + d) = sum;
@@ -663,18 +666,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
   constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = sizeof(E) == 4 ? 8 : 16;
   __shared__ float4 s_sum[3][32];
   __shared__ float2 s_ml[4];
-  __shared__ int64_t s_units[4][2];
+  __shared__ int s_units[4][2];
   const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
-  const int per = min(RM, p.rows);
-  int id = blockIdx.x;
-  const int d = id % NW * 128 + lane * 4;
-  id /= NW;
-  const int r = id % per, h = id / per % p.Hkv, e = id / per / p.Hkv;
+  const int id = blockIdx.x / NW, d = blockIdx.x % NW * 128 + lane * 4;
+  const int eh = id / p.joined, r = id - eh * (int)p.joined.by;
+  const int e = eh / p.heads, h = eh - e * p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;");
   // the list of units, as the first kernel counts it
-  int64_t before = 0, total = 0;
+  int before = 0, total = 0;
+#pragma unroll 1
   for (int i = tid; i < p.entries; i += kJoinThreads) {
-    const int64_t n = (int64_t)entry_of<RM>(p, i).listed() * p.Hkv;
+    const int n = entry_of<RM>(p, i).listed() * p.Hkv;
     total += n;
     if (i < e) before += n;
   }
@@ -690,21 +692,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
   before = s_units[0][0] + s_units[1][0] + s_units[2][0] + s_units[3][0];
   total = s_units[0][1] + s_units[1][1] + s_units[2][1] + s_units[3][1];
   const Entry x = entry_of<RM>(p, e);
-  const int64_t W = runs<TEAMS>(total, blocks);
-  const int64_t s0 = before + (int64_t)h * x.listed();
+  const int run = run_of<TEAMS>(total, blocks);
+  const int s0 = before + h * x.listed();
   int c0 = 0, n = 0, first = 0;
   if (x.n > 0) {
-    c0 = (int)run_of(s0 + kHeadCost, total, W);
-    n = (int)run_of(s0 + x.listed() - 1, total, W) - c0 + 1;
+    c0 = (int)((uint32_t)(s0 + kHeadCost) / (uint32_t)run);
+    n = (int)((uint32_t)(s0 + x.listed() - 1) / (uint32_t)run) - c0 + 1;
     // the first block's part is its run's last piece unless its run starts in this head
-    first = run_start(c0, total, W) >= s0 ? 0 : 1;
+    first = c0 * run >= s0 ? 0 : 1;
   }
   // Every block waits, also one with nothing to do: this grid must not end before the first.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (r >= x.nr || x.bad || n == 1) return;   // n 1: stored whole
-  const int q = x.r0 + r;
-  E* to = (E*)p.out + (x.b * p.T + q / p.group) * p.out_row +
-          ((int64_t)h * p.group + q % p.group) * D + d;
+  const int q = x.r0 + r, t = q / p.group;
+  E* to = (E*)p.out + (x.b * p.T + t) * p.out_row +
+          (int64_t)(h * (int)p.group.by + q - t * (int)p.group.by) * D + d;
   if (n == 0) {
     if (grp == 0) store_row4(to, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
@@ -775,8 +777,16 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
                                 (int)sizeof(Shared)) == cudaSuccess ? kOk : kErrLaunch;
   });
   if (rc != kOk) return rc;
-  const int64_t at_once = std::max<int64_t>(1, kMaxEntries / p.tiles);   // sequences of a launch
+  // A launch takes as many (sequence, row tile) entries as its list can count.
+  const int64_t of_entry = (int64_t)p.Hkv * (p.cap / kUnit + 2 + kHeadCost);
+  if (of_entry > kMaxUnits) return kErrShape;
+  const int tiles = (p.rows + RM - 1) / RM;
+  const int most = (int)std::min<int64_t>(kMaxEntries, kMaxUnits / of_entry);
+  const int tiles_at_once = std::min(tiles, most);
+  const int64_t at_once = tiles_at_once < tiles ? 1 : most / tiles;   // sequences
   p.parts = static_cast<float*>(c.ws);
+  p.heads = divisor(p.Hkv);
+  p.joined = divisor(std::min(RM, p.rows));
   // Both kernels may be launched before what is in front of them has ended: they
   // wait (griddepcontrol) before they read what it writes.
   cudaLaunchAttribute attr;
@@ -787,32 +797,31 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   const int blocks = c.num_sms * kBlocksPerSm;
-  for (int64_t b = 0; b < B; b += at_once) {
-    p.b0 = b;
-    p.entries = (int)(std::min(at_once, B - b) * p.tiles);
-    const int64_t joins = (int64_t)p.entries * p.Hkv * std::min(RM, p.rows) * NW;
-    if (joins > 0x7fffffff) return kErrShape;
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(Shared);
-    cudaError_t err = cudaLaunchKernelEx(&cfg, decode_kernel<E, NW>, (const Params)p);
-    if (err == cudaSuccess) {
-      cfg.gridDim = dim3((unsigned)joins);
-      cfg.blockDim = dim3(kJoinThreads);
-      cfg.dynamicSmemBytes = 0;
-      err = cudaLaunchKernelEx(&cfg, join_kernel<E, NW>, (const Params)p, blocks);
+  for (int64_t b = 0; b < B; b += at_once)
+    for (int tile = 0; tile < tiles; tile += tiles_at_once) {
+      const int here = std::min(tiles_at_once, tiles - tile);
+      p.b0 = b;
+      p.tile0 = tile;
+      p.tiles = divisor(here);
+      p.entries = (int)std::min(at_once, B - b) * here;
+      const int64_t joins = (int64_t)p.entries * p.Hkv * std::min(RM, p.rows) * NW;
+      if (joins > 0x7fffffff) return kErrShape;
+      cfg.gridDim = dim3((unsigned)blocks);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = sizeof(Shared);
+      cudaError_t err = cudaLaunchKernelEx(&cfg, decode_kernel<E, NW>, (const Params)p);
+      if (err == cudaSuccess) {
+        cfg.gridDim = dim3((unsigned)joins);
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.dynamicSmemBytes = 0;
+        err = cudaLaunchKernelEx(&cfg, join_kernel<E, NW>, (const Params)p, blocks);
+      }
+      if (err != cudaSuccess) {
+        cudaGetLastError();
+        return kErrLaunch;
+      }
     }
-    if (err != cudaSuccess) {
-      cudaGetLastError();
-      return kErrLaunch;
-    }
-  }
   return kOk;
-}
-
-int tiles_of(int64_t T, int H, int Hkv, int dtype) {
-  const int rm = dtype == PFA_F32 ? 8 : 16;
-  return (int)((T * (H / Hkv) + rm - 1) / rm);
 }
 
 }  // namespace
@@ -831,10 +840,9 @@ int launch_decode_q8(const DecodeQ8Call& c) {
   p.T = c.span.T; p.start_pos = c.span.start_pos;
   p.q_row = c.q_row; p.out_row = c.out_row;
   p.cap = (int)c.cache.max_seq_len;
-  p.H = c.H; p.Hkv = c.Hkv; p.group = c.H / c.Hkv; p.window = c.window;
+  p.Hkv = c.Hkv; p.group = divisor(c.H / c.Hkv); p.window = c.window;
   p.block_shift = c.cache.block == 16 ? 4 : c.cache.block == 32 ? 5 : c.cache.block == 64 ? 6 : 7;
-  p.rows = (int)(p.T * p.group);
-  p.tiles = tiles_of(p.T, c.H, c.Hkv, c.dtype);
+  p.rows = (int)p.T * (c.H / c.Hkv);
   p.scale_log2 = c.scale * 1.4426950408889634f;
   p.err = c.err;
   const int64_t B = c.span.B;
