@@ -1,4 +1,5 @@
-"""Build libpfa.so (the C-ABI library) for sm_103a with nvcc, in-tree.
+"""Build libpfa.so (the C-ABI library) for sm_103a with nvcc, and _pfa_torch.so
+(the operators of the 8-bit cache on torch tensors, over that library) with g++, in-tree.
 
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 chunked_causal_gqa_gb300/_build/libpfa.so with the CUDA runtime linked
@@ -18,6 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpfa.so")
+EXT = os.path.join(BUILD, "_pfa_torch.so")
+EXT_SOURCE = os.path.join(CSRC, "pfa_torch.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -49,9 +52,36 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _build_extension() -> None:
+    """Compile _pfa_torch.so against this Python's torch, unless it is up to date."""
+    import sysconfig
+
+    import torch
+    deps = [EXT_SOURCE, os.path.join(INCLUDE, "pfa.h"), __file__, torch.__file__]
+    if os.path.exists(EXT) and all(os.path.getmtime(d) <= os.path.getmtime(EXT) for d in deps):
+        return
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    dirs = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api",
+                                                        "include"),
+            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", EXT_SOURCE, "-o", tmp]
+    for d in dirs:
+        cmd += ["-isystem", d]
+    cmd += ["-L", BUILD, "-L", os.path.join(base, "lib"), "-lpfa", "-ltorch_python", "-ltorch_cpu",
+            "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libpfa.so; returns its path."""
+    """Compile and link libpfa.so, then _pfa_torch.so; returns libpfa.so's path."""
     if not force and not extra_flags and up_to_date():
+        _build_extension()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -70,12 +100,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(compile_one, _sources()))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs + \
+    cmd = [cc] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-Xlinker",
+                         "-soname=libpfa.so", "-o", tmp] + objs + \
         ["-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_extension()
     return LIB
 
 
