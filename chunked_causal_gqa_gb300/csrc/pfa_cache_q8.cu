@@ -12,10 +12,12 @@
 
 #include "../../include/pfa.h"
 
+#include <algorithm>
+
 namespace pfa {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kMaxThreads = 512;
 
 struct WriteParams {
   const void *k, *v;
@@ -23,71 +25,119 @@ struct WriteParams {
   float *k_scale, *v_scale;
   const int64_t* lengths;
   int64_t T, start_pos, cap, k_row, v_row;
-  int Hkv, D, block, touched;  // touched: blocks that T rows can reach
+  Divisor touched, heads;  // blocks that T rows can reach; Hkv
+  Divisor per_row;         // vectors of 8 elements in a row
+  int D, block;
   unsigned* err;
 };
 
+// Eight elements as they are stored.
 template <typename E>
-__global__ void __launch_bounds__(kThreads) write_kernel(const WriteParams p) {
-  __shared__ float s_max[kThreads / 32];
-  int64_t id = blockIdx.x;
-  const bool isv = id % 2;
-  id /= 2;
-  const int i = (int)(id % p.touched);
-  id /= p.touched;
-  const int h = (int)(id % p.Hkv);
-  const int64_t b = id / p.Hkv;
+struct Raw8 {
+  uint4 w[sizeof(E) / 2];
+  __device__ __forceinline__ void load(const E* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(E) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    if (sizeof(E) == 4) return __uint_as_float(u[i]);
+    return __uint_as_float(i % 2 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+  }
+  __device__ __forceinline__ float amax() const {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_abs(get(i)));
+    return a;
+  }
+  __device__ __forceinline__ uint2 codes(float f) const {
+    return make_uint2(float_to_e4m3x4(get(0) * f, get(1) * f, get(2) * f, get(3) * f),
+                      float_to_e4m3x4(get(4) * f, get(5) * f, get(6) * f, get(7) * f));
+  }
+};
+
+// One block of threads for a block of rows of K or V of one head.  HELD vectors
+// a thread stay in registers between the maximum and the codes, so that the new
+// rows are read once (a block's elements beyond HELD * threads, which only
+// 128 rows of wide heads have, are read again, from L2).
+template <typename E, int HELD>
+__global__ void __launch_bounds__(kMaxThreads) write_kernel(const WriteParams p) {
+  __shared__ float s_max[kMaxThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int id = blockIdx.x / 2;
+  const bool isv = blockIdx.x % 2;
+  const int bh = id / p.touched, i = id - bh * (int)p.touched.by;
+  const int64_t b = bh / p.heads;
+  const int h = bh - (int)b * (int)p.heads.by;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t end = p.lengths ? p.lengths[b] : p.start_pos + p.T;
   if (end < 0 || end > p.cap) {
     if (h == 0 && i == 0 && !isv && threadIdx.x == 0) atomicOr(p.err, kErrLengths);
     return;
   }
-  const int64_t first = end - p.T, low = first > 0 ? first : 0;
-  const int64_t c = low / p.block + i;
-  const int64_t lo = max(low, c * p.block), hi = min(end, (c + 1) * p.block);
+  const int first = (int)(end - p.T), low = max(first, 0);
+  const int c = low / p.block + i, c0 = c * p.block;
+  const int lo = max(low, c0), hi = min((int)end, c0 + p.block);
   if (lo >= hi) return;
-  const int64_t head = b * p.Hkv + h;
-  const E* src = isv ? (const E*)p.v + b * p.T * p.v_row : (const E*)p.k + b * p.T * p.k_row;
   const int64_t row = isv ? p.v_row : p.k_row;
-  src += (int64_t)h * p.D;
-  uint8_t* dst = (isv ? p.v8 : p.k8) + head * p.cap * p.D;
-  float* scale = (isv ? p.v_scale : p.k_scale) + head * (p.cap / p.block) + c;
-  const int per_row = p.D / 8, n = (int)(hi - lo) * per_row;
-  float amax = 0.f;
-  for (int e = threadIdx.x; e < n; e += kThreads) {
-    float x[8];
-    load8(src + (lo - first + e / per_row) * row + e % per_row * 8, x);
+  const E* src = (isv ? (const E*)p.v : (const E*)p.k) + (b * p.T + lo - first) * row + (int64_t)h * p.D;
+  uint8_t* dst = (isv ? p.v8 : p.k8) + ((int64_t)bh * p.cap + c0) * p.D;   // the block's rows
+  float* scale = (isv ? p.v_scale : p.k_scale) + (int64_t)bh * (p.cap / p.block) + c;
+  const int n = (hi - lo) * (int)p.per_row.by, old = (lo - c0) * (int)p.per_row.by;
+  const int threads = blockDim.x, tid = threadIdx.x;
+  auto at = [&](int e) {
+    const int r = e / p.per_row;
+    return src + r * row + (e - r * (int)p.per_row.by) * 8;
+  };
+  Raw8<E> x[HELD];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(x[j]));
+  for (int j = 0; j < HELD; ++j) {
+    x[j] = {};
+    if (tid + j * threads < n) x[j].load(at(tid + j * threads));
+  }
+  const float s_old = old > 0 ? *scale : 0.f;
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < HELD; ++j) amax = fmaxf(amax, x[j].amax());
+#pragma unroll 1
+  for (int e = tid + HELD * threads; e < n; e += threads) {
+    Raw8<E> y;
+    y.load(at(e));
+    amax = fmaxf(amax, y.amax());
   }
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = amax;
-  const int old_rows = (int)(lo - c * p.block);
-  const float s_old = old_rows > 0 ? *scale : 0.f;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+  if (threads > 32) {
+    if (tid % 32 == 0) s_max[tid / 32] = amax;
+    __syncthreads();
+    for (int w = 0; w < threads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+  }
   const float s_new = fmaxf(s_old, pow2_scale(amax));
   const float inv = s_new > 0.f ? 1.f / s_new : 0.f;
-  if (threadIdx.x == 0) *scale = s_new;
   if (s_new != s_old) {
+    if (tid == 0) *scale = s_new;   // every thread has read it: s_old went into s_new
     const float f = s_old * inv;
-    for (int e = threadIdx.x; e < old_rows * per_row; e += kThreads) {
-      uint2* at = reinterpret_cast<uint2*>(dst + c * p.block * p.D + (int64_t)e * 8);
-      const uint2 w = *at;
-      float x[8];
-      e4m3x4_to_float(w.x, x);
-      e4m3x4_to_float(w.y, x + 4);
-      *at = make_uint2(float_to_e4m3x4(x[0] * f, x[1] * f, x[2] * f, x[3] * f),
-                       float_to_e4m3x4(x[4] * f, x[5] * f, x[6] * f, x[7] * f));
+#pragma unroll 1
+    for (int e = tid; e < old; e += threads) {
+      uint2* const w = reinterpret_cast<uint2*>(dst + (int64_t)e * 8);
+      const uint2 was = *w;
+      float y[8];
+      e4m3x4_to_float(was.x, y);
+      e4m3x4_to_float(was.y, y + 4);
+      *w = make_uint2(float_to_e4m3x4(y[0] * f, y[1] * f, y[2] * f, y[3] * f),
+                      float_to_e4m3x4(y[4] * f, y[5] * f, y[6] * f, y[7] * f));
     }
+  } else if (old == 0 && tid == 0) {
+    *scale = s_new;                 // a new block of zeros
   }
-  for (int e = threadIdx.x; e < n; e += kThreads) {
-    float x[8];
-    load8(src + (lo - first + e / per_row) * row + e % per_row * 8, x);
-    *reinterpret_cast<uint2*>(dst + lo * p.D + (int64_t)e * 8) =
-        make_uint2(float_to_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                   float_to_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+  uint2* const to = reinterpret_cast<uint2*>(dst) + old;
+#pragma unroll
+  for (int j = 0; j < HELD; ++j)
+    if (tid + j * threads < n) to[tid + j * threads] = x[j].codes(inv);
+#pragma unroll 1
+  for (int e = tid + HELD * threads; e < n; e += threads) {
+    Raw8<E> y;
+    y.load(at(e));
+    to[e] = y.codes(inv);
   }
 }
 
@@ -95,34 +145,78 @@ struct ReadParams {
   const uint8_t *k8, *v8;
   const float *k_scale, *v_scale;
   void *k_out, *v_out;
-  int64_t heads, start, rows, cap, out_head;
-  int D, block;
+  int64_t start, cap, out_head;
+  Divisor chunks;   // blocks of threads for a head's rows
+  Divisor per_row;  // pieces of 16 output bytes in a row
+  int pieces;       // of a head
+  int D, block_shift;
 };
 
+// A thread makes kPieces pieces of 16 output bytes, all their codes asked for first.
+constexpr int kReadThreads = 256, kPieces = 8;
+
 template <typename E>
-__global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
-  const int per_row = p.D / 16;
-  const int64_t n = p.heads * p.rows * per_row;
-  for (int64_t e = blockIdx.x * (int64_t)kThreads + threadIdx.x; e < 2 * n;
-       e += (int64_t)gridDim.x * kThreads) {
-    const bool isv = e >= n;
-    const int64_t at = isv ? e - n : e;
-    const int64_t r = at / per_row, head = r / p.rows, row = p.start + r % p.rows;
-    const int64_t d = at % per_row * 16;
-    const uint4 w = *reinterpret_cast<const uint4*>((isv ? p.v8 : p.k8) +
-                                                    (head * p.cap + row) * p.D + d);
-    const float s = (isv ? p.v_scale : p.k_scale)[head * (p.cap / p.block) + row / p.block];
-    float x[16];
-    e4m3x4_to_float(w.x, x);
-    e4m3x4_to_float(w.y, x + 4);
-    e4m3x4_to_float(w.z, x + 8);
-    e4m3x4_to_float(w.w, x + 12);
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadParams p) {
+  constexpr int N = 16 / sizeof(E);   // codes of a piece
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int id = blockIdx.x / 2;
+  const bool isv = blockIdx.x % 2;
+  const int head = id / p.chunks, e0 = (id - head * (int)p.chunks.by) * (kReadThreads * kPieces);
+  const uint8_t* src = (isv ? p.v8 : p.k8) + ((int64_t)head * p.cap + p.start) * p.D;
+  const float* scale = (isv ? p.v_scale : p.k_scale) + (int64_t)head * (p.cap >> p.block_shift);
+  E* out = (isv ? (E*)p.v_out : (E*)p.k_out) + (int64_t)head * p.out_head;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  uint32_t w[kPieces][N / 4];
+  float s[kPieces];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] *= s;
-    E* o = (E*)(isv ? p.v_out : p.k_out) + head * p.out_head + (row - p.start) * p.D + d;
-    store8(o, x);
-    store8(o + 8, x + 8);
+  for (int i = 0; i < kPieces; ++i) {
+    const int e = e0 + i * kReadThreads + threadIdx.x;
+    if (e >= p.pieces) break;
+    const int row = (int)p.start + e / p.per_row;
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(src + (int64_t)e * N);
+    if constexpr (N == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(from);
+      w[i][0] = v.x;
+      w[i][1] = v.y;
+    } else {
+      w[i][0] = *from;
+    }
+    s[i] = scale[row >> p.block_shift];
   }
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int e = e0 + i * kReadThreads + threadIdx.x;
+    if (e >= p.pieces) break;
+    float x[N];
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) e4m3x4_to_float(w[i][j], x + 4 * j);
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] *= s[i];
+    if constexpr (N == 8)
+      store8(out + (int64_t)e * N, x);
+    else
+      *reinterpret_cast<float4*>(out + (int64_t)e * N) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+int shift_of(int block) { return block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7; }
+
+// A launch that may start before what is in front of it has ended (it waits on the device).
+template <typename P>
+int launch(void (*kernel)(const P), int64_t grid, int threads, const P& p, cudaStream_t stream) {
+  if (grid > 0x7fffffff) return kErrShape;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return kOk;
+  cudaGetLastError();
+  return kErrLaunch;
 }
 
 }  // namespace
@@ -135,34 +229,50 @@ int launch_cache_write_q8(const WriteQ8Call& c) {
   p.lengths = c.span.lengths;
   p.T = c.span.T; p.start_pos = c.span.start_pos;
   p.cap = c.cache.max_seq_len; p.k_row = c.k_row; p.v_row = c.v_row;
-  p.Hkv = c.Hkv; p.D = c.D; p.block = c.cache.block;
-  p.touched = (int)((p.T + p.block - 2) / p.block + 1);
-  p.err = c.err;
-  const int64_t grid = c.span.B * c.Hkv * p.touched * 2;
+  p.D = c.D; p.block = c.cache.block;
+  const int64_t touched = (p.T + p.block - 2) / p.block + 1;
+  const int64_t grid = c.span.B * c.Hkv * touched * 2;
   if (grid > 0x7fffffff) return kErrShape;
-  if (c.dtype == PFA_F32)
-    write_kernel<float><<<(unsigned)grid, kThreads, 0, c.stream>>>(p);
-  else
-    write_kernel<__nv_bfloat16><<<(unsigned)grid, kThreads, 0, c.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? kOk : kErrLaunch;
+  p.touched = divisor((uint32_t)touched);
+  p.heads = divisor((uint32_t)c.Hkv);
+  p.per_row = divisor((uint32_t)c.D / 8);
+  p.err = c.err;
+  // Threads for a block's rows at HELD vectors each; at least four warps, for
+  // the rows of a block that a larger scale re-expresses.
+  const bool f32 = c.dtype == PFA_F32;
+  const int64_t vectors = std::min<int64_t>(p.T, p.block) * (c.D / 8), held = f32 ? 4 : 8;
+  const int threads = (int)std::min<int64_t>(
+      kMaxThreads, std::max<int64_t>(128, (vectors + held * 32 - 1) / (held * 32) * 32));
+  return f32 ? launch(write_kernel<float, 4>, grid, threads, p, c.stream)
+             : launch(write_kernel<__nv_bfloat16, 8>, grid, threads, p, c.stream);
 }
 
 int launch_cache_read_q8(const ReadQ8Call& c) {
   ReadParams p;
   p.k8 = (const uint8_t*)c.cache.k8; p.v8 = (const uint8_t*)c.cache.v8;
   p.k_scale = c.cache.k_scale; p.v_scale = c.cache.v_scale;
-  p.k_out = c.k_out; p.v_out = c.v_out;
-  p.heads = c.heads; p.start = c.start; p.rows = c.rows; p.cap = c.cache.max_seq_len;
+  p.D = c.D; p.block_shift = shift_of(c.cache.block);
+  p.cap = c.cache.max_seq_len;
   p.out_head = c.out_head;
-  p.D = c.D; p.block = c.cache.block;
-  const int64_t n = 2 * p.heads * p.rows * (p.D / 16);
-  const int64_t want = (n + kThreads - 1) / kThreads, most = (int64_t)c.num_sms * 64;
-  const unsigned grid = (unsigned)(want < most ? want : most);
-  if (c.dtype == PFA_F32)
-    read_kernel<float><<<grid, kThreads, 0, c.stream>>>(p);
-  else
-    read_kernel<__nv_bfloat16><<<grid, kThreads, 0, c.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? kOk : kErrLaunch;
+  const int per_row = c.D / (c.dtype == PFA_F32 ? 4 : 8);
+  p.per_row = divisor((uint32_t)per_row);
+  // rows of a launch: pieces of a head count in 31 bits
+  const int64_t most = (((int64_t)1 << 30) / per_row) & ~(int64_t)127;
+  for (int64_t at = 0; at < c.rows; at += most) {
+    const int64_t rows = std::min(most, c.rows - at), es = c.dtype == PFA_F32 ? 4 : 2;
+    p.start = c.start + at;
+    p.k_out = (char*)c.k_out + at * c.D * es;
+    p.v_out = (char*)c.v_out + at * c.D * es;
+    p.pieces = (int)(rows * per_row);
+    const int64_t chunks = (p.pieces + kReadThreads * kPieces - 1) / (kReadThreads * kPieces);
+    p.chunks = divisor((uint32_t)chunks);
+    const int64_t grid = c.heads * chunks * 2;
+    const int rc = c.dtype == PFA_F32
+                       ? launch(read_kernel<float>, grid, kReadThreads, p, c.stream)
+                       : launch(read_kernel<__nv_bfloat16>, grid, kReadThreads, p, c.stream);
+    if (rc != kOk) return rc;
+  }
+  return kOk;
 }
 
 }  // namespace pfa

@@ -56,22 +56,6 @@ constexpr int kJoinBytes = kWarps * 8 * 128 * 4;  // joins: 8 row sums of 128 fl
 constexpr int kHeadCost = 4;
 constexpr float kWeightScale = 16384.f;
 
-// Division of 0 <= n < 2^31 by a number that the host knows: a 64-bit product and a
-// shift, where / takes some thirty instructions (the kernels' code is mostly run
-// once a launch, and fetching it is a good part of their start).
-struct Divisor {
-  uint32_t by, m;
-  int shift;
-};
-Divisor divisor(uint32_t by) {
-  int s = 0;
-  while ((1u << s) < by) ++s;
-  return Divisor{by, (uint32_t)(((uint64_t)1 << (31 + s)) / by + 1), 31 + s};
-}
-__device__ __forceinline__ int operator/(int n, const Divisor& d) {
-  return (int)(((uint64_t)(uint32_t)n * d.m) >> d.shift);
-}
-
 struct Params {
   const void* q;
   void* out;

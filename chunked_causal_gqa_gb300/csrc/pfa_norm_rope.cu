@@ -16,11 +16,13 @@
 
 #include "../../include/pfa.h"
 
+#include <algorithm>
+
 namespace pfa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPairs = 256;  // rot_dim <= 512
+constexpr int kTableBytes = 32768;  // cosines and sines of a block's tokens
 
 struct Params {
   const void *q, *k;
@@ -28,9 +30,11 @@ struct Params {
   const void *q_weight, *k_weight;
   const double* inv_freq;
   const int64_t* lengths;
-  int64_t N, T, start_pos;
+  int64_t start_pos;
   int64_t q_row, k_row, q_out_row, k_out_row, k_out_head;
-  int H, heads, D, rot, interleaved;  // heads = H + Hkv
+  Divisor heads, T;        // H + Hkv
+  int rows;                // tokens * heads
+  int H, D, rot, interleaved, block_rows;
   float eps, offset;
 };
 
@@ -51,100 +55,179 @@ __device__ uint64_t turn_fraction(double f) {
   return (bits >> 63) ? 0 - r : r;
 }
 
+// Sixteen elements as they are stored.
 template <typename E>
+struct Raw {
+  uint4 w[sizeof(E)];
+  __device__ __forceinline__ void load(const E* a, const E* b) {
+    constexpr int N = sizeof(E) / 2, V = 16 / sizeof(E);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[i] = *reinterpret_cast<const uint4*>(a + i * V);
+      w[N + i] = *reinterpret_cast<const uint4*>(b + i * V);
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    if (sizeof(E) == 4) return __uint_as_float(u[i]);
+    return __uint_as_float(i % 2 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+  }
+};
+
+// A block takes block_rows = ROWS * kThreads / width consecutive head rows (in the
+// order of tokens, then query heads, then key heads).  `width` lanes, a power of two,
+// share a row; a lane owns two pieces of 8 elements, the two halves of eight
+// pairs or sixteen neighbours.  All of a block's rows are asked for before the
+// cosines of its tokens are computed, once for all heads.
+template <typename E, int ROWS>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
-  __shared__ float2 sCS[kMaxPairs];  // {cos, sin} of this token's pairs
-  const int64_t n = blockIdx.x;
-  const int64_t pos = p.lengths ? p.lengths[n / p.T] - p.T + n % p.T : p.start_pos + n;
-  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) {
-    const uint64_t turn = turn_fraction(p.inv_freq[i]) * (uint64_t)pos;
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-    sCS[i] = make_float2(c, s);
+  __shared__ __align__(16) float2 table[kTableBytes / sizeof(float2)];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int pieces = p.D / 16, half = p.interleaved ? 0 : p.rot / 16, turned = p.rot / 16;
+  const int shift = pieces <= 1 ? 0 : 32 - __clz(pieces - 1);   // width = 1 << shift
+  const int lane = threadIdx.x & ((1 << shift) - 1);
+  const int a = lane < half ? 8 * lane : 16 * lane;
+  const int b = lane < half ? a + 8 * half : a + 8;
+  const int row0 = blockIdx.x * p.block_rows;
+  const int row_end = min(p.rows, row0 + p.block_rows);
+  const int n0 = row0 / p.heads, tokens = (row_end - 1) / p.heads - n0 + 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  Raw<E> x[ROWS], wq, wk;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int row = row0 + i * (kThreads >> shift) + (threadIdx.x >> shift);
+    if (row < row_end && lane < pieces) {
+      const int n = row / p.heads, h = row - n * (int)p.heads.by;
+      const E* src = h < p.H ? (const E*)p.q + n * p.q_row + h * p.D
+                             : (const E*)p.k + n * p.k_row + (h - p.H) * p.D;
+      x[i].load(src + a, src + b);
+    } else {
+      x[i] = {};
+    }
+  }
+  if (lane < pieces) {
+    if (p.q_weight) wq.load((const E*)p.q_weight + a, (const E*)p.q_weight + b);
+    if (p.k_weight) wk.load((const E*)p.k_weight + a, (const E*)p.k_weight + b);
+  }
+  // pair 8 l + i of a token at [i / 2][l][i % 2]: the lanes of a row read side by side
+  for (int j = threadIdx.x; j < tokens * (p.rot / 2); j += kThreads) {
+    const int t = (uint32_t)j / (uint32_t)(p.rot / 2), pair = j - t * (p.rot / 2), n = n0 + t;
+    const int s = n / p.T;
+    const int64_t pos = p.lengths ? p.lengths[s] - (int)p.T.by + (n - s * (int)p.T.by)
+                                  : p.start_pos + n;
+    const uint64_t turn = turn_fraction(p.inv_freq[pair]) * (uint64_t)pos;
+    float sn, cs;
+    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
+    table[t * (p.rot / 2) + ((pair % 8 / 2) * turned + pair / 8) * 2 + pair % 2] =
+        make_float2(cs, sn);
   }
   __syncthreads();
-  // A lane owns two 8-element pieces of a head row: the two halves of eight
-  // pairs, or sixteen neighbours.  `width` lanes (a power of two) share a row.
-  const int pieces = p.D / 16, half = p.interleaved ? 0 : p.rot / 16;
-  int width = 1;
-  while (width < pieces) width *= 2;
-  const int lane = threadIdx.x % width;
-  for (int h0 = 0; h0 < p.heads; h0 += kThreads / width) {
-    const int h = h0 + threadIdx.x / width;
-    const bool on = h < p.heads && lane < pieces;
-    const bool isq = h < p.H;
-    const int a = lane < half ? 8 * lane : 16 * lane;
-    const int b = lane < half ? a + 8 * half : a + 8;
-    float x[16] = {};
-    if (on) {
-      const E* row = isq ? (const E*)p.q + n * p.q_row + (int64_t)h * p.D
-                         : (const E*)p.k + n * p.k_row + (int64_t)(h - p.H) * p.D;
-      load8(row + a, x);
-      load8(row + b, x + 8);
-    }
-    const E* w = (const E*)(isq ? p.q_weight : p.k_weight);
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int row = row0 + i * (kThreads >> shift) + (threadIdx.x >> shift);
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-    for (int o = width / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!on) continue;
-    if (w) {
+    for (int j = 0; j < 16; ++j) ss = fmaf(x[i].get(j), x[i].get(j), ss);
+    for (int o = (1 << shift) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (row >= row_end || lane >= pieces) continue;
+    const int n = row / p.heads, h = row - n * (int)p.heads.by;
+    const bool isq = h < p.H;
+    float y[16];
+    if (isq ? p.q_weight != nullptr : p.k_weight != nullptr) {
       const float r = rsqrtf(ss / (float)p.D + p.eps);
-      float g[16];
-      load8(w + a, g);
-      load8(w + b, g + 8);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = x[i] * r * (g[i] + p.offset);
+      for (int j = 0; j < 16; ++j)
+        y[j] = x[i].get(j) * r * ((isq ? wq.get(j) : wk.get(j)) + p.offset);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] = x[i].get(j);
     }
-    if (p.interleaved) {
-      if (a < p.rot) {
+    if (lane < turned) {
+      const float4* cs = reinterpret_cast<const float4*>(table + (n - n0) * (p.rot / 2)) + lane;
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float2 cs = sCS[a / 2 + i / 2];
-          const float u = x[i], v = x[i + 1];
-          x[i] = u * cs.x - v * cs.y;
-          x[i + 1] = u * cs.y + v * cs.x;
+      for (int j = 0; j < 4; ++j) {   // pairs 2 j and 2 j + 1 of the lane
+        const float4 c = cs[j * turned];
+        if (p.interleaved) {
+          const float u0 = y[4 * j], v0 = y[4 * j + 1], u1 = y[4 * j + 2], v1 = y[4 * j + 3];
+          y[4 * j] = u0 * c.x - v0 * c.y;
+          y[4 * j + 1] = u0 * c.y + v0 * c.x;
+          y[4 * j + 2] = u1 * c.z - v1 * c.w;
+          y[4 * j + 3] = u1 * c.w + v1 * c.z;
+        } else {
+          const float u0 = y[2 * j], v0 = y[2 * j + 8], u1 = y[2 * j + 1], v1 = y[2 * j + 9];
+          y[2 * j] = u0 * c.x - v0 * c.y;
+          y[2 * j + 8] = u0 * c.y + v0 * c.x;
+          y[2 * j + 1] = u1 * c.z - v1 * c.w;
+          y[2 * j + 9] = u1 * c.w + v1 * c.z;
         }
       }
-    } else if (lane < half) {
+    }
+    if (p.lengths) {
+      const int s = n / p.T;
+      if (p.lengths[s] - (int)p.T.by + (n - s * (int)p.T.by) < 0) {  // padding in front
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 cs = sCS[a + i];
-        const float u = x[i], v = x[i + 8];
-        x[i] = u * cs.x - v * cs.y;
-        x[i + 8] = u * cs.y + v * cs.x;
+        for (int j = 0; j < 16; ++j) y[j] = 0.f;
       }
     }
-    if (pos < 0) {  // padding in front of a short sequence
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    }
-    E* o = isq ? (E*)p.q_out + n * p.q_out_row + (int64_t)h * p.D
-               : (E*)p.k_out + n * p.k_out_row + (int64_t)(h - p.H) * p.k_out_head;
-    store8(o + a, x);
-    store8(o + b, x + 8);
+    E* o = isq ? (E*)p.q_out + n * p.q_out_row + h * p.D
+               : (E*)p.k_out + n * p.k_out_row + (h - p.H) * p.k_out_head;
+    store8(o + a, y);
+    store8(o + b, y + 8);
   }
+}
+
+template <typename E, int ROWS>
+cudaError_t launch(Params p, int width, cudaStream_t stream) {
+  p.block_rows = ROWS * kThreads / width;
+  // the table holds the tokens that a block's rows can touch
+  if (p.rot > 0) {
+    const int most = kTableBytes / (p.rot / 2 * (int)sizeof(float2));
+    p.block_rows = std::min<int64_t>(p.block_rows, (int64_t)(most - 1) * p.heads.by + 1);
+  }
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.rows + p.block_rows - 1) / p.block_rows));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<E, ROWS>, (const Params)p);
 }
 
 }  // namespace
 
 int launch_norm_rope(const NormRopeCall& c) {
+  const int64_t tokens = c.span.B * c.span.T, rows = tokens * (c.H + c.Hkv);
+  if (rows > 0x7fffffff - 65536) return kErrShape;
   Params p;
   p.q = c.q; p.k = c.k; p.q_out = c.q_out; p.k_out = c.k_out;
   p.q_weight = c.q_weight; p.k_weight = c.k_weight;
   p.inv_freq = c.inv_freq;
   p.lengths = c.span.lengths;
-  p.N = c.span.B * c.span.T; p.T = c.span.T; p.start_pos = c.span.start_pos;
+  p.start_pos = c.span.start_pos;
   p.q_row = c.q_row; p.k_row = c.k_row; p.q_out_row = c.q_out_row; p.k_out_row = c.k_out_row;
   p.k_out_head = c.k_out_head;
-  p.H = c.H; p.heads = c.H + c.Hkv; p.D = c.D;
+  p.heads = divisor(c.H + c.Hkv);
+  p.T = divisor((uint32_t)c.span.T);
+  p.rows = (int)rows;
+  p.H = c.H; p.D = c.D;
   p.rot = c.rot_dim; p.interleaved = c.interleaved;
   p.eps = c.eps; p.offset = c.weight_offset;
+  int width = 1;
+  while (width < c.D / 16) width *= 2;
+  // Few rows: one to a lane group, for the shortest chain; many: several in flight.
+  const bool few = rows * width <= (int64_t)c.num_sms * kThreads * 4;
+  cudaError_t e;
   if (c.dtype == PFA_F32)
-    norm_rope_kernel<float><<<(unsigned)p.N, kThreads, 0, c.stream>>>(p);
+    e = few ? launch<float, 1>(p, width, c.stream) : launch<float, 2>(p, width, c.stream);
   else
-    norm_rope_kernel<__nv_bfloat16><<<(unsigned)p.N, kThreads, 0, c.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? kOk : kErrLaunch;
+    e = few ? launch<__nv_bfloat16, 1>(p, width, c.stream) : launch<__nv_bfloat16, 4>(p, width, c.stream);
+  if (e == cudaSuccess) return kOk;
+  cudaGetLastError();
+  return kErrLaunch;
 }
 
 }  // namespace pfa

@@ -7,6 +7,22 @@
 
 namespace pfa {
 
+// Division of 0 <= n < 2^31 by a number that the host knows: a 64-bit product and a
+// shift, where / takes some thirty instructions (the kernels' code is mostly run
+// once a launch, and fetching it is a good part of their start).
+struct Divisor {
+  uint32_t by, m;
+  int shift;
+};
+inline Divisor divisor(uint32_t by) {
+  int s = 0;
+  while ((1u << s) < by) ++s;
+  return Divisor{by, (uint32_t)(((uint64_t)1 << (31 + s)) / by + 1), 31 + s};
+}
+__device__ __forceinline__ int operator/(int n, const Divisor& d) {
+  return (int)(((uint64_t)(uint32_t)n * d.m) >> d.shift);
+}
+
 // Four e4m3 codes of a word -> two half pairs; every e4m3 value (NaN among
 // them) is exact in half.
 __device__ __forceinline__ void e4m3x4_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
