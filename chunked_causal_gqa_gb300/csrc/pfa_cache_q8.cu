@@ -243,6 +243,9 @@ int launch_cache_write_q8(const WriteQ8Call& c) {
   const int64_t vectors = std::min<int64_t>(p.T, p.block) * (c.D / 8), held = f32 ? 4 : 8;
   const int threads = (int)std::min<int64_t>(
       kMaxThreads, std::max<int64_t>(128, (vectors + held * 32 - 1) / (held * 32) * 32));
+  if (vectors <= threads)   // decoding: one vector a thread, a third of the code to fetch
+    return f32 ? launch(write_kernel<float, 1>, grid, threads, p, c.stream)
+               : launch(write_kernel<__nv_bfloat16, 1>, grid, threads, p, c.stream);
   return f32 ? launch(write_kernel<float, 4>, grid, threads, p, c.stream)
              : launch(write_kernel<__nv_bfloat16, 8>, grid, threads, p, c.stream);
 }

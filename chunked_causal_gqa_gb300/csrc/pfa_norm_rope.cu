@@ -22,20 +22,25 @@ namespace pfa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTableBytes = 32768;  // cosines and sines of a block's tokens
+constexpr int kTableBytes = 32768;  // most of cosines and sines of a block's tokens
 
+struct Side {               // the queries or the keys
+  const void* in;
+  void* out;
+  const void* weight;
+  int64_t in_row, out_row, out_head;
+  Divisor heads;
+  int rows, block_rows;     // tokens * heads; rows of a block
+};
 struct Params {
-  const void *q, *k;
-  void *q_out, *k_out;
-  const void *q_weight, *k_weight;
+  Side side[2];
+  int q_blocks;             // blocks of the queries, in front of the keys'
   const double* inv_freq;
   const int64_t* lengths;
   int64_t start_pos;
-  int64_t q_row, k_row, q_out_row, k_out_row, k_out_head;
-  Divisor heads, T;        // H + Hkv
-  int rows;                // tokens * heads
-  int H, D, rot, interleaved, block_rows;
-  float eps, offset;
+  Divisor T;
+  int D, rot, interleaved;
+  float eps, offset, inv_dim;   // 1 / D
 };
 
 // f / (2 pi) modulo 1 as a 64-bit fraction, from the double's bits.
@@ -55,142 +60,193 @@ __device__ uint64_t turn_fraction(double f) {
   return (bits >> 63) ? 0 - r : r;
 }
 
-// Sixteen elements as they are stored.
+// Two floats in one register pair: one instruction for both.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ uint64_t bits(F2 a) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a.x), "f"(a.y));
+  return v;
+}
+__device__ __forceinline__ F2 of_bits(uint64_t v) {
+  F2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(v));
+  return a;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(bits(a)), "l"(bits(b)));
+  return of_bits(v);
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return of_bits(v);
+}
+
+// A lane's sixteen elements as they are stored: pieces of 16 bytes.
 template <typename E>
 struct Raw {
-  uint4 w[sizeof(E)];
-  __device__ __forceinline__ void load(const E* a, const E* b) {
-    constexpr int N = sizeof(E) / 2, V = 16 / sizeof(E);
+  static constexpr int V = 16 / sizeof(E), N = sizeof(E);   // elements of a piece, pieces
+  uint4 w[N];
+  __device__ __forceinline__ void load(const E* p, int stride) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      w[i] = *reinterpret_cast<const uint4*>(a + i * V);
-      w[N + i] = *reinterpret_cast<const uint4*>(b + i * V);
-    }
+    for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4*>(p + i * stride);
   }
-  __device__ __forceinline__ float get(int i) const {
+  __device__ __forceinline__ F2 pair(int i) const {   // elements 2 i and 2 i + 1
     const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
-    if (sizeof(E) == 4) return __uint_as_float(u[i]);
-    return __uint_as_float(i % 2 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    if (sizeof(E) == 4) return F2{__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])};
+    return F2{__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u)};
   }
 };
+__device__ __forceinline__ void store_pieces(float* p, int stride, const F2* y) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<float4*>(p + i * stride) =
+        make_float4(y[2 * i].x, y[2 * i].y, y[2 * i + 1].x, y[2 * i + 1].y);
+}
+__device__ __forceinline__ void store_pieces(__nv_bfloat16* p, int stride, const F2* y) {
+  store8(p, reinterpret_cast<const float*>(y));
+  store8(p + stride, reinterpret_cast<const float*>(y + 4));
+}
 
-// A block takes block_rows = ROWS * kThreads / width consecutive head rows (in the
-// order of tokens, then query heads, then key heads).  `width` lanes, a power of two,
-// share a row; a lane owns two pieces of 8 elements, the two halves of eight
-// pairs or sixteen neighbours.  All of a block's rows are asked for before the
-// cosines of its tokens are computed, once for all heads.
+// A block takes block_rows = ROWS * kThreads / width consecutive head rows of the
+// queries or of the keys (in the order of tokens, then heads).  `width` lanes, a
+// power of two, share a row; a lane owns 16 elements, whose 16-byte pieces lie
+// side by side with the other lanes'.  Of a head's rot / 16 lanes that rotate, lane l has
+// the pieces l + m * rot / 16 of the first rot elements: for pairs (i, i + rot / 2) the
+// second half of its pieces are the partners of the first.  All of a block's rows are
+// asked for before the cosines of its tokens are computed, once for all heads.
 template <typename E, int ROWS>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
-  __shared__ __align__(16) float2 table[kTableBytes / sizeof(float2)];
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) float table[];
   asm volatile("griddepcontrol.launch_dependents;");
-  const int pieces = p.D / 16, half = p.interleaved ? 0 : p.rot / 16, turned = p.rot / 16;
-  const int shift = pieces <= 1 ? 0 : 32 - __clz(pieces - 1);   // width = 1 << shift
+  const bool isk = (int)blockIdx.x >= p.q_blocks;
+  const Side& side = p.side[isk ? 1 : 0];
+  constexpr int V = Raw<E>::V;
+  const int lanes = p.D / 16, turned = p.rot / 16;
+  const int shift = lanes <= 1 ? 0 : 32 - __clz(lanes - 1);   // width = 1 << shift
   const int lane = threadIdx.x & ((1 << shift) - 1);
-  const int a = lane < half ? 8 * lane : 16 * lane;
-  const int b = lane < half ? a + 8 * half : a + 8;
-  const int row0 = blockIdx.x * p.block_rows;
-  const int row_end = min(p.rows, row0 + p.block_rows);
-  const int n0 = row0 / p.heads, tokens = (row_end - 1) / p.heads - n0 + 1;
+  const int at = lane < turned ? V * lane : p.rot + V * (lane - turned);
+  const int stride = V * (lane < turned ? turned : lanes - turned);
+  const int row0 = ((int)blockIdx.x - (isk ? p.q_blocks : 0)) * side.block_rows;
+  const int row_end = min(side.rows, row0 + side.block_rows);
+  const int n0 = row0 / side.heads, tokens = (row_end - 1) / side.heads - n0 + 1;
+  const int step = kThreads >> shift, mine = row0 + (threadIdx.x >> shift);
+  const bool on = lane < lanes;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  Raw<E> x[ROWS], wq, wk;
+  Raw<E> x[ROWS], w;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const int row = row0 + i * (kThreads >> shift) + (threadIdx.x >> shift);
-    if (row < row_end && lane < pieces) {
-      const int n = row / p.heads, h = row - n * (int)p.heads.by;
-      const E* src = h < p.H ? (const E*)p.q + n * p.q_row + h * p.D
-                             : (const E*)p.k + n * p.k_row + (h - p.H) * p.D;
-      x[i].load(src + a, src + b);
-    } else {
-      x[i] = {};
+    const int row = mine + i * step;
+    x[i] = {};
+    if (on && row < row_end) {
+      const int n = row / side.heads, h = row - n * (int)side.heads.by;
+      x[i].load((const E*)side.in + n * side.in_row + h * p.D + at, stride);
     }
   }
-  if (lane < pieces) {
-    if (p.q_weight) wq.load((const E*)p.q_weight + a, (const E*)p.q_weight + b);
-    if (p.k_weight) wk.load((const E*)p.k_weight + a, (const E*)p.k_weight + b);
-  }
-  // pair 8 l + i of a token at [i / 2][l][i % 2]: the lanes of a row read side by side
-  for (int j = threadIdx.x; j < tokens * (p.rot / 2); j += kThreads) {
-    const int t = (uint32_t)j / (uint32_t)(p.rot / 2), pair = j - t * (p.rot / 2), n = n0 + t;
+  w = {};
+  const bool norm = side.weight != nullptr;
+  if (on && norm) w.load((const E*)side.weight + at, stride);
+  auto position = [&](int n) -> int64_t {
+    if (!p.lengths) return p.start_pos + n;
     const int s = n / p.T;
-    const int64_t pos = p.lengths ? p.lengths[s] - (int)p.T.by + (n - s * (int)p.T.by)
-                                  : p.start_pos + n;
-    const uint64_t turn = turn_fraction(p.inv_freq[pair]) * (uint64_t)pos;
-    float sn, cs;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
-    table[t * (p.rot / 2) + ((pair % 8 / 2) * turned + pair / 8) * 2 + pair % 2] =
-        make_float2(cs, sn);
+    return p.lengths[s] - (int)p.T.by + (n - s * (int)p.T.by);
+  };
+  // a lane's pairs 2 i and 2 i + 1 at [i][lane]: {cos, cos, sin, sin}; a piece has `in` pairs
+  const int in = p.interleaved ? V / 2 : V;
+  const int pairs = p.rot / 2;
+  if (pairs > 0) {   // a thread has one pair of every `apart`-th token
+    const int apart = (int)((uint32_t)kThreads / (uint32_t)pairs);
+    const int t0 = (int)((uint32_t)threadIdx.x / (uint32_t)pairs), pair = threadIdx.x - t0 * pairs;
+    if (t0 < apart) {
+      const uint64_t fraction = turn_fraction(p.inv_freq[pair]);
+      const int piece = pair / in, m = (int)((uint32_t)piece / (uint32_t)turned);
+      const int k = m * in + pair % in;
+      float* to = table + ((k / 2) * turned + piece - m * turned) * 4 + k % 2;
+      for (int t = t0; t < tokens; t += apart) {
+        const uint64_t turn = fraction * (uint64_t)position(n0 + t);
+        float sn, cs;
+        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
+        to[t * p.rot] = cs;
+        to[t * p.rot + 2] = sn;
+      }
+    }
+  }
+  F2 g[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const F2 v = w.pair(j);
+    g[j] = norm ? F2{v.x + p.offset, v.y + p.offset} : F2{1.f, 1.f};
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const int row = row0 + i * (kThreads >> shift) + (threadIdx.x >> shift);
-    float ss = 0.f;
+    const int row = mine + i * step;
+    F2 y[8], sum = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < 16; ++j) ss = fmaf(x[i].get(j), x[i].get(j), ss);
+    for (int j = 0; j < 8; ++j) {
+      y[j] = x[i].pair(j);
+      sum = fma(y[j], y[j], sum);
+    }
+    float ss = sum.x + sum.y;
     for (int o = (1 << shift) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (row >= row_end || lane >= pieces) continue;
-    const int n = row / p.heads, h = row - n * (int)p.heads.by;
-    const bool isq = h < p.H;
-    float y[16];
-    if (isq ? p.q_weight != nullptr : p.k_weight != nullptr) {
-      const float r = rsqrtf(ss / (float)p.D + p.eps);
+    if (!on || row >= row_end) continue;
+    const int n = row / side.heads, h = row - n * (int)side.heads.by;
+    if (norm) {
+      const float r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        y[j] = x[i].get(j) * r * ((isq ? wq.get(j) : wk.get(j)) + p.offset);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) y[j] = x[i].get(j);
+      for (int j = 0; j < 8; ++j) y[j] = mul(mul(y[j], F2{r, r}), g[j]);
     }
     if (lane < turned) {
-      const float4* cs = reinterpret_cast<const float4*>(table + (n - n0) * (p.rot / 2)) + lane;
+      const float4* cs = reinterpret_cast<const float4*>(table + (n - n0) * p.rot) + lane;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {   // pairs 2 j and 2 j + 1 of the lane
-        const float4 c = cs[j * turned];
+        const float4 t = cs[j * turned];
+        const F2 c = {t.x, t.y}, s = {t.z, t.w}, ns = {-t.z, -t.w};
         if (p.interleaved) {
-          const float u0 = y[4 * j], v0 = y[4 * j + 1], u1 = y[4 * j + 2], v1 = y[4 * j + 3];
-          y[4 * j] = u0 * c.x - v0 * c.y;
-          y[4 * j + 1] = u0 * c.y + v0 * c.x;
-          y[4 * j + 2] = u1 * c.z - v1 * c.w;
-          y[4 * j + 3] = u1 * c.w + v1 * c.z;
+          const F2 u = {y[2 * j].x, y[2 * j + 1].x}, v = {y[2 * j].y, y[2 * j + 1].y};
+          const F2 re = fma(u, c, mul(v, ns)), im = fma(u, s, mul(v, c));
+          y[2 * j] = {re.x, im.x};
+          y[2 * j + 1] = {re.y, im.y};
         } else {
-          const float u0 = y[2 * j], v0 = y[2 * j + 8], u1 = y[2 * j + 1], v1 = y[2 * j + 9];
-          y[2 * j] = u0 * c.x - v0 * c.y;
-          y[2 * j + 8] = u0 * c.y + v0 * c.x;
-          y[2 * j + 1] = u1 * c.z - v1 * c.w;
-          y[2 * j + 9] = u1 * c.w + v1 * c.z;
+          const F2 u = y[j], v = y[j + 4];
+          y[j] = fma(u, c, mul(v, ns));
+          y[j + 4] = fma(u, s, mul(v, c));
         }
       }
     }
-    if (p.lengths) {
-      const int s = n / p.T;
-      if (p.lengths[s] - (int)p.T.by + (n - s * (int)p.T.by) < 0) {  // padding in front
+    if (p.lengths && position(n) < 0) {  // padding in front
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = 0.f;
-      }
+      for (int j = 0; j < 8; ++j) y[j] = {0.f, 0.f};
     }
-    E* o = isq ? (E*)p.q_out + n * p.q_out_row + h * p.D
-               : (E*)p.k_out + n * p.k_out_row + (h - p.H) * p.k_out_head;
-    store8(o + a, y);
-    store8(o + b, y + 8);
+    store_pieces((E*)side.out + n * side.out_row + h * side.out_head + at, stride, y);
   }
 }
 
 template <typename E, int ROWS>
 cudaError_t launch(Params p, int width, cudaStream_t stream) {
-  p.block_rows = ROWS * kThreads / width;
-  // the table holds the tokens that a block's rows can touch
-  if (p.rot > 0) {
-    const int most = kTableBytes / (p.rot / 2 * (int)sizeof(float2));
-    p.block_rows = std::min<int64_t>(p.block_rows, (int64_t)(most - 1) * p.heads.by + 1);
+  int blocks[2], tokens = 0;
+  for (int i = 0; i < 2; ++i) {
+    Side& s = p.side[i];
+    const int64_t heads = s.heads.by;
+    int64_t n = ROWS * kThreads / width;
+    // the table holds the tokens that a block's rows can touch
+    if (p.rot > 0) n = std::min<int64_t>(n, (kTableBytes / (p.rot * (int64_t)sizeof(float)) - 1) * heads + 1);
+    s.block_rows = (int)n;
+    blocks[i] = (int)((s.rows + n - 1) / n);
+    tokens = std::max<int>(tokens, (int)((n - 1 + heads - 1) / heads) + 1);
   }
+  p.q_blocks = blocks[0];
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.rows + p.block_rows - 1) / p.block_rows));
+  cfg.gridDim = dim3((unsigned)(blocks[0] + blocks[1]));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)tokens * p.rot * sizeof(float);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -203,28 +259,26 @@ int launch_norm_rope(const NormRopeCall& c) {
   const int64_t tokens = c.span.B * c.span.T, rows = tokens * (c.H + c.Hkv);
   if (rows > 0x7fffffff - 65536) return kErrShape;
   Params p;
-  p.q = c.q; p.k = c.k; p.q_out = c.q_out; p.k_out = c.k_out;
-  p.q_weight = c.q_weight; p.k_weight = c.k_weight;
+  p.side[0] = Side{c.q, c.q_out, c.q_weight, c.q_row, c.q_out_row, c.D, divisor(c.H),
+                   (int)(tokens * c.H), 0};
+  p.side[1] = Side{c.k, c.k_out, c.k_weight, c.k_row, c.k_out_row, c.k_out_head, divisor(c.Hkv),
+                   (int)(tokens * c.Hkv), 0};
   p.inv_freq = c.inv_freq;
   p.lengths = c.span.lengths;
   p.start_pos = c.span.start_pos;
-  p.q_row = c.q_row; p.k_row = c.k_row; p.q_out_row = c.q_out_row; p.k_out_row = c.k_out_row;
-  p.k_out_head = c.k_out_head;
-  p.heads = divisor(c.H + c.Hkv);
   p.T = divisor((uint32_t)c.span.T);
-  p.rows = (int)rows;
-  p.H = c.H; p.D = c.D;
+  p.D = c.D;
   p.rot = c.rot_dim; p.interleaved = c.interleaved;
-  p.eps = c.eps; p.offset = c.weight_offset;
+  p.eps = c.eps; p.offset = c.weight_offset; p.inv_dim = 1.f / (float)c.D;
   int width = 1;
   while (width < c.D / 16) width *= 2;
   // Few rows: one to a lane group, for the shortest chain; many: several in flight.
   const bool few = rows * width <= (int64_t)c.num_sms * kThreads * 4;
   cudaError_t e;
   if (c.dtype == PFA_F32)
-    e = few ? launch<float, 1>(p, width, c.stream) : launch<float, 2>(p, width, c.stream);
+    e = few ? launch<float, 1>(p, width, c.stream) : launch<float, 1>(p, width, c.stream);
   else
-    e = few ? launch<__nv_bfloat16, 1>(p, width, c.stream) : launch<__nv_bfloat16, 4>(p, width, c.stream);
+    e = few ? launch<__nv_bfloat16, 1>(p, width, c.stream) : launch<__nv_bfloat16, 2>(p, width, c.stream);
   if (e == cudaSuccess) return kOk;
   cudaGetLastError();
   return kErrLaunch;
