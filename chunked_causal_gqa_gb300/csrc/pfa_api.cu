@@ -95,6 +95,9 @@ int current_device(DeviceInfo* d) {
   d->device = dev;
   d->num_sms = st->num_sms;
   d->err = st->err;
+  std::lock_guard<std::mutex> lk(g_mutex);
+  d->wait_limit_ns = (uint64_t)(g_wait_limit_ms * 1e6);
+  d->flags = g_force_timeout ? kFlagForceTimeout : 0;
   return kOk;
 }
 

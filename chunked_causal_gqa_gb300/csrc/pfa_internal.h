@@ -90,6 +90,8 @@ struct DeviceInfo {
   int device;
   int num_sms;
   unsigned* err;  // device error word
+  uint64_t wait_limit_ns;
+  int flags;
 };
 int current_device(DeviceInfo* d);
 // Whether kernels on device `dev` can use p (device or managed memory).
@@ -208,11 +210,19 @@ struct DecodeQ8Call {
   unsigned* err;
   int num_sms;
   int device;
+  uint64_t wait_limit_ns;           // as in Call
+  int flags;
   void* ws;
   cudaStream_t stream;
 };
 // Workspace bytes of launch_decode_q8 for B sequences of T tokens.
 size_t decode_q8_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int num_sms);
 int launch_decode_q8(const DecodeQ8Call& c);
+
+// A bf16 chunk of one sequence, head_dim 128, on the tensor cores from the codes:
+// whether it serves the call, its workspace bytes, the launch.
+bool q8_d128_serves(int64_t T, int H, int Hkv);
+size_t q8_d128_workspace(int64_t T, int64_t start_pos, int H, int Hkv, int window, int num_sms);
+int launch_q8_d128(const DecodeQ8Call& c);
 
 }  // namespace pfa

@@ -87,23 +87,33 @@ int check_attention(int64_t B, int64_t T, int H, int Hkv, int D, float scale, in
   return PFA_OK;
 }
 
-// How a chunk of one sequence runs: its few rows straight from the codes, or
-// the visible cache rows read back into the workspace and the 16/32-bit
-// kernels on them.
+// How a chunk of one sequence runs: its few rows by the decode kernel, the tiles of
+// a bf16 chunk of head_dim 128 from the codes, or the visible cache rows read back
+// into the workspace and the 16/32-bit kernels on them.
+enum class How { kDecode, kCodes, kReadBack };
 struct PrefillPlan {
-  bool direct;
-  int64_t lo, rows;       // cache rows [lo, lo + rows) are visible
-  size_t v_at, ws_at, total;
+  How how;
+  size_t total;           // workspace
+  int64_t lo, rows;       // kReadBack: cache rows [lo, lo + rows) are visible
+  size_t v_at, ws_at;
   Call call;              // on the read-back rows
 };
 
-bool prefill_direct(int64_t T, int group) { return T * group <= 64; }
+How prefill_how(int64_t T, int H, int Hkv, int D, int dtype) {
+  if (T * (H / Hkv) <= 64) return How::kDecode;
+  if (dtype == PFA_BF16 && D == 128 && q8_d128_serves(T, H, Hkv)) return How::kCodes;
+  return How::kReadBack;
+}
 
 int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window, float scale,
                  int dtype, int64_t qkv_dim, int num_sms, void* stream, PrefillPlan* p) {
-  p->direct = prefill_direct(T, H / Hkv);
-  if (p->direct) {
+  p->how = prefill_how(T, H, Hkv, D, dtype);
+  if (p->how == How::kDecode) {
     p->total = decode_q8_workspace(1, T, H, Hkv, D, dtype, num_sms);
+    return PFA_OK;
+  }
+  if (p->how == How::kCodes) {
+    p->total = q8_d128_workspace(T, start_pos, H, Hkv, std::max(window, 0), num_sms);
     return PFA_OK;
   }
   p->lo = window > 0 ? std::max<int64_t>(0, start_pos - window + 1) : 0;
@@ -350,6 +360,7 @@ int pfa_decode_attention_q8(const void* q, const void* k8, const void* v8, const
   c.window = window > 0 ? window : 0; c.dtype = dtype; c.scale = scale;
   c.q_row = q_stride; c.out_row = out_stride;
   c.err = d.err; c.num_sms = d.num_sms; c.device = d.device;
+  c.wait_limit_ns = d.wait_limit_ns; c.flags = d.flags;
   c.ws = workspace;
   c.stream = static_cast<cudaStream_t>(stream);
   return launch_decode_q8(c);
@@ -412,7 +423,7 @@ int pfa_prefill_attention_q8(const void* q, const void* k8, const void* v8, cons
   if (!device_accessible(q, d.device) || !device_accessible(out, d.device) ||
       !accessible(cache, d.device))
     return PFA_ERR_DEVICE;
-  if (plan.direct) {
+  if (plan.how != How::kReadBack) {
     DecodeQ8Call c;
     c.q = q; c.out = out; c.cache = cache;
     c.span = Span{1, T, start_pos, nullptr};
@@ -420,9 +431,10 @@ int pfa_prefill_attention_q8(const void* q, const void* k8, const void* v8, cons
     c.window = window > 0 ? window : 0; c.dtype = dtype; c.scale = scale;
     c.q_row = qkv_dim; c.out_row = qkv_dim;
     c.err = d.err; c.num_sms = d.num_sms; c.device = d.device;
+    c.wait_limit_ns = d.wait_limit_ns; c.flags = d.flags;
     c.ws = workspace;
     c.stream = static_cast<cudaStream_t>(stream);
-    return launch_decode_q8(c);
+    return plan.how == How::kDecode ? launch_decode_q8(c) : launch_q8_d128(c);
   }
   char* base = static_cast<char*>(workspace);
   ReadQ8Call r;

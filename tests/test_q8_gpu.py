@@ -410,7 +410,7 @@ def test_prefill(T, sp, window, D, dt):
 
 
 def test_prefill_on_read_back_rows_is_prefill_attention():
-    T, sp, H, Hkv, D = 300, 701, 8, 2, 128
+    T, sp, H, Hkv, D = 300, 701, 8, 2, 512
     cache = pkg.Q8Cache(*R.make_cache(Hkv, 1024, D, 64, seed=3, device=G.dev(), dead=[sp + T]))
     q = randn((T, H, D), BF16, 1)
     k, v = pkg.cache_read_q8(cache, 0, sp + T)
