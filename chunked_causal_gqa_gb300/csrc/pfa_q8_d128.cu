@@ -249,59 +249,81 @@ q8_d128_kernel(const __grid_constant__ Params p) {
   } else if (warp >= 8) {
     // ------------------------------------------------------------ converters
     registers_down<88>();
-    // load i of 8: row 16 i + r0 of the tile, codes 16 j .. 16 j + 15
-    const int r0 = (warp - 8) * 4 + (lane >> 3), j = lane & 7;
-    const uint32_t swz = (uint32_t)(r0 & 7), chunk = (uint32_t)(j & 3) * 2, flip = (uint32_t)j >> 2;
-    // Lanes of the second half write their upper chunk first: eight lanes, eight chunks.
-    const uint32_t base = (j >> 2) * kHalfBytes + r0 * 128;
-    const uint32_t at_first = base + (((chunk + flip) ^ swz) << 4);
-    const uint32_t at_second = base + (((chunk + 1 - flip) ^ swz) << 4);
-    const int64_t row0 = (int64_t)u.kh * p.cap;
+    // A warp has 32 rows of the tile, eight at a time: lane l row l % 8 and, of the row's
+    // eight pieces of 16 codes, piece l / 8 of the first half or of the second (load 2 g + half).
+    // Eight lanes with eight rows and one chunk fill all chunks of the swizzle.
+    const int r0 = (warp - 8) * 32 + (lane & 7), piece = lane >> 3;
+    const uint32_t at = (uint32_t)r0 * 128 + (((uint32_t)piece * 2 ^ (uint32_t)(lane & 7)) << 4);
+    const int64_t off0 = ((int64_t)u.kh * p.cap + r0) * 128 + piece * 16;
     const float unit_k = kOperandScale / kref, unit_v = kOperandScale / vref;
     uint4 code[8];
-    float sc[8];
+    float sc[4];
     // load i of the ring's tile t (K and V in turn); nothing of a key that no row sees
     auto load = [&](int t, int i) {
-      const int key = key_first + (t >> 1) * kBN + r0 + 16 * i;
-      code[i] = make_uint4(0, 0, 0, 0);
-      sc[i] = 0.f;
-      if (key >= lo && key <= hi) {
-        code[i] = __ldg(reinterpret_cast<const uint4*>((t & 1 ? p.v8 : p.k8) + (row0 + key) * 128 +
-                                                       j * 16));
-        sc[i] = __ldg((t & 1 ? p.v_scale : p.k_scale) + scales + (key >> p.block_shift));
+      const int key0 = key_first + (t >> 1) * kBN, key = key0 + r0 + 8 * (i >> 1);
+      const uint8_t* src = (t & 1 ? p.v8 : p.k8) + off0 + (int64_t)key0 * 128 + (i >> 1) * 1024 +
+                           (i & 1) * 64;
+      const bool on = key >= lo && key <= hi;
+      code[i] = on ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+      if (i % 2 == 0) {   // eight rows are in one block
+        sc[i >> 1] = on ? __ldg((t & 1 ? p.v_scale : p.k_scale) + scales + (key >> p.block_shift)) : 0.f;
       }
+    };
+    auto load_inner = [&](int t, int i) {   // all keys of the tile are seen
+      const int key0 = key_first + (t >> 1) * kBN, key = key0 + r0 + 8 * (i >> 1);
+      const uint8_t* src = (t & 1 ? p.v8 : p.k8) + off0 + (int64_t)key0 * 128;
+      code[i] = __ldg(reinterpret_cast<const uint4*>(src + (i >> 1) * 1024 + (i & 1) * 64));
+      if (i % 2 == 0)
+        sc[i >> 1] = __ldg((t & 1 ? p.v_scale : p.k_scale) + scales + (key >> p.block_shift));
+    };
+    auto convert = [&](int i, uint8_t* dst, float unit) {
+      const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+      const float f = sc[i >> 1] * unit;
+      const uint32_t ff = pack_half2(f, f);
+      uint32_t h[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        e4m3x4_to_half(w[k], h[2 * k], h[2 * k + 1]);
+        h[2 * k] = mul_half2(h[2 * k], ff);
+        h[2 * k + 1] = mul_half2(h[2 * k + 1], ff);
+      }
+      uint8_t* to = dst + (i >> 1) * 1024 + (i & 1) * kHalfBytes;
+      *reinterpret_cast<uint4*>(to + at) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(to + (at ^ 16u)) = make_uint4(h[4], h[5], h[6], h[7]);
     };
     bool ok = true;
 #pragma unroll
     for (int i = 0; i < 8; ++i) load(0, i);
+#pragma unroll 1
     for (int t = 0; t < 2 * n; ++t) {
       // the rows two tiles on, into L2
       const int ahead = key_first + ((t >> 1) + 2) * kBN + (tid & 127);
       if (ahead <= hi)
-        asm volatile("prefetch.global.L2 [%0];" :: "l"((t & 1 ? p.v8 : p.k8) + (row0 + ahead) * 128));
+        asm volatile("prefetch.global.L2 [%0];"
+                     :: "l"((t & 1 ? p.v8 : p.k8) + ((int64_t)u.kh * p.cap + ahead) * 128));
       const float unit = t & 1 ? unit_v : unit_k;
       const uint32_t e = (uint32_t)t % kSlots;
       ok = mbar_wait_warp(bar(kBarEmpty + (int)e), (((uint32_t)t / kSlots) & 1u) ^ 1u, abort_flag,
                           p.err, lim);
       if (!ok) break;
       uint8_t* dst = smem + kSmemRing + e * kTileBytes;
+      const int next0 = key_first + ((t + 1) >> 1) * kBN;
+      if (t + 1 < 2 * n && next0 >= lo && next0 + kBN - 1 <= hi) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-        const float f = sc[i] * unit;
-        const uint32_t ff = pack_half2(f, f);
-        uint32_t h[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          e4m3x4_to_half(w[k], h[2 * k], h[2 * k + 1]);
-          h[2 * k] = mul_half2(h[2 * k], ff);
-          h[2 * k + 1] = mul_half2(h[2 * k + 1], ff);
+        for (int i = 0; i < 8; ++i) {
+          convert(i, dst, unit);
+          if (i % 2) {
+            load_inner(t + 1, i - 1);   // arrives while the ring is full
+            load_inner(t + 1, i);
+          }
         }
-        if (t + 1 < 2 * n) load(t + 1, i);   // arrives while the ring is full
-        const uint4 a = make_uint4(h[0], h[1], h[2], h[3]);
-        const uint4 b = make_uint4(h[4], h[5], h[6], h[7]);
-        *reinterpret_cast<uint4*>(dst + at_first + i * 2048) = flip ? b : a;
-        *reinterpret_cast<uint4*>(dst + at_second + i * 2048) = flip ? a : b;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) convert(i, dst, unit);
+        if (t + 1 < 2 * n) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) load(t + 1, i);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
