@@ -296,11 +296,12 @@ q8_d128_kernel(const __grid_constant__ Params p) {
     for (int i = 0; i < 8; ++i) load(0, i);
 #pragma unroll 1
     for (int t = 0; t < 2 * n; ++t) {
-      // the rows two tiles on, into L2
-      const int ahead = key_first + ((t >> 1) + 2) * kBN + (tid & 127);
-      if (ahead <= hi)
-        asm volatile("prefetch.global.L2 [%0];"
-                     :: "l"((t & 1 ? p.v8 : p.k8) + ((int64_t)u.kh * p.cap + ahead) * 128));
+      // the rows two key tiles on, into L2: one lane, one instruction
+      const int ahead = key_first + ((t >> 1) + 2) * kBN;
+      if (tid == 256 && ahead + kBN - 1 <= hi)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                     :: "l"((t & 1 ? p.v8 : p.k8) + ((int64_t)u.kh * p.cap + ahead) * 128),
+                        "n"(kBN * 128) : "memory");
       const float unit = t & 1 ? unit_v : unit_k;
       const uint32_t e = (uint32_t)t % kSlots;
       ok = mbar_wait_warp(bar(kBarEmpty + (int)e), (((uint32_t)t / kSlots) & 1u) ^ 1u, abort_flag,
