@@ -826,6 +826,7 @@ int launch_decode_q8(const DecodeQ8Call& c) {
   p.cap = (int)c.cache.max_seq_len;
   p.Hkv = c.Hkv; p.group = divisor(c.H / c.Hkv); p.window = c.window;
   p.block_shift = c.cache.block == 16 ? 4 : c.cache.block == 32 ? 5 : c.cache.block == 64 ? 6 : 7;
+  if (p.T * (c.H / c.Hkv) > (1 << 30)) return kErrShape;
   p.rows = (int)p.T * (c.H / c.Hkv);
   p.scale_log2 = c.scale * 1.4426950408889634f;
   p.err = c.err;

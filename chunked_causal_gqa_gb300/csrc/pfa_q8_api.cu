@@ -99,15 +99,36 @@ struct PrefillPlan {
   Call call;              // on the read-back rows
 };
 
-How prefill_how(int64_t T, int H, int Hkv, int D, int dtype) {
-  if (T * (H / Hkv) <= 64) return How::kDecode;
-  if (dtype == PFA_BF16 && D == 128 && q8_d128_serves(T, H, Hkv)) return How::kCodes;
-  return How::kReadBack;
+// Which of them is fastest, by what bounds it.  The decode kernel's time grows with rows *
+// kv heads (it takes 16 rows at a time, 8 of fp32); the others walk the keys with
+// 128-row tiles in waves of the SMs.  Measured on GB300 (us):
+//   bf16, head_dim 128, 32/8 heads, rows = T * 4:      decode  codes  read back
+//     63488 keys, rows 32 / 64 / 128                 50 / 82 / 144   71 / 70 / 72   120
+//     63488 keys, rows 512 / 768 / 1024 / 2048        123 / 171 / 244 / 434 (codes), 153 / 191 / 235 / 398 (read back)
+//     4096 keys, rows 32 / 128 / 256 / 384           15 / 21 / 33 / 43   21 / 22 / 25 / 26   26 / 25 / 26 / 24
+//   bf16, head_dim 512, 8/2 heads, 16384 keys, rows 256 / 512 / 768:  108 / 202 / 296, read back 224
+//   fp32, head_dim 128, 32/8 heads, 16384 keys, rows 512 / 768:  269 / 398, read back 360
+//   fp32, head_dim 512, 8/2 heads, 8192 keys, rows 256 / 1024:  101 / 366, read back 3456 / 6847
+//     (that attention runs on the CUDA cores)
+How prefill_how(int64_t T, int64_t keys, int H, int Hkv, int D, int dtype, int num_sms) {
+  const int64_t rows = T * (H / Hkv);
+  if (dtype == PFA_BF16 && D == 128) {
+    if (rows <= 48) return How::kDecode;
+    if (rows <= 256 || (rows <= 768 && keys >= 16384))
+      return q8_d128_serves(T, H, Hkv) ? How::kCodes : How::kReadBack;
+    return How::kReadBack;
+  }
+  if (dtype == PFA_F32 && D != 128) return How::kDecode;
+  // A wave of tiles costs what the decode kernel takes for this many rows of one kv head.
+  const int64_t wave = dtype == PFA_F32 ? 5300 : 1150;
+  const int64_t blocks = dtype == PFA_F32 ? (rows + 127) / 128 * Hkv : (rows + 255) / 256 * 4 * Hkv;
+  return rows * Hkv <= wave * ((blocks + num_sms - 1) / num_sms) ? How::kDecode : How::kReadBack;
 }
 
 int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window, float scale,
                  int dtype, int64_t qkv_dim, int num_sms, void* stream, PrefillPlan* p) {
-  p->how = prefill_how(T, H, Hkv, D, dtype);
+  p->how = prefill_how(T, window > 0 ? std::min<int64_t>(start_pos + T, window + T) : start_pos + T,
+                       H, Hkv, D, dtype, num_sms);
   if (p->how == How::kDecode) {
     p->total = decode_q8_workspace(1, T, H, Hkv, D, dtype, num_sms);
     return PFA_OK;
