@@ -174,8 +174,9 @@ struct Cursor {
     stop = stop_;
     e = e_;
     x = entry_of<RM>(p, e);
-    h = (int)((uint32_t)into / (uint32_t)max(x.listed(), 1));
-    piece(into - h * x.listed(), team);
+    // (the clamps matter only if the lengths change under the kernel)
+    h = min((int)((uint32_t)into / (uint32_t)max(x.listed(), 1)), p.Hkv - 1);
+    piece(min(into - h * x.listed(), x.listed()), team);
     if (kend <= k0) next_piece(p, team);
   }
   __device__ __forceinline__ void piece(int first, int team) {
@@ -243,47 +244,68 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before has written its results
 
-  // ---- the list of units, and where this block's run starts in it: thread i has
-  // the entries [i * per, (i + 1) * per)
-  const int per = (p.entries + kThreads - 1) / kThreads;
-  int mine = 0;
-#pragma unroll 1
-  for (int e = tid * per; e < min(p.entries, (tid + 1) * per); ++e) {
-    const Entry x = entry_of<RM>(p, e);
-    mine += x.listed() * p.Hkv;
-    if (x.bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
-  }
-  int up = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, up, o);
-    if (lane >= o) up += v;
-  }
-  if (lane == 31) sm.sums[warp] = up;
-  __syncthreads();
-  int before = up - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm.sums[w];
-    total += sm.sums[w];
-  }
-  const int run = run_of<TEAMS>(total, gridDim.x);
-  const int at = blockIdx.x * run, stop = min(total, at + run);
-  if (at >= total) return;
-  if (before <= at && at < before + mine) {   // one thread
-    int e = tid * per, into = at - before;
-#pragma unroll 1
-    for (;; ++e) {
-      const int n = entry_of<RM>(p, e).listed() * p.Hkv;
-      if (into < n || e + 1 >= min(p.entries, (tid + 1) * per)) break;
-      into -= n;
+  // ---- the list of units, and where this block's run starts in it
+  int at, stop, first_entry, into;
+  if (p.entries <= 32) {   // each warp for itself, an entry a lane
+    const Entry x = entry_of<RM>(p, min(lane, p.entries - 1));
+    const int mine = lane < p.entries ? x.listed() * p.Hkv : 0;
+    if (x.bad && blockIdx.x == 0 && warp == 0) atomicOr(p.err, kErrLengths);
+    int up = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += v;
     }
-    sm.first_entry = e;
-    sm.into = into;
+    const int total = __shfl_sync(0xffffffffu, up, 31);
+    const int run = run_of<TEAMS>(total, gridDim.x);
+    at = blockIdx.x * run;
+    stop = min(total, at + run);
+    if (at >= total) return;
+    first_entry = __ffs(__ballot_sync(0xffffffffu, at < up)) - 1;
+    into = at - __shfl_sync(0xffffffffu, up - mine, first_entry);
+  } else {   // thread i has the entries [i * per, (i + 1) * per)
+    const int per = (p.entries + kThreads - 1) / kThreads;
+    int mine = 0;
+#pragma unroll 1
+    for (int e = tid * per; e < min(p.entries, (tid + 1) * per); ++e) {
+      const Entry x = entry_of<RM>(p, e);
+      mine += x.listed() * p.Hkv;
+      if (x.bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
+    }
+    int up = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += v;
+    }
+    if (lane == 31) sm.sums[warp] = up;
+    __syncthreads();
+    int before = up - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm.sums[w];
+      total += sm.sums[w];
+    }
+    const int run = run_of<TEAMS>(total, gridDim.x);
+    at = blockIdx.x * run;
+    stop = min(total, at + run);
+    if (at >= total) return;
+    if (before <= at && at < before + mine) {   // one thread
+      int e = tid * per, rest = at - before;
+#pragma unroll 1
+      for (;; ++e) {
+        const int n = entry_of<RM>(p, e).listed() * p.Hkv;
+        if (rest < n || e + 1 >= min(p.entries, (tid + 1) * per)) break;
+        rest -= n;
+      }
+      sm.first_entry = e;
+      sm.into = rest;
+    }
+    __syncthreads();
+    first_entry = sm.first_entry;
+    into = sm.into;
   }
-  __syncthreads();
 
   Cursor<RM, TEAMS> in, cu;   // copies, products
-  in.start(p, at, stop, sm.first_entry, sm.into, team);
+  in.start(p, at, stop, first_entry, into, team);
   cu = in;
 
   // Query rows of a piece as they are stored, this warp's columns: the lane's 32
@@ -641,16 +663,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 }
 
 // One block for each row and 128 columns: joins the parts of its head, and
-// writes the zeros of rows that see nothing.  Four groups of threads take every
-// fourth part in the blocks' order, each with a running maximum.
-constexpr int kJoinThreads = 128;
-
-template <typename E, int NW>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int blocks) {
+// writes the zeros of rows that see nothing.  GROUPS warps take the parts in turn,
+// in the blocks' order, each with a running maximum.
+template <typename E, int NW, int GROUPS>
+__global__ void __launch_bounds__(GROUPS * 32) join_kernel(const Params p, int blocks) {
   constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = sizeof(E) == 4 ? 8 : 16;
-  __shared__ float4 s_sum[3][32];
-  __shared__ float2 s_ml[4];
-  __shared__ int s_units[4][2];
+  __shared__ float4 s_sum[GROUPS - 1][32];
+  __shared__ float2 s_ml[GROUPS];
+  __shared__ int s_units[GROUPS][2];
   const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
   const int id = blockIdx.x / NW, d = blockIdx.x % NW * 128 + lane * 4;
   const int eh = id / p.joined, r = id - eh * (int)p.joined.by;
@@ -659,7 +679,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
   // the list of units, as the first kernel counts it
   int before = 0, total = 0;
 #pragma unroll 1
-  for (int i = tid; i < p.entries; i += kJoinThreads) {
+  for (int i = tid; i < p.entries; i += GROUPS * 32) {
     const int n = entry_of<RM>(p, i).listed() * p.Hkv;
     total += n;
     if (i < e) before += n;
@@ -673,8 +693,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
     s_units[grp][1] = total;
   }
   __syncthreads();
-  before = s_units[0][0] + s_units[1][0] + s_units[2][0] + s_units[3][0];
-  total = s_units[0][1] + s_units[1][1] + s_units[2][1] + s_units[3][1];
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < GROUPS; ++w) {
+    before += s_units[w][0];
+    total += s_units[w][1];
+  }
   const Entry x = entry_of<RM>(p, e);
   const int run = run_of<TEAMS>(total, blocks);
   const int s0 = before + h * x.listed();
@@ -698,12 +722,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
   float mx = -INFINITY, l = 0.f;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int i0 = grp; i0 < n; i0 += 32) {
-    float4 v[8];
-    float2 ml[8];
+  for (int i0 = grp; i0 < n; i0 += 6 * GROUPS) {
+    float4 v[6];
+    float2 ml[6];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = i0 + 4 * j;
+    for (int j = 0; j < 6; ++j) {
+      const int i = i0 + GROUPS * j;
       ml[j] = make_float2(-INFINITY, 0.f);
       v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
@@ -715,14 +739,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
     }
     float m = mx;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, ml[j].x);
+    for (int j = 0; j < 6; ++j) m = fmaxf(m, ml[j].x);
     const float base = m == -INFINITY ? 0.f : m;
     const float a = exp2_fast(mx - base);
     mx = m;
     l *= a;
     sum.x *= a; sum.y *= a; sum.z *= a; sum.w *= a;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 6; ++j) {
       const float f = exp2_fast(ml[j].x - base);
       l = fmaf(ml[j].y, f, l);
       sum.x = fmaf(v[j].x, f, sum.x); sum.y = fmaf(v[j].y, f, sum.y);
@@ -735,13 +759,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
   if (grp > 0) return;
   float m = mx;
 #pragma unroll
-  for (int w = 1; w < 4; ++w) m = fmaxf(m, s_ml[w].x);
+  for (int w = 1; w < GROUPS; ++w) m = fmaxf(m, s_ml[w].x);
   const float base = m == -INFINITY ? 0.f : m;
   const float a = exp2_fast(mx - base);
   l *= a;
   sum.x *= a; sum.y *= a; sum.z *= a; sum.w *= a;
 #pragma unroll
-  for (int w = 1; w < 4; ++w) {
+  for (int w = 1; w < GROUPS; ++w) {
     const float f = exp2_fast(s_ml[w].x - base);
     const float4 v = s_sum[w - 1][lane];
     l = fmaf(s_ml[w].y, f, l);
@@ -795,10 +819,15 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
       cfg.dynamicSmemBytes = sizeof(Shared);
       cudaError_t err = cudaLaunchKernelEx(&cfg, decode_kernel<E, NW>, (const Params)p);
       if (err == cudaSuccess) {
+        // a head has about blocks / heads parts: eight warps for many of them; with many
+        // heads two, so that the blocks are quickly through (32 sequences of 8 heads:
+        // 49.7 us for both kernels with eight, 47.6 with two)
+        const bool many = (int64_t)p.entries * p.Hkv * 8 <= blocks;
         cfg.gridDim = dim3((unsigned)joins);
-        cfg.blockDim = dim3(kJoinThreads);
+        cfg.blockDim = dim3(many ? 256 : 64);
         cfg.dynamicSmemBytes = 0;
-        err = cudaLaunchKernelEx(&cfg, join_kernel<E, NW>, (const Params)p, blocks);
+        err = many ? cudaLaunchKernelEx(&cfg, join_kernel<E, NW, 8>, (const Params)p, blocks)
+                   : cudaLaunchKernelEx(&cfg, join_kernel<E, NW, 2>, (const Params)p, blocks);
       }
       if (err != cudaSuccess) {
         cudaGetLastError();
