@@ -53,7 +53,7 @@ constexpr int kMaxEntries = 1 << 14;           // (sequence, row tile) pairs of 
 constexpr int64_t kMaxUnits = 1 << 30;         // units that a launch can list
 constexpr int kJoinBytes = kWarps * 8 * 128 * 4;  // joins: 8 row sums of 128 floats for each warp
 // What the start and end of a head cost a block, in units: its query rows, the join.
-constexpr int kHeadCost = 4;
+constexpr int kHeadCost = 8;
 constexpr float kWeightScale = 16384.f;
 
 struct Params {

@@ -387,7 +387,103 @@ def test_decode_workspace():
     ok()
 
 
+def test_decode_of_more_sequences_than_one_launch_lists():
+    """17000 short sequences (two launches), against 64 bits all at once."""
+    B, H, D, cap = 17000, 2, 128, 16
+    cache = pkg.Q8Cache(*R.make_cache(1, cap, D, 16, batch=B, seed=2, device=G.dev()))
+    q = randn((B, 1, H, D), BF16, 3, 2.0)
+    n = torch.randint(0, cap + 1, (B,), generator=torch.Generator().manual_seed(4)).to(G.dev())
+    out = pkg.decode_attention_q8(q, cache, n)
+    k, v = R.values(cache.k, cache.k_scale)[:, 0], R.values(cache.v, cache.v_scale)[:, 0]
+    s = (q[:, 0].double() @ k.transpose(1, 2)) * R.default_scale(D)
+    hidden = torch.arange(cap, device=G.dev()) >= n[:, None, None]
+    p = torch.softmax(s.masked_fill(hidden, float("-inf")), -1).nan_to_num(0.0)
+    want, a = p @ v, p @ v.abs()
+    # half a step, the weights' 2^-11 (see attention()), scores of up to a few hundred off by
+    # 10 * 2^-22 of their terms
+    size = (q[:, 0].double().abs() @ k.abs().transpose(1, 2)).amax(-1, keepdim=True) * R.default_scale(D)
+    within(out[:, 0], want, 2.0 ** -8 * want.abs() + a * (2.0 ** -11 + 2.0 ** -20 + 2 * size * 10 * 2.0 ** -22)
+           + 2.0 ** -39 * 30 * 16 * cache.v_scale.max().item())
+    ok()
+
+
 # ------------------------------------------------------------------ chunks
+
+def test_prefill_of_more_row_tiles_than_one_launch_lists():
+    T, H, D = 1100, 128, 512                              # 17600 tiles of 8 rows
+    cache = pkg.Q8Cache(*R.make_cache(1, 1152, D, 64, seed=3, device=G.dev(), dead=[T]))
+    q = randn((T, H, D), F32, 4, 1.0)
+    out = pkg.prefill_attention_q8(q, cache, start_pos=0)
+    heads = [0, 77, 127]
+    want, tol = R.attention(q[:, heads], cache, T, 0, R.default_scale(D), F32)
+    within(out[:, heads], want, tol)
+    ok()
+
+
+@pytest.mark.parametrize("T", [8, 60, 300])
+def test_prefill_in_a_graph(T):
+    H, Hkv, D, cap = 8, 2, 128, 1024                      # decode kernel, codes, read back
+    cache = pkg.Q8Cache(*R.make_cache(Hkv, cap, D, 64, seed=3, device=G.dev()))
+    q = randn((T, H, D), BF16, 1)
+    want = pkg.prefill_attention_q8(q, cache, start_pos=cap - T).clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = pkg.prefill_attention_q8(q, cache, start_pos=cap - T)
+    q2 = randn((T, H, D), BF16, 2)
+    for x in (q2, q.clone()):
+        q.copy_(x)
+        graph.replay()
+    ok()
+    assert torch.equal(out, want)
+
+
+def test_prefill_from_the_codes_reports_a_wait_that_runs_out():
+    H, Hkv, D, cap, T = 8, 2, 128, 1024, 60
+    cache = pkg.Q8Cache(*R.make_cache(Hkv, cap, D, 64, seed=3, device=G.dev()))
+    q = randn((T, H, D), BF16, 1)
+    want = pkg.prefill_attention_q8(q, cache, start_pos=cap - T)
+    ok()
+    pkg.debug_configure(wait_limit_ms=50.0, force_timeout=True)
+    try:
+        pkg.prefill_attention_q8(q, cache, start_pos=cap - T)
+        status = pkg.last_device_error()
+    finally:
+        pkg.debug_configure(0.0, False)
+    assert status == -7, pkg.status_string(status)
+    assert torch.equal(want, pkg.prefill_attention_q8(q, cache, start_pos=cap - T))
+    ok()
+
+
+PREFILL = [  # T, start_pos, H, Hkv, block, window, scale: chunks from the codes
+    (14, 0, 8, 2, 16, 0, None), (40, 3000, 8, 2, 16, 0, None), (33, 2999, 12, 2, 32, 130, None),
+    (50, 700, 5, 1, 128, 0, None), (2, 900, 128, 1, 64, 0, None), (64, 0, 6, 2, 64, 20, None),
+    (50, 1000, 8, 2, 64, 0, -0.07), (50, 1000, 8, 2, 64, 0, 0.0), (17, 40000, 8, 2, 64, 0, None),
+    (190, 20000, 32, 8, 64, 0, None), (2, 500, 100, 1, 16, 7, None),
+]
+
+
+@pytest.mark.parametrize("case", PREFILL, ids=str)
+def test_prefill_from_the_codes(case):
+    T, sp, H, Hkv, block, window, scale = case
+    n, D = sp + T, 128
+    cap = -(-n // block) * block + block
+    cache = R.make_cache(Hkv, cap, D, block, seed=T, device=G.dev(), dead=[n])
+    k, v, ks, vs = (t.view(torch.uint8) if t.dtype == F8 else t for t in cache)
+    lo = max(0, sp - window + 1) if window else 0
+    k[:, :lo], v[:, :lo] = 0x7f, 0xff                     # NaN in front of every window
+    cache = pkg.Q8Cache(k.view(F8), v.view(F8), ks, vs)
+    q = randn((T, H, D), BF16, T + 1, 2.0)
+    out = pkg.prefill_attention_q8(q, cache, start_pos=sp, window=window, scale=scale)
+    live = pkg.Q8Cache(*(t.view(torch.uint8).clone().view(F8) for t in (k, v)), ks, vs)
+    for t in (live.k, live.v):
+        t.view(torch.uint8)[:, :lo] = 0
+    want, tol = R.attention(q, live, n, window, R.default_scale(D) if scale is None else scale, BF16)
+    # beside attention()'s terms: weights up to 2^8 where the exponent's base lags, so small ones
+    # round to 2^-25 of a weight of 1, times the largest V
+    vmax = R.values(live.v, vs)[:, lo:n].abs().nan_to_num(0.0).amax().item()
+    within(out, want, tol + (n - lo) * 2.0 ** -25 * vmax, f"T {T}")
+    assert torch.equal(out, pkg.prefill_attention_q8(q, cache, start_pos=sp, window=window, scale=scale))
+    ok()
 
 @pytest.mark.parametrize("dt", [BF16, F32])
 @pytest.mark.parametrize("D", [128, 512])
