@@ -26,7 +26,7 @@
 //
 // Warps: 0-3 and 4-7 softmax of tiles A and B, 8-11 converters, 12 TMEM and MMA
 // issue; 16 warps are launched with 128 registers a thread and split them
-// 184 / 184 / 88 / 56 by warpgroup (512 = 4 * 128).
+// 200 / 200 / 72 / 40 by warpgroup (512 = 4 * 128).
 #include "pfa_internal.h"
 #include "pfa_ptx.cuh"
 #include "pfa_q8.cuh"
@@ -127,6 +127,26 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Two floats in a register pair, one instruction for both.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void split_pair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 q8_d128_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -197,7 +217,7 @@ q8_d128_kernel(const __grid_constant__ Params p) {
   }
 
   if (warp >= 12) {
-    registers_down<56>();
+    registers_down<40>();
     if (warp == 12) {
       // ---------------------------------------------------------- MMA issue (whole warp)
       const uint32_t tSA = tmem + 0, tSB = tmem + 128, tOA = tmem + 256, tOB = tmem + 384;
@@ -248,7 +268,7 @@ q8_d128_kernel(const __grid_constant__ Params p) {
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ converters
-    registers_down<88>();
+    registers_down<72>();
     // A warp has 32 rows of the tile, eight at a time: lane l row l % 8 and, of the row's
     // eight pieces of 16 codes, piece l / 8 of the first half or of the second (load 2 g + half).
     // Eight lanes with eight rows and one chunk fill all chunks of the swizzle.
@@ -332,7 +352,7 @@ q8_d128_kernel(const __grid_constant__ Params p) {
     }
   } else {
     // ------------------------------------------------------------ softmax
-    registers_up<184>();
+    registers_up<200>();
     const int X = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
     const int tok = row / p.group, hrow = row - tok * (int)p.group.by;
     const int t0 = u.t0 + X * p.tok_per_tile;
@@ -443,18 +463,21 @@ q8_d128_kernel(const __grid_constant__ Params p) {
       }
       const float base = m_run == -INFINITY ? 0.f : m_run;
       uint32_t pk0[32], pk1[32];
-      float ls[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ls[k] = 0.f;
+      const uint64_t cc = pair_of(c, c), bb = pair_of(-base, -base);
+      uint64_t ls[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < 64; ++k) {
-        const float a = ex2(fmaf(x[2 * k], c, -base)), b = ex2(fmaf(x[2 * k + 1], c, -base));
+        float a, b;
+        split_pair(fma_pair(pair_of(x[2 * k], x[2 * k + 1]), cc, bb), a, b);
+        a = ex2(a);
+        b = ex2(b);
         const uint32_t w = pack_half2(a, b);
         if (k < 32) pk0[k] = w; else pk1[k - 32] = w;
-        ls[(2 * k) & 7] += a;
-        ls[(2 * k + 1) & 7] += b;
+        ls[k & 3] = add_pair(ls[k & 3], pair_of(a, b));
       }
-      l = l * alpha + (((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7])));
+      float s0, s1;
+      split_pair(add_pair(add_pair(ls[0], ls[1]), add_pair(ls[2], ls[3])), s0, s1);
+      l = l * alpha + (s0 + s1);
       // the commit that signalled these scores covers the last product into O
       if (__any_sync(0xffffffffu, rescale)) {
         const float f = rescale ? alpha : 1.f;
