@@ -29,16 +29,14 @@ struct Side {               // the queries or the keys
   void* out;
   const void* weight;
   int64_t in_row, out_row, out_head;
-  Divisor heads;
-  int rows, block_rows;     // tokens * heads; rows of a block
 };
 struct Params {
-  Side side[2];
-  int q_blocks;             // blocks of the queries, in front of the keys'
+  Side q, k;
   const double* inv_freq;
   const int64_t* lengths;
   int64_t start_pos;
-  Divisor T;
+  Divisor heads, T;         // H + Hkv
+  int H, rows, block_rows;  // tokens * heads; rows of a block
   int D, rot, interleaved;
   float eps, offset, inv_dim;   // 1 / D
 };
@@ -85,6 +83,9 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
   return of_bits(v);
 }
 
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
 // A lane's sixteen elements as they are stored: pieces of 16 bytes.
 template <typename E>
 struct Raw {
@@ -111,52 +112,54 @@ __device__ __forceinline__ void store_pieces(__nv_bfloat16* p, int stride, const
   store8(p + stride, reinterpret_cast<const float*>(y + 4));
 }
 
-// A block takes block_rows = ROWS * kThreads / width consecutive head rows of the
-// queries or of the keys (in the order of tokens, then heads).  `width` lanes, a
-// power of two, share a row; a lane owns 16 elements, whose 16-byte pieces lie
-// side by side with the other lanes'.  Of a head's rot / 16 lanes that rotate, lane l has
-// the pieces l + m * rot / 16 of the first rot elements: for pairs (i, i + rot / 2) the
-// second half of its pieces are the partners of the first.  All of a block's rows are
-// asked for before the cosines of its tokens are computed, once for all heads.
-template <typename E, int ROWS>
+// A block takes block_rows consecutive head rows (in the order of tokens, then query
+// heads, then key heads), kThreads / width at a time, the next ones on their way.  `width`
+// lanes, a power of two, share a row; a lane owns 16 elements, whose 16-byte pieces
+// lie side by side with the other lanes'.  Of a head's rot / 16 lanes that rotate, lane l
+// has the pieces l + m * rot / 16 of the first rot elements: for pairs (i, i + rot / 2) the
+// second half of its pieces are the partners of the first.  A block's cosines are computed
+// once for all heads of its tokens, while its first rows arrive.
+// SHIFT: log2 of width where it is known (head_dim 128: 3, 512: 5), or -1.
+template <typename E, int SHIFT, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_constant__ Params p) {
-  extern __shared__ __align__(16) float table[];
+  extern __shared__ __align__(16) float smem[];
+  float* gain = smem;                // weight + offset of q, then of k
+  float* table = smem + 2 * p.D;
   asm volatile("griddepcontrol.launch_dependents;");
-  const bool isk = (int)blockIdx.x >= p.q_blocks;
-  const Side& side = p.side[isk ? 1 : 0];
   constexpr int V = Raw<E>::V;
-  const int lanes = p.D / 16, turned = p.rot / 16;
-  const int shift = lanes <= 1 ? 0 : 32 - __clz(lanes - 1);   // width = 1 << shift
+  const int lanes = SHIFT >= 0 ? 1 << SHIFT : p.D / 16, turned = p.rot / 16;
+  const int shift = SHIFT >= 0 ? SHIFT : lanes <= 1 ? 0 : 32 - __clz(lanes - 1);
   const int lane = threadIdx.x & ((1 << shift) - 1);
   const int at = lane < turned ? V * lane : p.rot + V * (lane - turned);
   const int stride = V * (lane < turned ? turned : lanes - turned);
-  const int row0 = ((int)blockIdx.x - (isk ? p.q_blocks : 0)) * side.block_rows;
-  const int row_end = min(side.rows, row0 + side.block_rows);
-  const int n0 = row0 / side.heads, tokens = (row_end - 1) / side.heads - n0 + 1;
+  const int row0 = blockIdx.x * p.block_rows;
+  const int row_end = min(p.rows, row0 + p.block_rows);
+  const int n0 = row0 / p.heads, tokens = (row_end - 1) / p.heads - n0 + 1;
   const int step = kThreads >> shift, mine = row0 + (threadIdx.x >> shift);
-  const bool on = lane < lanes;
+  const bool on = SHIFT >= 0 || lane < lanes;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  Raw<E> x[ROWS], w;
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int row = mine + i * step;
-    x[i] = {};
+  Raw<E> next = {};
+  auto load = [&](int row) {
     if (on && row < row_end) {
-      const int n = row / side.heads, h = row - n * (int)side.heads.by;
-      x[i].load((const E*)side.in + n * side.in_row + h * p.D + at, stride);
+      const int n = row / p.heads, h = row - n * (int)p.heads.by;
+      const E* src = h < p.H ? (const E*)p.q.in + n * p.q.in_row + h * p.D
+                             : (const E*)p.k.in + n * p.k.in_row + (h - p.H) * p.D;
+      next.load(src + at, stride);
     }
-  }
-  w = {};
-  const bool norm = side.weight != nullptr;
-  if (on && norm) w.load((const E*)side.weight + at, stride);
+  };
+  load(mine);
   auto position = [&](int n) -> int64_t {
     if (!p.lengths) return p.start_pos + n;
     const int s = n / p.T;
     return p.lengths[s] - (int)p.T.by + (n - s * (int)p.T.by);
   };
+  for (int i = threadIdx.x; i < 2 * p.D; i += kThreads) {
+    const E* w = (const E*)(i < p.D ? p.q.weight : p.k.weight);
+    gain[i] = w ? to_float(w[i < p.D ? i : i - p.D]) + p.offset : 1.f;
+  }
   // a lane's pairs 2 i and 2 i + 1 at [i][lane]: {cos, cos, sin, sin}; a piece has `in` pairs
-  const int in = p.interleaved ? V / 2 : V;
+  constexpr int in = NEIGHBOURS ? V / 2 : V;
   const int pairs = p.rot / 2;
   if (pairs > 0) {   // a thread has one pair of every `apart`-th token
     const int apart = (int)((uint32_t)kThreads / (uint32_t)pairs);
@@ -175,110 +178,123 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_con
       }
     }
   }
-  F2 g[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const F2 v = w.pair(j);
-    g[j] = norm ? F2{v.x + p.offset, v.y + p.offset} : F2{1.f, 1.f};
-  }
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int row = mine + i * step;
+#pragma unroll 1
+  for (int first = row0; first < row_end; first += step) {   // of the block's threads together
+    const int row = first + (threadIdx.x >> shift);
     F2 y[8], sum = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      y[j] = x[i].pair(j);
+      y[j] = next.pair(j);
       sum = fma(y[j], y[j], sum);
     }
+    load(row + step);
     float ss = sum.x + sum.y;
-    for (int o = (1 << shift) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!on || row >= row_end) continue;
-    const int n = row / side.heads, h = row - n * (int)side.heads.by;
-    if (norm) {
-      const float r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
+    if constexpr (SHIFT >= 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = mul(mul(y[j], F2{r, r}), g[j]);
+      for (int o = (1 << SHIFT) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    } else {
+      for (int o = (1 << shift) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
-    if (lane < turned) {
-      const float4* cs = reinterpret_cast<const float4*>(table + (n - n0) * p.rot) + lane;
+    if (on && row < row_end) {
+      const int n = row / p.heads, h = row - n * (int)p.heads.by;
+      const bool isq = h < p.H;
+      if ((isq ? p.q.weight : p.k.weight) != nullptr) {
+        const float r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
+        const float4* g = reinterpret_cast<const float4*>(gain + (isq ? 0 : p.D) + at);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {   // pairs 2 j and 2 j + 1 of the lane
-        const float4 t = cs[j * turned];
-        const F2 c = {t.x, t.y}, s = {t.z, t.w}, ns = {-t.z, -t.w};
-        if (p.interleaved) {
-          const F2 u = {y[2 * j].x, y[2 * j + 1].x}, v = {y[2 * j].y, y[2 * j + 1].y};
-          const F2 re = fma(u, c, mul(v, ns)), im = fma(u, s, mul(v, c));
-          y[2 * j] = {re.x, im.x};
-          y[2 * j + 1] = {re.y, im.y};
-        } else {
-          const F2 u = y[j], v = y[j + 4];
-          y[j] = fma(u, c, mul(v, ns));
-          y[j + 4] = fma(u, s, mul(v, c));
+        for (int j = 0; j < 4; ++j) {   // four elements: V / 4 to a piece
+          const float4 v = g[(j / (V / 4)) * (stride / 4) + j % (V / 4)];
+          y[2 * j] = mul(mul(y[2 * j], F2{r, r}), F2{v.x, v.y});
+          y[2 * j + 1] = mul(mul(y[2 * j + 1], F2{r, r}), F2{v.z, v.w});
         }
       }
-    }
-    if (p.lengths && position(n) < 0) {  // padding in front
+      if (lane < turned) {
+        const float4* cs = reinterpret_cast<const float4*>(table + (n - n0) * p.rot) + lane;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = {0.f, 0.f};
+        for (int j = 0; j < 4; ++j) {   // pairs 2 j and 2 j + 1 of the lane
+          const float4 t = cs[j * turned];
+          const F2 c = {t.x, t.y}, s = {t.z, t.w}, ns = {-t.z, -t.w};
+          if constexpr (NEIGHBOURS) {
+            const F2 u = {y[2 * j].x, y[2 * j + 1].x}, v = {y[2 * j].y, y[2 * j + 1].y};
+            const F2 re = fma(u, c, mul(v, ns)), im = fma(u, s, mul(v, c));
+            y[2 * j] = {re.x, im.x};
+            y[2 * j + 1] = {re.y, im.y};
+          } else {
+            const F2 u = y[j], v = y[j + 4];
+            y[j] = fma(u, c, mul(v, ns));
+            y[j + 4] = fma(u, s, mul(v, c));
+          }
+        }
+      }
+      if (p.lengths && position(n) < 0) {  // padding in front
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = {0.f, 0.f};
+      }
+      E* dst = isq ? (E*)p.q.out + n * p.q.out_row + h * p.D
+                   : (E*)p.k.out + n * p.k.out_row + (h - p.H) * p.k.out_head;
+      store_pieces(dst + at, stride, y);
     }
-    store_pieces((E*)side.out + n * side.out_row + h * side.out_head + at, stride, y);
   }
 }
 
-template <typename E, int ROWS>
-cudaError_t launch(Params p, int width, cudaStream_t stream) {
-  int blocks[2], tokens = 0;
-  for (int i = 0; i < 2; ++i) {
-    Side& s = p.side[i];
-    const int64_t heads = s.heads.by;
-    int64_t n = ROWS * kThreads / width;
-    // the table holds the tokens that a block's rows can touch
-    if (p.rot > 0) n = std::min<int64_t>(n, (kTableBytes / (p.rot * (int64_t)sizeof(float)) - 1) * heads + 1);
-    s.block_rows = (int)n;
-    blocks[i] = (int)((s.rows + n - 1) / n);
-    tokens = std::max<int>(tokens, (int)((n - 1 + heads - 1) / heads) + 1);
-  }
-  p.q_blocks = blocks[0];
+template <typename E, int SHIFT, bool NEIGHBOURS>
+cudaError_t launch(Params p, int num_sms, cudaStream_t stream) {
+  int width = 1;
+  while (width < p.D / 16) width *= 2;
+  const int step = kThreads / width;
+  // as many turns as bring all rows into one wave of four blocks an SM
+  const int64_t turns = ((int64_t)p.rows + step - 1) / step, blocks = (int64_t)num_sms * 4;
+  int64_t n = (turns + blocks - 1) / blocks * step;
+  // the table holds the tokens that a block's rows can touch
+  const int64_t heads = p.heads.by;
+  if (p.rot > 0) n = std::min<int64_t>(n, (kTableBytes / (p.rot * (int64_t)sizeof(float)) - 1) * heads + 1);
+  p.block_rows = (int)n;
+  const int64_t tokens = (n - 1 + heads - 1) / heads + 1;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks[0] + blocks[1]));
+  cfg.gridDim = dim3((unsigned)((p.rows + n - 1) / n));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)tokens * p.rot * sizeof(float);
+  cfg.dynamicSmemBytes = (size_t)(tokens * p.rot + 2 * p.D) * sizeof(float);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<E, ROWS>, (const Params)p);
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<E, SHIFT, NEIGHBOURS>, (const Params)p);
+}
+
+template <typename E>
+cudaError_t launch(const Params& p, int num_sms, cudaStream_t stream) {
+  if (p.interleaved)
+    return p.D == 128   ? launch<E, 3, true>(p, num_sms, stream)
+           : p.D == 512 ? launch<E, 5, true>(p, num_sms, stream)
+                        : launch<E, -1, true>(p, num_sms, stream);
+  return p.D == 128   ? launch<E, 3, false>(p, num_sms, stream)
+         : p.D == 512 ? launch<E, 5, false>(p, num_sms, stream)
+                      : launch<E, -1, false>(p, num_sms, stream);
 }
 
 }  // namespace
 
 int launch_norm_rope(const NormRopeCall& c) {
   const int64_t tokens = c.span.B * c.span.T, rows = tokens * (c.H + c.Hkv);
-  if (rows > 0x7fffffff - 65536) return kErrShape;
+  if (rows > 0x7fffffff - (1 << 22)) return kErrShape;
   Params p;
-  p.side[0] = Side{c.q, c.q_out, c.q_weight, c.q_row, c.q_out_row, c.D, divisor(c.H),
-                   (int)(tokens * c.H), 0};
-  p.side[1] = Side{c.k, c.k_out, c.k_weight, c.k_row, c.k_out_row, c.k_out_head, divisor(c.Hkv),
-                   (int)(tokens * c.Hkv), 0};
+  p.q = Side{c.q, c.q_out, c.q_weight, c.q_row, c.q_out_row, c.D};
+  p.k = Side{c.k, c.k_out, c.k_weight, c.k_row, c.k_out_row, c.k_out_head};
   p.inv_freq = c.inv_freq;
   p.lengths = c.span.lengths;
   p.start_pos = c.span.start_pos;
+  p.heads = divisor((uint32_t)(c.H + c.Hkv));
   p.T = divisor((uint32_t)c.span.T);
+  p.H = c.H;
+  p.rows = (int)rows;
   p.D = c.D;
   p.rot = c.rot_dim; p.interleaved = c.interleaved;
   p.eps = c.eps; p.offset = c.weight_offset; p.inv_dim = 1.f / (float)c.D;
-  int width = 1;
-  while (width < c.D / 16) width *= 2;
-  // Few rows: one to a lane group, for the shortest chain; many: several in flight.
-  const bool few = rows * width <= (int64_t)c.num_sms * kThreads * 4;
-  cudaError_t e;
-  if (c.dtype == PFA_F32)
-    e = few ? launch<float, 1>(p, width, c.stream) : launch<float, 1>(p, width, c.stream);
-  else
-    e = few ? launch<__nv_bfloat16, 1>(p, width, c.stream) : launch<__nv_bfloat16, 2>(p, width, c.stream);
+  const cudaError_t e = c.dtype == PFA_F32 ? launch<float>(p, c.num_sms, c.stream)
+                                           : launch<__nv_bfloat16>(p, c.num_sms, c.stream);
   if (e == cudaSuccess) return kOk;
   cudaGetLastError();
   return kErrLaunch;
