@@ -554,8 +554,8 @@ q8_d128_kernel(const __grid_constant__ Params p) {
 }
 
 // Joins the parts of a pair in key order: block (e, g) has pair p1 + e and columns
-// 16 g .. 16 g + 15, thread R its row R.
-constexpr int kMergeCols = 16, kMergeAhead = 4;
+// 8 g .. 8 g + 7, thread R its row R.
+constexpr int kMergeCols = 8, kMergeAhead = 8;
 __global__ void __launch_bounds__(kPairRows) q8_merge_kernel(const __grid_constant__ Params p) {
   const int e = blockIdx.x, R = threadIdx.x, X = R / kBM, row = R % kBM;
   const Unit u = unit_of(p.T, p.start_pos, p.Hkv, p.tok_per_tile, p.window, p.units_per_head,
