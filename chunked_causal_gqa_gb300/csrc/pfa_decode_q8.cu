@@ -25,9 +25,10 @@
 // form one list, cut into equal runs, one for each block (two blocks an SM).
 // Four warps take the run's units in turn, each with its own ring of three
 // stages filled by cp.async (no barrier in the loop); their sums join in shared
-// memory where a run leaves a head, while the SM's other block streams on.  What covers a head alone is stored as
-// output, what covers part of it goes to the workspace, and a second kernel,
-// launched so that its start overlaps, joins the parts in order.
+// memory where a run leaves a head, while the SM's other block streams on.  What
+// covers a head alone is stored as output, what covers part of it goes to the
+// workspace, and a second kernel, launched so that its start overlaps, joins the
+// parts in order.
 //
 // head_dim 512: four warps share a unit, each with 128 columns of K and V; the
 // scores' four partial sums are exchanged through shared memory.
@@ -68,7 +69,7 @@ struct Params {
   int cap, Hkv, window, block_shift;
   int rows, entries;          // T * group; entries of this launch
   Divisor group, tiles;       // H / Hkv; row tiles of a sequence in this launch
-  Divisor heads, joined;      // Hkv and min(RM, rows), for the second kernel's grid
+  Divisor heads, joined;      // Hkv, and the second kernel's blocks for a tile's rows
   float scale_log2;
   unsigned* err;
   float* parts;               // workspace: slots of partial sums
@@ -662,24 +663,26 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// One block for each row and 128 columns: joins the parts of its head, and
-// writes the zeros of rows that see nothing.  GROUPS warps take the parts in turn,
-// in the blocks' order, each with a running maximum.
+// A block has 128 columns of one row (GROUPS warps that take the parts in turn, in the
+// blocks' order, each with a running maximum) or, with GROUPS 1, of all rows of a
+// tile, a warp each.  It joins the parts of its head, and writes the zeros of rows
+// that see nothing.
 template <typename E, int NW, int GROUPS>
-__global__ void __launch_bounds__(GROUPS * 32) join_kernel(const Params p, int blocks) {
+__global__ void __launch_bounds__(512) join_kernel(const Params p, int blocks) {
   constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = sizeof(E) == 4 ? 8 : 16;
-  __shared__ float4 s_sum[GROUPS - 1][32];
+  __shared__ float4 s_sum[GROUPS > 1 ? GROUPS - 1 : 1][32];
   __shared__ float2 s_ml[GROUPS];
-  __shared__ int s_units[GROUPS][2];
-  const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
+  __shared__ int s_units[16][2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int grp = warp % GROUPS;
   const int id = blockIdx.x / NW, d = blockIdx.x % NW * 128 + lane * 4;
-  const int eh = id / p.joined, r = id - eh * (int)p.joined.by;
+  const int eh = id / p.joined, r = id - eh * (int)p.joined.by + warp / GROUPS;
   const int e = eh / p.heads, h = eh - e * p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;");
   // the list of units, as the first kernel counts it
   int before = 0, total = 0;
 #pragma unroll 1
-  for (int i = tid; i < p.entries; i += GROUPS * 32) {
+  for (int i = tid; i < p.entries; i += blockDim.x) {
     const int n = entry_of<RM>(p, i).listed() * p.Hkv;
     total += n;
     if (i < e) before += n;
@@ -689,13 +692,12 @@ __global__ void __launch_bounds__(GROUPS * 32) join_kernel(const Params p, int b
     total += __shfl_xor_sync(0xffffffffu, total, o);
   }
   if (lane == 0) {
-    s_units[grp][0] = before;
-    s_units[grp][1] = total;
+    s_units[warp][0] = before;
+    s_units[warp][1] = total;
   }
   __syncthreads();
   before = total = 0;
-#pragma unroll
-  for (int w = 0; w < GROUPS; ++w) {
+  for (int w = 0; w < warps; ++w) {
     before += s_units[w][0];
     total += s_units[w][1];
   }
@@ -753,10 +755,12 @@ __global__ void __launch_bounds__(GROUPS * 32) join_kernel(const Params p, int b
       sum.z = fmaf(v[j].z, f, sum.z); sum.w = fmaf(v[j].w, f, sum.w);
     }
   }
-  if (grp > 0) s_sum[grp - 1][lane] = sum;
-  if (lane == 0) s_ml[grp] = make_float2(mx, l);
-  __syncthreads();
-  if (grp > 0) return;
+  if constexpr (GROUPS > 1) {
+    if (grp > 0) s_sum[grp - 1][lane] = sum;
+    if (lane == 0) s_ml[grp] = make_float2(mx, l);
+    __syncthreads();   // the block has one row: no warp has returned
+    if (grp > 0) return;
+  }
   float m = mx;
 #pragma unroll
   for (int w = 1; w < GROUPS; ++w) m = fmaxf(m, s_ml[w].x);
@@ -794,7 +798,6 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
   const int64_t at_once = tiles_at_once < tiles ? 1 : most / tiles;   // sequences
   p.parts = static_cast<float*>(c.ws);
   p.heads = divisor(p.Hkv);
-  p.joined = divisor(std::min(RM, p.rows));
   // Both kernels may be launched before what is in front of them has ended: they
   // wait (griddepcontrol) before they read what it writes.
   cudaLaunchAttribute attr;
@@ -812,22 +815,23 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
       p.tile0 = tile;
       p.tiles = divisor(here);
       p.entries = (int)std::min(at_once, B - b) * here;
-      const int64_t joins = (int64_t)p.entries * p.Hkv * std::min(RM, p.rows) * NW;
+      // A head has about blocks / heads parts: for many of them eight warps to a row, for
+      // few a warp (32 sequences of 8 heads: 49.7 us for both kernels with eight, 46.3 with one).
+      const int rows = std::min(RM, p.rows);
+      const bool many = (int64_t)p.entries * p.Hkv * 8 <= blocks;
+      p.joined = divisor(many ? rows : 1);
+      const int64_t joins = (int64_t)p.entries * p.Hkv * p.joined.by * NW;
       if (joins > 0x7fffffff) return kErrShape;
       cfg.gridDim = dim3((unsigned)blocks);
       cfg.blockDim = dim3(kThreads);
       cfg.dynamicSmemBytes = sizeof(Shared);
       cudaError_t err = cudaLaunchKernelEx(&cfg, decode_kernel<E, NW>, (const Params)p);
       if (err == cudaSuccess) {
-        // a head has about blocks / heads parts: eight warps for many of them; with many
-        // heads two, so that the blocks are quickly through (32 sequences of 8 heads:
-        // 49.7 us for both kernels with eight, 47.6 with two)
-        const bool many = (int64_t)p.entries * p.Hkv * 8 <= blocks;
         cfg.gridDim = dim3((unsigned)joins);
-        cfg.blockDim = dim3(many ? 256 : 64);
+        cfg.blockDim = dim3(many ? 256 : rows * 32);
         cfg.dynamicSmemBytes = 0;
         err = many ? cudaLaunchKernelEx(&cfg, join_kernel<E, NW, 8>, (const Params)p, blocks)
-                   : cudaLaunchKernelEx(&cfg, join_kernel<E, NW, 2>, (const Params)p, blocks);
+                   : cudaLaunchKernelEx(&cfg, join_kernel<E, NW, 1>, (const Params)p, blocks);
       }
       if (err != cudaSuccess) {
         cudaGetLastError();

@@ -93,6 +93,7 @@ int check_attention(int64_t B, int64_t T, int H, int Hkv, int D, float scale, in
 enum class How { kDecode, kCodes, kReadBack };
 struct PrefillPlan {
   How how;
+  int window;             // 0: none
   size_t total;           // workspace
   int64_t lo, rows;       // kReadBack: cache rows [lo, lo + rows) are visible
   size_t v_at, ws_at;
@@ -127,6 +128,9 @@ How prefill_how(int64_t T, int64_t keys, int H, int Hkv, int D, int dtype, int n
 
 int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window, float scale,
                  int dtype, int64_t qkv_dim, int num_sms, void* stream, PrefillPlan* p) {
+  // a window of all keys is none, and the kernels' 32-bit positions stay in range
+  if (window < 0 || window >= start_pos + T) window = 0;
+  p->window = window;
   p->how = prefill_how(T, window > 0 ? std::min<int64_t>(start_pos + T, window + T) : start_pos + T,
                        H, Hkv, D, dtype, num_sms);
   if (p->how == How::kDecode) {
@@ -378,7 +382,9 @@ int pfa_decode_attention_q8(const void* q, const void* k8, const void* v8, const
   c.q = q; c.out = out;
   c.span = Span{B, T, 0, lengths};
   c.H = num_heads; c.Hkv = num_kv_heads; c.D = head_dim;
-  c.window = window > 0 ? window : 0; c.dtype = dtype; c.scale = scale;
+  // (a window of the whole cache is none, and the kernels' 32-bit positions stay in range)
+  c.window = window > 0 && window < max_seq_len ? window : 0;
+  c.dtype = dtype; c.scale = scale;
   c.q_row = q_stride; c.out_row = out_stride;
   c.err = d.err; c.num_sms = d.num_sms; c.device = d.device;
   c.wait_limit_ns = d.wait_limit_ns; c.flags = d.flags;
@@ -449,7 +455,7 @@ int pfa_prefill_attention_q8(const void* q, const void* k8, const void* v8, cons
     c.q = q; c.out = out; c.cache = cache;
     c.span = Span{1, T, start_pos, nullptr};
     c.H = num_heads; c.Hkv = num_kv_heads; c.D = head_dim;
-    c.window = window > 0 ? window : 0; c.dtype = dtype; c.scale = scale;
+    c.window = plan.window; c.dtype = dtype; c.scale = scale;
     c.q_row = qkv_dim; c.out_row = qkv_dim;
     c.err = d.err; c.num_sms = d.num_sms; c.device = d.device;
     c.wait_limit_ns = d.wait_limit_ns; c.flags = d.flags;

@@ -34,6 +34,7 @@
 #include "../../include/pfa.h"
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 namespace pfa {
@@ -619,12 +620,17 @@ Plan plan_of(int T, int start_pos, int H, int Hkv, int window, int sms) {
   s.p2 = s.pairs - s.p1;
   s.parts = 1;
   if (s.p2 > 0) {
-    // the tail's pairs are the earliest tokens: the fewest keys
-    const Unit u = unit_of(T, start_pos, Hkv, s.tok_per_tile, window, s.units_per_head, s.p1);
-    int64_t best = u.n + kFixedTiles;
-    for (int parts = 2; parts <= std::min(u.n, s.p1 > 0 ? 8 : std::max(8, sms / s.p2)); ++parts) {
+    // every part of every pair has a key tile
+    int least = INT_MAX, most = 0;
+    for (int e = s.p1; e < s.pairs; ++e) {
+      const int n = unit_of(T, start_pos, Hkv, s.tok_per_tile, window, s.units_per_head, e).n;
+      least = std::min(least, n);
+      most = std::max(most, n);
+    }
+    int64_t best = most + kFixedTiles;
+    for (int parts = 2; parts <= std::min(least, s.p1 > 0 ? 8 : std::max(8, sms / s.p2)); ++parts) {
       const int64_t waves = ((int64_t)s.p2 * parts + sms - 1) / sms;
-      const int64_t cost = waves * ((u.n + parts - 1) / parts + kFixedTiles) + kFixedTiles;  // + merge
+      const int64_t cost = waves * ((most + parts - 1) / parts + kFixedTiles) + kFixedTiles;  // + merge
       if (cost < best) {
         best = cost;
         s.parts = parts;

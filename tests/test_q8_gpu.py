@@ -315,6 +315,25 @@ def test_decode_extremes(D, dt):
     ok()
 
 
+@pytest.mark.parametrize("D,dt", [(128, BF16), (128, F32), (512, BF16)])
+def test_the_widest_window_is_none(D, dt):
+    cache = R.make_cache(2, 256, D, 64, batch=3, seed=5, device=G.dev(), dead=[200, 2, 0])
+    cache = pkg.Q8Cache(*cache)
+    q = randn((3, 4, 8, D), dt, 6)
+    d = torch.tensor([200, 2, 0], device=G.dev())
+    want = pkg.decode_attention_q8(q, cache, d)
+    for w in (256, 257, 2 ** 31 - 1):
+        assert torch.equal(want, pkg.decode_attention_q8(q, cache, d, window=w))
+    with pytest.raises(ValueError):
+        pkg.decode_attention_q8(q, cache, d, window=2 ** 31)
+    for T in (3, 50, 190):                     # decode kernel, codes (bf16, 128), read back
+        x = randn((T, 8, D), dt, T)
+        want = pkg.prefill_attention_q8(x, cache.slot(0), start_pos=200 - T)
+        for w in (200, 2 ** 31 - 1):
+            assert torch.equal(want, pkg.prefill_attention_q8(x, cache.slot(0), start_pos=200 - T, window=w))
+    ok()
+
+
 def test_decode_reads_a_cache_of_more_than_four_gigabytes():
     B, Hkv, cap, D, block = 5, 8, 1 << 20, 128, 64
     cache = pkg.q8_cache(Hkv, cap, D, batch=B, block=block)
@@ -458,6 +477,8 @@ PREFILL = [  # T, start_pos, H, Hkv, block, window, scale: chunks from the codes
     (14, 0, 8, 2, 16, 0, None), (40, 3000, 8, 2, 16, 0, None), (33, 2999, 12, 2, 32, 130, None),
     (50, 700, 5, 1, 128, 0, None), (2, 900, 128, 1, 64, 0, None), (64, 0, 6, 2, 64, 20, None),
     (50, 1000, 8, 2, 64, 0, -0.07), (50, 1000, 8, 2, 64, 0, 0.0), (17, 40000, 8, 2, 64, 0, None),
+    # one pair of tiles sees one key tile, the other two: no part without keys
+    (5, 124, 48, 1, 64, 0, None), (5, 252, 48, 1, 64, 100, None),
     (190, 20000, 32, 8, 64, 0, None), (2, 500, 100, 1, 16, 7, None),
 ]
 
