@@ -122,6 +122,12 @@ __device__ __forceinline__ int swizzle(int r) {
   return (((r ^ (r >> 1)) & 1) << 2) | ((r >> 1) & 2) | ((r >> 1) & 1);
 }
 
+// Where column d (a multiple of 4) of a row of the join area is: lanes hold runs of 16
+// columns, 32 apart, and would all write to the same banks.
+__device__ __forceinline__ int join_at(int d, int row) {
+  return d ^ ((((d >> 5) & 3) | ((row & 1) << 2)) << 2);
+}
+
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                :: "r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
@@ -620,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
         float mx = -INFINITY;
         for (int w = 0; w < TEAMS; ++w) mx = fmaxf(mx, sm.ml[w * NW][g + 8 * i].x);
         const float f = exp2_fast(m[i] - (mx == -INFINITY ? 0.f : mx)) * vref / kWeightScale;
-        float* to = join + (team * 8 + g) * D + part * 128 + qd * 32;
+        float* to = join + (team * 8 + g) * D;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -629,7 +635,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               v[j] = (F32 ? o[d + j][c] + o[d + j][c + 2] : o[d + j][2 * i + c]) * f;
-            *reinterpret_cast<float4*>(to + c * 16 + d) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(to + join_at(part * 128 + qd * 32 + c * 16 + d, g)) =
+                make_float4(v[0], v[1], v[2], v[3]);
           }
       }
       __syncthreads();
@@ -637,9 +644,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 #pragma unroll 1
       for (int c = tid; c < rows * (D / 4); c += kThreads) {
         const int rr = c / (D / 4), d = c % (D / 4) * 4, r = rr + 8 * i;
-        float4 sum = *reinterpret_cast<const float4*>(join + rr * D + d);
+        float4 sum = *reinterpret_cast<const float4*>(join + rr * D + join_at(d, rr));
         for (int w = 1; w < TEAMS; ++w) {
-          const float4 v = *reinterpret_cast<const float4*>(join + (w * 8 + rr) * D + d);
+          const float4 v = *reinterpret_cast<const float4*>(join + (w * 8 + rr) * D + join_at(d, rr));
           sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
         }
         float mx = -INFINITY, ls = 0.f;
