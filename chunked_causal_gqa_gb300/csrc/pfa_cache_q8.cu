@@ -6,6 +6,17 @@
 //   rows before the new ones: code <- e4m3(code * s_old / s_new)
 //   new rows:                 code <- e4m3(x / s_new)
 // Rows behind the last new one keep their codes.
+//
+// Both directions move bytes and nothing else.  Measured on GB300, one pass among others:
+//   write 2048 tokens of 8 heads of 128, bf16 (12.6 MB)   4.8 us, 2.6 TB/s (floor 1.9 us:
+//     a launch, the positions, the rows, a reduction and the codes follow one another)
+//   write 1 token of 32 sequences, 8 heads of 128         2.6 us: the same chain
+//   read 63488 rows of 8 heads of 128 as bf16 (390 MB)    57.9 us, 6.7 TB/s (floor 57.4 us)
+//   read 3188 rows of 2 heads of 512 as fp32 (33 MB)      5.6 us, 5.8 TB/s (floor 4.8 us)
+// A block of rows is read once: its elements wait in registers for the maximum (two
+// passes over global memory took 8.5 us for the chunk).  Reading back, a lane makes 16
+// output bytes at a time, so that both sides of a warp's pieces are contiguous (32
+// bytes a lane: 66.0 and 9.3 us).
 #include "pfa_internal.h"
 #include "pfa_ptx.cuh"
 #include "pfa_q8.cuh"

@@ -183,7 +183,6 @@ struct WriteQ8Call {
   int Hkv, D, dtype;
   int64_t k_row, v_row;
   unsigned* err;
-  int num_sms;
   cudaStream_t stream;
 };
 int launch_cache_write_q8(const WriteQ8Call& c);
@@ -194,7 +193,6 @@ struct ReadQ8Call {
   int64_t heads, start, rows;       // heads: B * Hkv blocks of max_seq_len rows
   int64_t out_head;                 // elements from one head's rows to the next in the outputs
   int D, dtype;
-  int num_sms;
   cudaStream_t stream;
 };
 int launch_cache_read_q8(const ReadQ8Call& c);

@@ -11,6 +11,17 @@
 // modulo one turn with an error of position * 2^-64 turns; only its top 32
 // bits are then rounded to float.  (Doubles would do, but the chip runs two
 // of their operations a clock and SM.)
+//
+// Bound by HBM's bytes, each element read and written once.  What costs beside them
+// is the start: the first rows come after a launch and a DRAM latency, and the
+// cosines (some 100 instructions a pair) are computed under that latency, once
+// for all heads of a token.  Measured on GB300, one pass among others:
+//   2048 tokens, 32/8 heads of 128, bf16 (42 MB)      10.1 us, 4.1 TB/s (floor 6.2 us)
+//   1358 tokens, 8/2 heads of 512, fp32 (56 MB)       9.8 us, 5.7 TB/s (floor 8.2 us)
+//   8 tokens, 32/8 heads of 128, bf16                 2.6 us: a launch and three latencies
+// Tried: each lane's 16 elements contiguous (fp32 15.2 us: half of every 32-byte
+// sector at a time); two rows ahead instead of one (11.0 / 11.4 us at 64 registers,
+// 10.0 / 10.2 with three blocks an SM).
 #include "pfa_internal.h"
 #include "pfa_q8.cuh"
 

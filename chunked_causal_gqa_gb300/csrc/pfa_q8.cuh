@@ -1,5 +1,5 @@
 // pfa_q8.cuh -- device helpers of the operators around the 8-bit cache: e4m3
-// conversions, the block scale, vector loads of either element type.
+// conversions, the block scale, division by numbers that the host knows.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -68,26 +68,7 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= 3.402823466e38f ? a : 0.f;  // NaN and infinity take no part in a scale
 }
 
-// Eight consecutive elements as floats (16-byte aligned).
-__device__ __forceinline__ void load8(const float* p, float* f) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void store8(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
-}
+// Eight floats -> eight consecutive bf16 (16-byte aligned).
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
   uint32_t w[4];
 #pragma unroll

@@ -278,7 +278,7 @@ int pfa_cache_write_q8(const void* k, const void* v, void* k8, void* v8, float* 
   c.span = Span{B, T, start_pos, lengths};
   c.Hkv = num_kv_heads; c.D = head_dim; c.dtype = dtype;
   c.k_row = k_stride; c.v_row = v_stride;
-  c.err = d.err; c.num_sms = d.num_sms;
+  c.err = d.err;
   c.stream = static_cast<cudaStream_t>(stream);
   return launch_cache_write_q8(c);
 }
@@ -315,7 +315,6 @@ int pfa_cache_read_q8(const void* k8, const void* v8, const float* k_scale, cons
   c.k_out = k_out; c.v_out = v_out;
   c.heads = heads; c.start = start; c.rows = rows; c.out_head = out_head_stride;
   c.D = head_dim; c.dtype = dtype;
-  c.num_sms = d.num_sms;
   c.stream = static_cast<cudaStream_t>(stream);
   return launch_cache_read_q8(c);
 }
@@ -469,7 +468,7 @@ int pfa_prefill_attention_q8(const void* q, const void* k8, const void* v8, cons
   r.k_out = base; r.v_out = base + plan.v_at;
   r.heads = num_kv_heads; r.start = plan.lo; r.rows = plan.rows;
   r.out_head = plan.rows * head_dim;
-  r.D = head_dim; r.dtype = dtype; r.num_sms = d.num_sms;
+  r.D = head_dim; r.dtype = dtype;
   r.stream = static_cast<cudaStream_t>(stream);
   if ((rc = launch_cache_read_q8(r)) != kOk) return rc;
   plan.call.q = q; plan.call.out = out;

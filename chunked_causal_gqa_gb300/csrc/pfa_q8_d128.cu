@@ -21,12 +21,23 @@
 // The factors are undone in the scores' multiplier and in the final 1 / l.
 //
 // Conversion is 4 instructions for 4 codes (two cvt.rn.f16x2.e4m3x2, two
-// products), about a seventh of the issue slots of a key tile; through bf16 it
-// would be 12 (no e4m3 -> bf16 conversion exists).
+// products); through bf16 it would be 12 (no e4m3 -> bf16 conversion exists).
 //
 // Warps: 0-3 and 4-7 softmax of tiles A and B, 8-11 converters, 12 TMEM and MMA
 // issue; 16 warps are launched with 128 registers a thread and split them
 // 200 / 200 / 72 / 40 by warpgroup (512 = 4 * 128).
+//
+// Measured on GB300: 128 tokens at 63360, 32/8 heads, 126.3 us (floor 69.5 us of tensor
+// time; reading the cache back and running the 16-bit kernel takes 160 us, 60 of them
+// for the 390 MB of the read-back).  A key tile of a pair takes 3600 cycles: 2200 of
+// tensor work, 900 of waiting for tile A's weights (the softmax's chain, which the
+// converters on the same schedulers lengthen: 2900 cycles a tile in pfa_bf16_d128.cu)
+// and 350 for operand tiles.  From about 1000 rows a kv head on the read-back costs
+// less than that, and pfa_prefill_attention_q8 takes it.
+// Steps: bounds checks and lane order of the converters 171 -> 129 us; packed fp32 pairs
+// and their registers 127.4; narrower merge blocks 126.3.  Tried: three converter warps
+// with a tile each and twelve warps in all (164 us: too few loads in flight), registers
+// 176 / 96 / 64 and 192 / 80 / 48 with scalar arithmetic (154, 139 us: spills).
 #include "pfa_internal.h"
 #include "pfa_ptx.cuh"
 #include "pfa_q8.cuh"

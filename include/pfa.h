@@ -504,6 +504,9 @@ PFA_API int pfa_cache_read_q8(const void *k8, const void *v8, const float *k_sca
  * Cache rows that no row of the sequence's T tokens sees are not read into the
  * result, whatever they hold.  A key that some of the T tokens see and others do
  * not must be finite (its weight is zero for the others, and zero times NaN is NaN).
+ * Weights are rounded to 11 bits (bf16) or 21 (fp32); small ones to 2^-39 of the largest
+ * weight and V scale of the sequence, so V scales of one sequence should not differ by
+ * more than some 2^20.
  */
 PFA_API int pfa_decode_attention_q8(const void *q, const void *k8, const void *v8,
                                     const float *k_scale, const float *v_scale, void *out,
@@ -518,12 +521,15 @@ PFA_API int pfa_decode_workspace_bytes_q8(int64_t B, int64_t T, int num_heads, i
 /*
  * pfa_prefill_attention_q8 -- pfa_prefill_attention_cache (linear) on one
  * sequence's 8-bit cache: T tokens at start_pos .., whose own rows have been
- * written.  q and out rows are qkv_dim elements apart.  A chunk of few rows runs
- * on the codes; a longer one reads the visible rows back into the workspace and
- * runs the 16/32-bit kernels on them (the softmax weights are then rounded as
- * those kernels round them).  workspace: pfa_prefill_workspace_bytes_q8 bytes
+ * written.  q and out rows are qkv_dim elements apart.  By the rows
+ * T * num_heads / num_kv_heads it runs the kernel of pfa_decode_attention_q8 (few rows,
+ * and all of fp32 with head_dim 512), a tensor-core kernel on the codes (bf16, head_dim
+ * 128), or it reads the visible rows back into the workspace and runs the 16/32-bit
+ * kernels on them (long chunks; the softmax weights are then rounded as those
+ * kernels round them).  workspace: pfa_prefill_workspace_bytes_q8 bytes
  * (PFA_ERR_SCRATCH otherwise), 256-byte aligned, not shared by calls that can run
- * at the same time.  head_dim and heads as for pfa_decode_attention_q8.
+ * at the same time.  head_dim, heads, and what a key that only some rows see may
+ * hold: as for pfa_decode_attention_q8.
  */
 PFA_API int pfa_prefill_attention_q8(const void *q, const void *k8, const void *v8,
                                      const float *k_scale, const float *v_scale, void *out,
