@@ -474,9 +474,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
     const int all_hi = x.end - (int)p.T + x.r0 / p.group;
     const int all_lo = p.window > 0 ? x.hi - p.window + 1 : 0;
 
-    float o[16][4];
+    // A lane's output columns: of rows g and g + 8, or (fp32) of row g, both halves' sum.
+    constexpr int OC = F32 ? 2 : 4;
+    float o[16][OC];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int c = 0; c < OC; ++c) o[i][c] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0x1p-100f;
 
 #pragma unroll 1
@@ -576,42 +580,74 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
         l[i] = l[i] * a + sum;
         alpha[i] = a * shrink;
       }
-      if constexpr (F32) alpha[1] = alpha[0];
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[NR - 1] != 1.f)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          o[i][0] *= alpha[0]; o[i][1] *= alpha[0];
-          o[i][2] *= alpha[1]; o[i][3] *= alpha[1];
-        }
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+          for (int c = 0; c < OC; ++c) o[i][c] *= alpha[c / 2];
       }
       // ---- weighted sum of V
       asm volatile("cp.async.wait_group %0;" :: "n"(2 * kStages - 1) : "memory");
       __syncwarp();
+      // V rows of k16 step j: 16 j + 2 qd, + 1 and 16 j + 8 + 2 qd, + 1
+      auto load_v = [&](int j, uint4 (&r)[4]) {
+        r[0] = lds16(vb + j * 2048 + v_at0);
+        r[1] = lds16(vb + j * 2048 + v_at1);
+        r[2] = lds16(vb + j * 2048 + 1024 + v_at0);
+        r[3] = lds16(vb + j * 2048 + 1024 + v_at1);
+      };
+      // word w of those rows -> fragments of output tiles 4 w .. 4 w + 3
+      auto fragments = [&](const uint4 (&r)[4], int w, uint32_t (&b)[8]) {
+        uint32_t v[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t a[4];
-        if constexpr (F32) {
-          split2(s[2 * j][0], s[2 * j][1], a[0], a[1]);
-          split2(s[2 * j + 1][0], s[2 * j + 1][1], a[2], a[3]);
-        } else {
+        for (int k = 0; k < 4; ++k) v[k] = w == 0 ? r[k].x : w == 1 ? r[k].y : w == 2 ? r[k].z : r[k].w;
+        e4m3x4_to_half(__byte_perm(v[0], v[1], 0x5140), b[0], b[1]);
+        e4m3x4_to_half(__byte_perm(v[0], v[1], 0x7362), b[2], b[3]);
+        e4m3x4_to_half(__byte_perm(v[2], v[3], 0x5140), b[4], b[5]);
+        e4m3x4_to_half(__byte_perm(v[2], v[3], 0x7362), b[6], b[7]);
+      };
+      if constexpr (F32) {
+        // The tensor cores truncate as they accumulate: over thousands of keys that is a bias of
+        // 1e-5 of the output.  So they add up one unit only, and rounding adds do the rest.
+        uint32_t a[2][4];
+        uint4 r[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          split2(s[2 * j][0], s[2 * j][1], a[j][0], a[j][1]);
+          split2(s[2 * j + 1][0], s[2 * j + 1][1], a[j][2], a[j][3]);
+          load_v(j, r[j]);
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t b[2][8];
+          fragments(r[0], w, b[0]);
+          fragments(r[1], w, b[1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma(c, a[0], b[0][i], b[0][4 + i]);
+            mma(c, a[1], b[1][i], b[1][4 + i]);
+            o[4 * w + i][0] += c[0] + c[2];
+            o[4 * w + i][1] += c[1] + c[3];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t a[4];
           a[0] = half2_of(s[2 * j][0], s[2 * j][1]);
           a[1] = half2_of(s[2 * j][2], s[2 * j][3]);
           a[2] = half2_of(s[2 * j + 1][0], s[2 * j + 1][1]);
           a[3] = half2_of(s[2 * j + 1][2], s[2 * j + 1][3]);
-        }
-        const uint4 r0 = lds16(vb + j * 2048 + v_at0), r1 = lds16(vb + j * 2048 + v_at1);
-        const uint4 r2 = lds16(vb + j * 2048 + 1024 + v_at0), r3 = lds16(vb + j * 2048 + 1024 + v_at1);
-        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-        const uint32_t w2[4] = {r2.x, r2.y, r2.z, r2.w}, w3[4] = {r3.x, r3.y, r3.z, r3.w};
+          uint4 r[4];
+          load_v(j, r);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t b[8];
-          e4m3x4_to_half(__byte_perm(w0[w], w1[w], 0x5140), b[0], b[1]);
-          e4m3x4_to_half(__byte_perm(w0[w], w1[w], 0x7362), b[2], b[3]);
-          e4m3x4_to_half(__byte_perm(w2[w], w3[w], 0x5140), b[4], b[5]);
-          e4m3x4_to_half(__byte_perm(w2[w], w3[w], 0x7362), b[6], b[7]);
+          for (int w = 0; w < 4; ++w) {
+            uint32_t b[8];
+            fragments(r, w, b);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma(o[4 * w + i], a, b[i], b[4 + i]);
+            for (int i = 0; i < 4; ++i) mma(o[4 * w + i], a, b[i], b[4 + i]);
+          }
         }
       }
       __syncwarp();
@@ -649,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
             float v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              v[j] = (F32 ? o[d + j][c] + o[d + j][c + 2] : o[d + j][2 * i + c]) * f;
+              v[j] = o[d + j][2 * i + c] * f;
             *reinterpret_cast<float4*>(to + join_at(part * 128 + qd * 32 + c * 16 + d, g)) =
                 make_float4(v[0], v[1], v[2], v[3]);
           }

@@ -87,9 +87,9 @@ int check_attention(int64_t B, int64_t T, int H, int Hkv, int D, float scale, in
   return PFA_OK;
 }
 
-// How a chunk of one sequence runs: its few rows by the decode kernel, the tiles of
-// a bf16 chunk of head_dim 128 from the codes, or the visible cache rows read back
-// into the workspace and the 16/32-bit kernels on them.
+// How a chunk of one sequence runs: few rows, and all of fp32, by the decode kernel; the
+// tiles of a bf16 chunk of head_dim 128 from the codes; or the visible cache rows read
+// back into the workspace and the bf16 kernels on them.
 enum class How { kDecode, kCodes, kReadBack };
 struct PrefillPlan {
   How how;
@@ -108,22 +108,23 @@ struct PrefillPlan {
 //     63488 keys, rows 512 / 768 / 1024 / 2048        123 / 171 / 244 / 434 (codes), 153 / 191 / 235 / 398 (read back)
 //     4096 keys, rows 32 / 128 / 256 / 384           15 / 21 / 33 / 43   21 / 22 / 25 / 26   26 / 25 / 26 / 24
 //   bf16, head_dim 512, 8/2 heads, 16384 keys, rows 256 / 512 / 768:  108 / 202 / 296, read back 224
-//   fp32, head_dim 128, 32/8 heads, 16384 keys, rows 512 / 768:  269 / 398, read back 360
-//   fp32, head_dim 512, 8/2 heads, 8192 keys, rows 256 / 1024:  101 / 366, read back 3456 / 6847
-//     (that attention runs on the CUDA cores)
+// fp32 always runs the decode kernel: pfa_f32x3_d128.cu on rows read back is faster from
+// some 600 rows on (16384 keys, 32/8 heads, 768 rows: 360 us against 398), but its split
+// into bf16 parts and its long sums leave up to 6e-5 of the output, six times what a
+// plain fp32 computation does; with head_dim 512 that attention runs on the CUDA cores
+// (8192 keys, 8/2 heads, 256 / 1024 rows: 3456 / 6847 us against 101 / 366).
 How prefill_how(int64_t T, int64_t keys, int H, int Hkv, int D, int dtype, int num_sms) {
   const int64_t rows = T * (H / Hkv);
-  if (dtype == PFA_BF16 && D == 128) {
+  if (dtype == PFA_F32) return How::kDecode;
+  if (D == 128) {
     if (rows <= 48) return How::kDecode;
     if (rows <= 256 || (rows <= 768 && keys >= 16384))
       return q8_d128_serves(T, H, Hkv) ? How::kCodes : How::kReadBack;
     return How::kReadBack;
   }
-  if (dtype == PFA_F32 && D != 128) return How::kDecode;
   // A wave of tiles costs what the decode kernel takes for this many rows of one kv head.
-  const int64_t wave = dtype == PFA_F32 ? 5300 : 1150;
-  const int64_t blocks = dtype == PFA_F32 ? (rows + 127) / 128 * Hkv : (rows + 255) / 256 * 4 * Hkv;
-  return rows * Hkv <= wave * ((blocks + num_sms - 1) / num_sms) ? How::kDecode : How::kReadBack;
+  const int64_t blocks = (rows + 255) / 256 * 4 * Hkv;
+  return rows * Hkv <= 1150 * ((blocks + num_sms - 1) / num_sms) ? How::kDecode : How::kReadBack;
 }
 
 int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window, float scale,
@@ -151,7 +152,7 @@ int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window
   if (rc != PFA_OK) return rc;
   p->v_at = kv;
   p->ws_at = 2 * kv;
-  p->call.ws_bytes = dtype == PFA_BF16 ? workspace_bytes_bf16(p->call) : 0;
+  p->call.ws_bytes = workspace_bytes_bf16(p->call);
   p->total = p->ws_at + round256(p->call.ws_bytes);
   return PFA_OK;
 }

@@ -194,9 +194,9 @@ def prefill_attention_q8(q: torch.Tensor, cache: Q8Cache, out: torch.Tensor | No
 
     q: [T, H, D], float32 or bfloat16, heads and elements dense (strides (qkv_dim, D, 1));
     cache: without a batch dimension (Q8Cache.slot), its rows up to start_pos + T
-    written; out: None or a tensor with q's shape and strides.  A chunk of more than a few
-    rows reads the visible rows back into the workspace (2 * Hkv * rows * D elements of
-    q's dtype) and runs the attention of prefill_attention_cache on them.  Other
+    written; out: None or a tensor with q's shape and strides.  A long bfloat16 chunk
+    reads the visible rows back into the workspace (2 * Hkv * rows * D elements) and runs
+    the attention of prefill_attention_cache on them; others run on the codes.  Other
     arguments: as for prefill_attention_cache; workspace: "auto" or a uint8 CUDA tensor
     of prefill_workspace_bytes_q8 bytes.
     """

@@ -523,10 +523,10 @@ PFA_API int pfa_decode_workspace_bytes_q8(int64_t B, int64_t T, int num_heads, i
  * sequence's 8-bit cache: T tokens at start_pos .., whose own rows have been
  * written.  q and out rows are qkv_dim elements apart.  By the rows
  * T * num_heads / num_kv_heads it runs the kernel of pfa_decode_attention_q8 (few rows,
- * and all of fp32 with head_dim 512), a tensor-core kernel on the codes (bf16, head_dim
- * 128), or it reads the visible rows back into the workspace and runs the 16/32-bit
- * kernels on them (long chunks; the softmax weights are then rounded as those
- * kernels round them).  workspace: pfa_prefill_workspace_bytes_q8 bytes
+ * and all of fp32), a tensor-core kernel on the codes (bf16, head_dim
+ * 128), or it reads the visible rows back into the workspace and runs the 16-bit
+ * kernels on them (long bf16 chunks; the softmax weights are then rounded to bf16 as
+ * those kernels do).  workspace: pfa_prefill_workspace_bytes_q8 bytes
  * (PFA_ERR_SCRATCH otherwise), 256-byte aligned, not shared by calls that can run
  * at the same time.  head_dim, heads, and what a key that only some rows see may
  * hold: as for pfa_decode_attention_q8.

@@ -519,10 +519,25 @@ def test_prefill(T, sp, window, D, dt):
     out = pkg.prefill_attention_q8(q, cache, start_pos=sp, window=window)
     assert out.stride() == q.stride() or T == 1
     want, tol = R.attention(q, cache, n, window, R.default_scale(D), dt)
-    # where the rows are read back, the weights are rounded as prefill_attention rounds them:
-    # bf16 weights (2^-8), fp32 as a high and a low bf16 part with three products (2^-15)
+    # where bf16 rows are read back, the weights are rounded as prefill_attention rounds them: 2^-8
     v = R.values(cache.v, cache.v_scale)[:, :n].abs().amax().item()
-    within(out, want, tol + v * (2.0 ** -8 if dt == BF16 else 2.0 ** -15), f"T {T}")
+    within(out, want, tol + (v * 2.0 ** -8 if dt == BF16 else 0.0), f"T {T}")
+    ok()
+
+
+def test_fp32_over_many_keys_is_fp32():
+    """A tensor core's sum truncates: over 30000 keys in one run the bias must not show.
+
+    Plain fp32 sums of n terms of random sign are off by some 2^-24 sqrt(log2 n) of their
+    root mean square; this asks for 2^-20 of the outputs' (a 2-norm), 16 roundings."""
+    cap, Hkv, H, D = 30016, 1, 8, 128
+    cache = pkg.Q8Cache(*R.make_cache(Hkv, cap, D, 64, batch=1, seed=3, device=G.dev()))
+    q = randn((1, 100, H, D), F32, 4, 0.02)                # flat weights: every key counts
+    d = torch.tensor([cap], device=G.dev())
+    out = pkg.decode_attention_q8(q, cache, d)
+    want, _ = R.attention(q[0], cache.slot(0), cap, 0, R.default_scale(D), F32)
+    assert (out[0].double() - want).norm() <= 2.0 ** -20 * want.norm()
+    assert torch.equal(out[0], pkg.prefill_attention_q8(q[0], cache.slot(0), start_pos=cap - 100))
     ok()
 
 
