@@ -242,6 +242,8 @@ DECODE = [  # B, T, H, Hkv, D, block, cap, window, dtype
     (4, 1, 8, 2, 512, 64, 512, 0, BF16),
     (4, 3, 8, 2, 512, 32, 320, 90, F32),
     (4, 5, 8, 2, 512, 16, 320, 0, BF16),
+    (40, 5, 12, 2, 512, 32, 1024, 0, F32),
+    (80, 6, 6, 2, 128, 64, 2048, 700, F32),
     (3, 1, 16, 1, 512, 128, 384, 5, F32),
     (2, 20, 16, 2, 128, 64, 320, 0, BF16),
     (40, 1, 2, 2, 128, 16, 96, 0, BF16),
@@ -429,8 +431,8 @@ def test_decode_of_more_sequences_than_one_launch_lists():
 # ------------------------------------------------------------------ chunks
 
 def test_prefill_of_more_row_tiles_than_one_launch_lists():
-    T, H, D = 1100, 128, 512                              # 17600 tiles of 8 rows
-    cache = pkg.Q8Cache(*R.make_cache(1, 1152, D, 64, seed=3, device=G.dev(), dead=[T]))
+    T, H, D = 2100, 128, 512                              # 16800 tiles of 16 rows
+    cache = pkg.Q8Cache(*R.make_cache(1, 2176, D, 64, seed=3, device=G.dev(), dead=[T]))
     q = randn((T, H, D), F32, 4, 1.0)
     out = pkg.prefill_attention_q8(q, cache, start_pos=0)
     heads = [0, 77, 127]
