@@ -21,7 +21,7 @@
 // word of four elements as its part of one k16 step; likewise output columns, so
 // a lane reads 16 bytes of four V rows and pairs the rows' bytes with prmt.
 //
-// Work split: tiles of 32 keys ("units") of all sequences, heads and row tiles
+// Work split: tiles of 32 keys ("units") of all row tiles, sequences and heads
 // form one list, cut into equal runs, one for each block (two blocks an SM).
 // Four warps take the run's units in turn, each with its own ring of three
 // stages filled by cp.async (no barrier in the loop); their sums join in shared
@@ -87,7 +87,7 @@ struct Params {
   int tile0;
   int cap, Hkv, window, block_shift;
   int rows, entries;          // T * group; entries of this launch
-  Divisor group, tiles;       // H / Hkv; row tiles of a sequence in this launch
+  Divisor group, seqs;        // H / Hkv; sequences in this launch
   Divisor heads, joined;      // Hkv, and the second kernel's blocks for a tile's rows
   float scale_log2;
   unsigned* err;
@@ -108,9 +108,9 @@ struct Entry {
 template <int RM>
 __device__ __forceinline__ Entry entry_of(const Params& p, int e) {
   Entry x;
-  const int s = e / p.tiles;
-  x.b = p.b0 + s;
-  x.r0 = (p.tile0 + e - s * (int)p.tiles.by) * RM;
+  const int tile = e / p.seqs;
+  x.b = p.b0 + e - tile * (int)p.seqs.by;
+  x.r0 = (p.tile0 + tile) * RM;
   x.nr = min(RM, p.rows - x.r0);
   const int64_t end = p.lengths ? p.lengths[x.b] : p.start_pos + p.T;
   x.bad = end < 0 || end > p.cap;
@@ -892,14 +892,21 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
   cfg.stream = c.stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const int blocks = c.num_sms * kBlocksPerSm;
+  const int most_blocks = c.num_sms * kBlocksPerSm;
   for (int64_t b = 0; b < B; b += at_once)
     for (int tile = 0; tile < tiles; tile += tiles_at_once) {
       const int here = std::min(tiles_at_once, tiles - tile);
       p.b0 = b;
       p.tile0 = tile;
-      p.tiles = divisor(here);
-      p.entries = (int)std::min(at_once, B - b) * here;
+      const int seqs = (int)std::min(at_once, B - b);
+      p.seqs = divisor(seqs);
+      p.entries = seqs * here;
+      // The list has all sequences' first row tiles, then all second ones: with a number of
+      // blocks that the tiles divide, blocks far apart read the same keys at the same time and
+      // the cache comes from HBM once (32 sequences of 8192 keys, 32/8 heads of 128, 8 / 12 / 20
+      // tokens: 159 / 244 / 370 us; each sequence's tiles in a row 172 / 247 / -, tiles that
+      // do not divide the blocks - / 254 / 407).
+      const int blocks = here <= 16 ? most_blocks - most_blocks % here : most_blocks;
       // A head has about blocks / heads parts: for many of them eight warps to a row, for
       // few a warp (32 sequences of 8 heads: 49.7 us for both kernels with eight, 46.3 with one).
       const int rows = std::min(RM, p.rows);
