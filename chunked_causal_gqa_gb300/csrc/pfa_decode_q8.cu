@@ -260,6 +260,9 @@ static_assert(kBlocksPerSm * (sizeof(Shared) + 1024) <= 228 * 1024, "shared memo
 // rows.  bf16 has NR 2, one set of fragments for both; fp32 a set for each.
 template <typename E, int NW, int NR>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Params p) {
+  // A team is a warp or the block, so that every barrier is the block's: it does not count
+  // warps that have ended, and no lengths, not even changing ones, leave a warp waiting.
+  static_assert(NW == 1 || NW == kWarps, "barriers are the block's");
   constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = 8 * NR;
   constexpr bool F32 = sizeof(E) == 4;
   constexpr int SETS = F32 ? NR : 1;
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       if constexpr (NW > 1) {   // over the team's columns
         if (qd == 0) sm.ml[warp][g + 8 * i].x = amax;
-        asm volatile("bar.sync %0, %1;" :: "r"(1 + team), "n"(NW * 32) : "memory");
+        __syncthreads();
 #pragma unroll
         for (int w = 0; w < NW; ++w) amax = fmaxf(amax, sm.ml[team * NW + w][g + 8 * i].x);
       }
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 #pragma unroll
           for (int i = 0; i < NR; ++i)
             ex[part * 256 + (nt * 2 + i) * 32 + lane] = make_float2(s[nt][2 * i], s[nt][2 * i + 1]);
-        asm volatile("bar.sync %0, %1;" :: "r"(1 + team), "n"(NW * 32) : "memory");
+        __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll

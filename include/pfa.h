@@ -401,7 +401,8 @@ PFA_API int pfa_prefill_attention_noalloc(const void *q, const void *k_cache,
  * Code pointers are 16-byte aligned, max_seq_len * head_dim may pass 2^31.
  *
  * Where new tokens sit: with `lengths` (device pointer, B int64, read when the
- * kernel runs, so that a captured graph replays for other lengths) sequence b
+ * kernel runs, so that a captured graph replays for other lengths; like any
+ * input they stay as they are until the call's kernels have ended) sequence b
  * has lengths[b] tokens after the call's T and its token t is at position
  * lengths[b] - T + t; without (NULL) there is one sequence and token t is at
  * start_pos + t.  lengths[b] < T pads the sequence in front: its first
