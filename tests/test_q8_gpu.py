@@ -428,6 +428,17 @@ def test_decode_of_more_sequences_than_one_launch_lists():
     ok()
 
 
+@pytest.mark.parametrize("case", [
+    (7, 12, 8, 2, 128, 64, 4096, 0, BF16),     # 3 tiles of 16 rows
+    (6, 52, 4, 1, 128, 32, 1024, 200, BF16),   # 13
+    (6, 9, 20, 2, 512, 16, 512, 0, BF16),      # 6
+    (3, 128, 16, 2, 128, 64, 512, 0, BF16),    # 64
+    (5, 35, 8, 4, 128, 128, 1024, 0, F32),     # 5, the last of 6 rows
+], ids=str)
+def test_decode_of_several_row_tiles(case):
+    test_decode(case)
+
+
 # ------------------------------------------------------------------ chunks
 
 def test_prefill_of_more_row_tiles_than_one_launch_lists():
