@@ -105,14 +105,17 @@ struct Entry {
   __device__ int listed() const { return n > 0 ? n + kHeadCost : 0; }
 };
 
-template <int RM>
+// L2: the length is read from there, past this SM's own cache.
+template <int RM, bool L2 = false>
 __device__ __forceinline__ Entry entry_of(const Params& p, int e) {
   Entry x;
   const int tile = e / p.seqs;
   x.b = p.b0 + e - tile * (int)p.seqs.by;
   x.r0 = (p.tile0 + tile) * RM;
   x.nr = min(RM, p.rows - x.r0);
-  const int64_t end = p.lengths ? p.lengths[x.b] : p.start_pos + p.T;
+  const int64_t end = !p.lengths ? p.start_pos + p.T
+                      : L2       ? __ldcg((const long long*)p.lengths + x.b)
+                                 : p.lengths[x.b];
   x.bad = end < 0 || end > p.cap;
   x.end = x.bad ? 0 : (int)end;
   const int first = x.end - (int)p.T;
@@ -272,8 +275,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   const int g = lane >> 2, qd = lane & 3;
   const int team = warp / NW, part = warp % NW;
 
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before has written its results
+  // What ran before has written its results; only then may the join start (it reads the lengths
+  // before its own wait).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- the list of units, and where this block's run starts in it
   int at, stop, first_entry, into;
@@ -767,11 +772,13 @@ __global__ void __launch_bounds__(512) join_kernel(const Params p, int blocks) {
   const int eh = id / p.joined, r = id - eh * (int)p.joined.by + warp / GROUPS;
   const int e = eh / p.heads, h = eh - e * p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;");
-  // the list of units, as the first kernel counts it
+  // The list of units, as the first kernel counts it, while that one runs.  Its blocks let this
+  // grid start behind their own wait: whatever wrote the lengths has ended, and its writes are in
+  // L2.  (The first kernel's own results are read behind the wait below.)
   int before = 0, total = 0;
 #pragma unroll 1
   for (int i = tid; i < p.entries; i += blockDim.x) {
-    const int n = entry_of<RM>(p, i).listed() * p.Hkv;
+    const int n = entry_of<RM, true>(p, i).listed() * p.Hkv;
     total += n;
     if (i < e) before += n;
   }
@@ -789,7 +796,7 @@ __global__ void __launch_bounds__(512) join_kernel(const Params p, int blocks) {
     before += s_units[w][0];
     total += s_units[w][1];
   }
-  const Entry x = entry_of<RM>(p, e);
+  const Entry x = entry_of<RM, true>(p, e);
   const int run = run_of<TEAMS>(total, blocks);
   const int s0 = before + h * x.listed();
   int c0 = 0, n = 0, first = 0;
@@ -886,8 +893,9 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
   const int64_t at_once = tiles_at_once < tiles ? 1 : most / tiles;   // sequences
   p.parts = static_cast<float*>(c.ws);
   p.heads = divisor(p.Hkv);
-  // Both kernels may be launched before what is in front of them has ended: they
-  // wait (griddepcontrol) before they read what it writes.
+  // The first kernel may be launched before what is in front of it has ended: it waits
+  // (griddepcontrol) before it reads anything.  The second one starts when every block of the
+  // first is past that wait, and waits for the first before it reads what that writes.
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
