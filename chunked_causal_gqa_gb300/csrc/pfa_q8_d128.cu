@@ -17,7 +17,9 @@
 //      half's 2^-24); below that it is rounded to 2^-32 of the largest block's step.
 //   q: times a power of two for each row that brings its largest element to 2^13 ..
 //      2^14, exact but for elements 2^27 below it.
-//   p = 2^(s - base) <= 2^8, rounded to 11 bits (bf16 would keep 8).
+//   p = 2^(s - base + 7), rounded to 11 bits, small ones to 2^-25.  The base is at most 8 below
+//      the row's running maximum, so p <= 2^15, and small weights are off by up to 2^-32 of the
+//      row's largest (bf16 weights would keep 8 bits of each).  l has the same factor 2^7.
 // The factors are undone in the scores' multiplier and in the final 1 / l.
 //
 // Conversion is 4 instructions for 4 codes (two cvt.rn.f16x2.e4m3x2, two
@@ -58,6 +60,7 @@ constexpr int kSlots = 5;                       // operand ring depth (tiles)
 constexpr int kThreads = 512;
 constexpr float kRescaleThreshold = 8.f;        // log2 units
 constexpr float kOperandScale = 128.f;          // of k and v
+constexpr float kWeightBits = 7.f;              // weights and their sum are times 2^7
 
 constexpr int kSmemQ = 0;
 constexpr int kSmemRing = 2 * kTileBytes;
@@ -475,7 +478,7 @@ q8_d128_kernel(const __grid_constant__ Params p) {
       }
       const float base = m_run == -INFINITY ? 0.f : m_run;
       uint32_t pk0[32], pk1[32];
-      const uint64_t cc = pair_of(c, c), bb = pair_of(-base, -base);
+      const uint64_t cc = pair_of(c, c), bb = pair_of(kWeightBits - base, kWeightBits - base);
       uint64_t ls[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < 64; ++k) {

@@ -527,7 +527,8 @@ PFA_API int pfa_decode_workspace_bytes_q8(int64_t B, int64_t T, int num_heads, i
  * and all of fp32), a tensor-core kernel on the codes (bf16, head_dim
  * 128), or it reads the visible rows back into the workspace and runs the 16-bit
  * kernels on them (long bf16 chunks; the softmax weights are then rounded to bf16 as
- * those kernels do).  workspace: pfa_prefill_workspace_bytes_q8 bytes
+ * those kernels do).  On the codes the tensor-core kernel rounds weights to 11 bits, small
+ * ones to 2^-32 of the row's largest.  workspace: pfa_prefill_workspace_bytes_q8 bytes
  * (PFA_ERR_SCRATCH otherwise), 256-byte aligned, not shared by calls that can run
  * at the same time.  head_dim, heads, and what a key that only some rows see may
  * hold: as for pfa_decode_attention_q8.
