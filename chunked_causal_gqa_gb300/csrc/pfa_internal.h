@@ -162,6 +162,7 @@ struct NormRopeCall {
   int rot_dim, interleaved, dtype;
   // elements from one token's row to the next, and from one head to the next of k_out
   int64_t q_row, k_row, q_out_row, k_out_row, k_out_head;
+  unsigned* err;
   int num_sms;
   cudaStream_t stream;
 };

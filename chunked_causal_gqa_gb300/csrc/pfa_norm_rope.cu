@@ -23,6 +23,7 @@
 // sector at a time); two rows ahead instead of one (11.0 / 11.4 us at 64 registers,
 // 10.0 / 10.2 with three blocks an SM).
 #include "pfa_internal.h"
+#include "pfa_ptx.cuh"
 #include "pfa_q8.cuh"
 
 #include "../../include/pfa.h"
@@ -50,6 +51,7 @@ struct Params {
   int H, rows, block_rows;  // tokens * heads; rows of a block
   int D, rot, interleaved;
   float eps, offset, inv_dim;   // 1 / D
+  unsigned* err;
 };
 
 // f / (2 pi) modulo 1 as a 64-bit fraction, from the double's bits.
@@ -238,13 +240,16 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_con
           }
         }
       }
-      if (p.lengths && position(n) < 0) {  // padding in front
+      bool write = true;
+      if (p.lengths && position(n) < 0) {  // padding in front, or no length
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = {0.f, 0.f};
+        write = p.lengths[n / p.T] >= 0;
+        if (!write && h == 0 && lane == 0) atomicOr(p.err, kErrLengths);
       }
       E* dst = isq ? (E*)p.q.out + n * p.q.out_row + h * p.D
                    : (E*)p.k.out + n * p.k.out_row + (h - p.H) * p.k.out_head;
-      store_pieces(dst + at, stride, y);
+      if (write) store_pieces(dst + at, stride, y);
     }
   }
 }
@@ -304,6 +309,7 @@ int launch_norm_rope(const NormRopeCall& c) {
   p.D = c.D;
   p.rot = c.rot_dim; p.interleaved = c.interleaved;
   p.eps = c.eps; p.offset = c.weight_offset; p.inv_dim = 1.f / (float)c.D;
+  p.err = c.err;
   const cudaError_t e = c.dtype == PFA_F32 ? launch<float>(p, c.num_sms, c.stream)
                                            : launch<__nv_bfloat16>(p, c.num_sms, c.stream);
   if (e == cudaSuccess) return kOk;

@@ -233,6 +233,7 @@ int pfa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int
   c.dtype = dtype;
   c.q_row = q_stride; c.k_row = k_stride; c.q_out_row = q_out_stride;
   c.k_out_row = k_out_stride; c.k_out_head = k_out_head_stride;
+  c.err = d.err;
   c.num_sms = d.num_sms;
   c.stream = static_cast<cudaStream_t>(stream);
   return launch_norm_rope(c);

@@ -407,8 +407,8 @@ PFA_API int pfa_prefill_attention_noalloc(const void *q, const void *k_cache,
  * lengths[b] - T + t; without (NULL) there is one sequence and token t is at
  * start_pos + t.  lengths[b] < T pads the sequence in front: its first
  * T - lengths[b] tokens have negative positions; lengths[b] = 0 is an empty
- * slot.  lengths[b] < 0 or > max_seq_len: nothing of that sequence is written and
- * PFA_ERR_LENGTHS is recorded for pfa_last_device_error.
+ * slot.  lengths[b] < 0, or > max_seq_len where the call has one: nothing of that
+ * sequence is written and PFA_ERR_LENGTHS is recorded for pfa_last_device_error.
  *
  * Row b * T + t of a token-major array starts at (b * T + t) * its stride
  * (elements; stride * element size a multiple of 16 bytes), heads and elements
