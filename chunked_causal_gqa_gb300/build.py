@@ -9,10 +9,13 @@ machine without a GPU driver.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpfa.so")
 EXT = os.path.join(BUILD, "_pfa_torch.so")
+EXT_KEY = os.path.join(BUILD, "_pfa_torch.key")
 EXT_SOURCE = os.path.join(CSRC, "pfa_torch.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -52,14 +56,50 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
-def _build_extension() -> None:
-    """Compile _pfa_torch.so against this Python's torch, unless it is up to date."""
+def extension_environment() -> str:
+    """The Python and torch that _pfa_torch.so is compiled against, in one line."""
     import sysconfig
 
     import torch
-    deps = [EXT_SOURCE, os.path.join(INCLUDE, "pfa.h"), __file__, torch.__file__]
-    if os.path.exists(EXT) and all(os.path.getmtime(d) <= os.path.getmtime(EXT) for d in deps):
-        return
+    return (f"{sysconfig.get_config_var('SOABI')} torch {torch.__version__} "
+            f"{torch.version.git_version} cxx11abi {int(torch.compiled_with_cxx11_abi())}")
+
+
+def _extension_key() -> str:
+    """What _pfa_torch.so depends on: its environment, then its sources and this file."""
+    h = hashlib.sha256()
+    for path in (EXT_SOURCE, os.path.join(INCLUDE, "pfa.h"), __file__):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return f"{extension_environment()}\n{h.hexdigest()}\n"
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def built_environment() -> str:
+    """The environment that the present _pfa_torch.so was compiled against ("": unknown)."""
+    return _read(EXT_KEY).partition("\n")[0]
+
+
+def build_extension(force: bool = False) -> str:
+    """Compile _pfa_torch.so against this Python's torch, unless it is up to date; returns its path.
+
+    Raises RuntimeError or OSError where it cannot be compiled, and then leaves none."""
+    import sysconfig
+
+    import torch
+    key = _extension_key()
+    if not force and os.path.exists(EXT) and _read(EXT_KEY) == key:
+        return EXT
+    for stale in (EXT_KEY, EXT):
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(stale)
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     dirs = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api",
@@ -76,12 +116,28 @@ def _build_extension() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT)
+    with open(tmp, "w") as f:
+        f.write(key)
+    os.replace(tmp, EXT_KEY)
+    return EXT
+
+
+def _extension_or_warning(force: bool) -> None:
+    """libpfa.so serves C callers and the 16/32-bit path without the extension."""
+    try:
+        build_extension(force)
+    except (OSError, RuntimeError) as e:
+        warnings.warn("_pfa_torch.so was not built, so the Python functions of the 8-bit cache's "
+                      f"operators will raise ImportError: {e}", stacklevel=3)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libpfa.so, then _pfa_torch.so; returns libpfa.so's path."""
+    """Compile and link libpfa.so, then _pfa_torch.so; returns libpfa.so's path.
+
+    Where _pfa_torch.so cannot be compiled (no g++, no headers of Python or torch) that is a
+    warning: only the operators of the 8-bit cache need it, and only from Python."""
     if not force and not extra_flags and up_to_date():
-        _build_extension()
+        _extension_or_warning(force)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -107,7 +163,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_extension()
+    _extension_or_warning(force)
     return LIB
 
 

@@ -21,7 +21,6 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
-import os
 import threading
 from typing import NamedTuple
 
@@ -70,18 +69,23 @@ _module = None
 
 
 def _ext():
-    """_pfa_torch.so (raises if it is missing: build it with build.build())."""
+    """_pfa_torch.so (raises if it is missing or another torch's: build it with build.build())."""
     global _module
     if _module is None:
         with _lock:
             if _module is None:
+                from . import build
                 _binding.load()
-                path = os.path.join(os.path.dirname(_binding.LIB_PATH), "_pfa_torch.so")
-                if not os.path.exists(path):
+                if not os.path.exists(build.EXT):
                     raise ImportError(
-                        f"_pfa_torch.so not found at {path}; build it with "
-                        "`python -c 'import chunked_causal_gqa_gb300.build as b; b.build()'`")
-                spec = importlib.util.spec_from_file_location("_pfa_torch", path)
+                        f"_pfa_torch.so not found at {build.EXT}; build it with "
+                        "`python -c 'import chunked_causal_gqa_gb300.build as b; b.build_extension()'`")
+                if build.built_environment() != build.extension_environment():
+                    raise ImportError(
+                        f"{build.EXT} was built for '{build.built_environment()}', this is "
+                        f"'{build.extension_environment()}'; build it again with "
+                        "`python -c 'import chunked_causal_gqa_gb300.build as b; b.build_extension()'`")
+                spec = importlib.util.spec_from_file_location("_pfa_torch", build.EXT)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)
                 _module = module
