@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import os
 import threading
 from typing import NamedTuple
 
