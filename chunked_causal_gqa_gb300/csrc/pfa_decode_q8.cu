@@ -946,7 +946,7 @@ int launch(Params p, const DecodeQ8Call& c, int64_t B) {
 
 }  // namespace
 
-size_t decode_q8_workspace(int64_t, int64_t T, int H, int Hkv, int D, int dtype, int num_sms) {
+size_t decode_q8_workspace(int64_t T, int H, int Hkv, int D, int dtype, int num_sms) {
   const int rm = dtype == PFA_F32 && T * (H / Hkv) <= 8 ? 8 : 16;   // most rows of a tile
   return 2 * (size_t)num_sms * kBlocksPerSm * (rm * D + rm * 2) * sizeof(float);  // two slots a run
 }

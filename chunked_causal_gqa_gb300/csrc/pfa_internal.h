@@ -214,13 +214,12 @@ struct DecodeQ8Call {
   void* ws;
   cudaStream_t stream;
 };
-// Workspace bytes of launch_decode_q8 for B sequences of T tokens.
-size_t decode_q8_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int num_sms);
+// Workspace bytes of launch_decode_q8 for T tokens of each sequence.
+size_t decode_q8_workspace(int64_t T, int H, int Hkv, int D, int dtype, int num_sms);
 int launch_decode_q8(const DecodeQ8Call& c);
 
-// A bf16 chunk of one sequence, head_dim 128, on the tensor cores from the codes:
-// whether it serves the call, its workspace bytes, the launch.
-bool q8_d128_serves(int64_t T, int H, int Hkv);
+// A bf16 chunk of one sequence, head_dim 128, on the tensor cores from the codes: its
+// workspace bytes, the launch.  T * H < 2^30.
 size_t q8_d128_workspace(int64_t T, int64_t start_pos, int H, int Hkv, int window, int num_sms);
 int launch_q8_d128(const DecodeQ8Call& c);
 

@@ -118,9 +118,7 @@ How prefill_how(int64_t T, int64_t keys, int H, int Hkv, int D, int dtype, int n
   if (dtype == PFA_F32) return How::kDecode;
   if (D == 128) {
     if (rows <= 48) return How::kDecode;
-    if (rows <= 256 || (rows <= 768 && keys >= 16384))
-      return q8_d128_serves(T, H, Hkv) ? How::kCodes : How::kReadBack;
-    return How::kReadBack;
+    return rows <= 256 || (rows <= 768 && keys >= 16384) ? How::kCodes : How::kReadBack;
   }
   // A wave of tiles costs what the decode kernel takes for this many rows of one kv head.
   const int64_t blocks = (rows + 255) / 256 * 4 * Hkv;
@@ -135,19 +133,20 @@ int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window
   p->how = prefill_how(T, window > 0 ? std::min<int64_t>(start_pos + T, window + T) : start_pos + T,
                        H, Hkv, D, dtype, num_sms);
   if (p->how == How::kDecode) {
-    p->total = decode_q8_workspace(1, T, H, Hkv, D, dtype, num_sms);
+    p->total = decode_q8_workspace(T, H, Hkv, D, dtype, num_sms);
     return PFA_OK;
   }
   if (p->how == How::kCodes) {
-    p->total = q8_d128_workspace(T, start_pos, H, Hkv, std::max(window, 0), num_sms);
+    if (T * H >= (int64_t)1 << 30) return PFA_ERR_SHAPE;   // 32-bit rows; its q takes 256 GB
+    p->total = q8_d128_workspace(T, start_pos, H, Hkv, window, num_sms);
     return PFA_OK;
   }
   p->lo = window > 0 ? std::max<int64_t>(0, start_pos - window + 1) : 0;
   p->rows = start_pos + T - p->lo;
-  const size_t kv = round256((size_t)Hkv * p->rows * D * elem(dtype));
+  const size_t kv = round256((size_t)Hkv * p->rows * D * elem(PFA_BF16));
   // causal and window masks depend on differences of positions only
   const int rc = prepare_layout(nullptr, nullptr, nullptr, nullptr, T, start_pos - p->lo, H, Hkv,
-                                D, window, scale, dtype, qkv_dim, p->rows, 0, stream, false,
+                                D, window, scale, PFA_BF16, qkv_dim, p->rows, 0, stream, false,
                                 &p->call);
   if (rc != PFA_OK) return rc;
   p->v_at = kv;
@@ -332,7 +331,7 @@ int pfa_decode_workspace_bytes_q8(int64_t B, int64_t T, int num_heads, int num_k
   if (B == 0 || T == 0) return PFA_OK;
   DeviceInfo d;
   if ((rc = current_device(&d)) != kOk) return rc;
-  *bytes = decode_q8_workspace(B, T, num_heads, num_kv_heads, head_dim, dtype, d.num_sms);
+  *bytes = decode_q8_workspace(T, num_heads, num_kv_heads, head_dim, dtype, d.num_sms);
   return PFA_OK;
 }
 
@@ -368,7 +367,7 @@ int pfa_decode_attention_q8(const void* q, const void* k8, const void* v8, const
   DeviceInfo d;
   if ((rc = current_device(&d)) != kOk) return rc;
   const size_t need =
-      decode_q8_workspace(B, T, num_heads, num_kv_heads, head_dim, dtype, d.num_sms);
+      decode_q8_workspace(T, num_heads, num_kv_heads, head_dim, dtype, d.num_sms);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return PFA_ERR_SCRATCH;
     if (overlaps(workspace, need, q, rq.span()) || overlaps(workspace, need, out, ro.span()) ||
@@ -470,13 +469,13 @@ int pfa_prefill_attention_q8(const void* q, const void* k8, const void* v8, cons
   r.k_out = base; r.v_out = base + plan.v_at;
   r.heads = num_kv_heads; r.start = plan.lo; r.rows = plan.rows;
   r.out_head = plan.rows * head_dim;
-  r.D = head_dim; r.dtype = dtype;
+  r.D = head_dim; r.dtype = PFA_BF16;
   r.stream = static_cast<cudaStream_t>(stream);
   if ((rc = launch_cache_read_q8(r)) != kOk) return rc;
   plan.call.q = q; plan.call.out = out;
   plan.call.k = r.k_out; plan.call.v = r.v_out;
   plan.call.ws = plan.call.ws_bytes ? base + plan.ws_at : nullptr;
-  return dispatch(plan.call, dtype);
+  return dispatch(plan.call, PFA_BF16);
 }
 
 }  // extern "C"

@@ -660,11 +660,6 @@ Plan plan_of(int T, int start_pos, int H, int Hkv, int window, int sms) {
 
 }  // namespace
 
-bool q8_d128_serves(int64_t T, int H, int Hkv) {
-  // 32-bit rows and blocks
-  return H / Hkv <= 128 && T * (H / Hkv) * Hkv < ((int64_t)1 << 30);
-}
-
 size_t q8_d128_workspace(int64_t T, int64_t start_pos, int H, int Hkv, int window, int num_sms) {
   const Plan s = plan_of((int)T, (int)start_pos, H, Hkv, window, num_sms);
   return (size_t)s.p2 * s.parts * kSlotFloats * sizeof(float);

@@ -50,3 +50,11 @@ def test_a_flat_tail_under_a_few_large_weights(n, bits):
     over = ((out.double() - want).abs() - tol - small).max().item()
     assert over <= 0, f"{over:.3e} over the tolerance, outputs of {want.abs().median().item():.3e}"
     ok()
+
+
+def test_a_chunk_of_more_rows_than_the_kernel_counts_is_refused():
+    heads = 1 << 24                                         # 2^30 rows and more: q alone has 256 GB
+    with pytest.raises(pkg.PfaError) as e:
+        pkg.prefill_workspace_bytes_q8(100, 20000, heads, heads, 128)
+    assert e.value.name == "PFA_ERR_SHAPE"
+    assert pkg.prefill_workspace_bytes_q8(100, 20000, 160, 160, 128) > 0
