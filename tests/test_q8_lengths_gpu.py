@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("D,rot,T", [(128, 128, 1), (128, 64, 3), (512, 512, 2), (80, 0, 2)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_norm_rope_leaves_sequences_of_negative_length_unwritten(dt, D, rot, T, in_place):
-    H, Hkv, lens = 5, 1, [-1, 7, 0, -(1 << 40), T, -T]
+    H, Hkv, lens = 5, 1, [-1, 7, 0, -(1 << 40), T, -T, -(1 << 63)]
     B = len(lens)
     g = torch.Generator().manual_seed(D + T)
     q, k = (torch.randn((B, T, h, D), generator=g).to(dt).to(G.dev()) for h in (H, Hkv))
