@@ -107,7 +107,18 @@ struct PrefillPlan {
 //     63488 keys, rows 32 / 64 / 128                 50 / 82 / 144   71 / 70 / 72   120
 //     63488 keys, rows 512 / 768 / 1024 / 2048        123 / 171 / 244 / 434 (codes), 153 / 191 / 235 / 398 (read back)
 //     4096 keys, rows 32 / 128 / 256 / 384           15 / 21 / 33 / 43   21 / 22 / 25 / 26   26 / 25 / 26 / 24
-//   bf16, head_dim 512, 8/2 heads, 16384 keys, rows 256 / 512 / 768:  108 / 202 / 296, read back 224
+//   The thresholds of head_dim 128 are those of 8 kv heads (8/8 heads within 4% of 32/8).  With
+//   few kv heads the decode kernel would be the faster one for longer, up to some 400 rows *
+//   kv heads, which this rule leaves unused (decode / codes / read back):
+//     1 kv head, 16384 keys, rows 64 / 256 / 512     11 / 50 / 45   16 / 55 / 47   26 / 38 / 49
+//     1 kv head, 63488 keys, rows 64 / 256 / 512     18 / 56 / 89   42 / 61 / 91   76 / 52 / 61
+//     2 kv heads, 16384 keys, rows 64 / 256 / 512    12 / 34 / 51   26 / 39 / 51   44 / 32 / 38
+//     2 kv heads, 63488 keys, rows 64 / 256 / 512    26 / 46 / 69   77 / 52 / 68   144 / 52 / 64
+//   bf16, head_dim 512, 16384 keys (decode / read back), the rule's last rows of decode and the next:
+//     1 kv head, rows 1024 / 1536      195 / 219   290 / 219
+//     2 kv heads, rows 512 / 768       196 / 225   292 / 225
+//     4 kv heads, rows 256 / 512       197 / 240   385 / 240
+//     (4096 keys: 56 / 63 and 83 / 63, 58 / 65 and 85 / 65, 58 / 67 and 109 / 67)
 // fp32 always runs the decode kernel: pfa_f32x3_d128.cu on rows read back is faster from
 // some 600 rows on (16384 keys, 32/8 heads, 768 rows: 360 us against 398), but its split
 // into bf16 parts and its long sums leave up to 6e-5 of the output, six times what a

@@ -29,9 +29,9 @@
 // issue; 16 warps are launched with 128 registers a thread and split them
 // 200 / 200 / 72 / 40 by warpgroup (512 = 4 * 128).
 //
-// Measured on GB300: 128 tokens at 63360, 32/8 heads, 126.3 us (floor 69.5 us of tensor
-// time; reading the cache back and running the 16-bit kernel takes 160 us, 60 of them
-// for the 390 MB of the read-back).  A key tile of a pair takes 3600 cycles: 2200 of
+// Measured on GB300: 128 tokens at 63360, 32/8 heads, 124 us in a graph, 129 through Python
+// (floor 69.5 us of tensor time; reading the cache back and running the 16-bit kernel takes
+// 153 us, 60 of them for the 390 MB of the read-back).  A key tile of a pair takes 3600 cycles: 2200 of
 // tensor work, 900 of waiting for tile A's weights (the softmax's chain, which the
 // converters on the same schedulers lengthen: 2900 cycles a tile in pfa_bf16_d128.cu)
 // and 350 for operand tiles.  From about 1000 rows a kv head on the read-back costs

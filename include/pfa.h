@@ -396,7 +396,8 @@ PFA_API int pfa_prefill_attention_noalloc(const void *q, const void *k_cache,
  *           block of `block` consecutive rows (16, 32, 64 or 128; max_seq_len is
  *           a multiple of it)
  * and stands for code * scale.  Scales are powers of two as
- * pfa_cache_write_q8 makes them (0 for a block of zeros).  Key j of a sequence
+ * pfa_cache_write_q8 makes them (0 for a block of zeros); any others are rounded to
+ * 11 bits by the tensor-core kernel of pfa_prefill_attention_q8.  Key j of a sequence
  * is in row j; one sequence's part (a slot) is itself a cache with B = 1.
  * Code pointers are 16-byte aligned, max_seq_len * head_dim may pass 2^31.
  *
@@ -412,7 +413,8 @@ PFA_API int pfa_prefill_attention_noalloc(const void *q, const void *k_cache,
  *
  * Row b * T + t of a token-major array starts at (b * T + t) * its stride
  * (elements; stride * element size a multiple of 16 bytes), heads and elements
- * dense inside it, so columns of one projection buffer can be passed.
+ * dense inside it, so columns of one projection buffer can be passed.  Such arrays and
+ * the norm's weights are 16-byte aligned.
  *
  * All calls are asynchronous on `stream`, allocate nothing, and give
  * results that are a deterministic function of their inputs.  As for
@@ -454,7 +456,7 @@ PFA_API int pfa_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_
  * pfa_cache_write_q8 -- quantise T new tokens of each sequence into its cache.
  *
  *   k, v    [B * T] rows of num_kv_heads heads of head_dim elements (dtype),
- *           k_stride (v_stride) elements apart.
+ *           k_stride (v_stride) elements apart.  T <= max_seq_len, padding included.
  *   k8, v8, k_scale, v_scale   the cache; written in place.
  *   head_dim  a multiple of 16 up to 512.
  * For each head and block that new rows touch, with low the first new position:
