@@ -254,7 +254,7 @@ def run(s):
             return pfa.cache_read_q4(cache, case["start"], case["stop"], dtype=DTYPES[case["dtype"]])
         if op == "decode":
             o = pfa.decode_attention_q4(s["q"], cache, s["lengths"], weights=s.get("weights"), window=case["window"])
-            return [o] + [s["weights"]] * case["weights"]
+            return [o] + ([s["weights"]] if case["weights"] else [])
         if op == "evict":
             n, rows = pfa.cache_evict_q4(cache, s["weights"], s["lengths"], case["keep"], recent=case["recent"])
             return [n, rows, s["weights"]] + s["cache"]
