@@ -31,7 +31,10 @@ EXPORTS = ("pfa_prefill_attention", "pfa_prefill_attention_ws", "pfa_workspace_b
            "pfa_debug_check_schedule", "pfa_debug_check_schedule_d512",
            "pfa_qk_norm_rope", "pfa_cache_write_q8", "pfa_cache_read_q8",
            "pfa_decode_attention_q8", "pfa_decode_workspace_bytes_q8",
-           "pfa_prefill_attention_q8", "pfa_prefill_workspace_bytes_q8")
+           "pfa_prefill_attention_q8", "pfa_prefill_workspace_bytes_q8",
+           "pfa_cache_write_q4", "pfa_cache_read_q4", "pfa_decode_attention_q4",
+           "pfa_decode_workspace_bytes_q4", "pfa_prefill_attention_q4",
+           "pfa_prefill_workspace_bytes_q4", "pfa_cache_evict_q4")
 
 _lock = threading.Lock()
 _lib = None
@@ -116,7 +119,22 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                                  i32, f32, i32, i64, i64, i32, vp, sz, vp]
         lib.pfa_prefill_workspace_bytes_q8.argtypes = [i64, i64, i32, i32, i32, i32, i32,
                                                        ctypes.POINTER(sz)]
-        for name in EXPORTS[-7:]:
+        lib.pfa_cache_write_q4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, i32, i32,
+                                           i64, i32, i32, i32, i64, i64, vp]
+        lib.pfa_cache_read_q4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i64, i32,
+                                          i32, i32, i64, vp]
+        lib.pfa_decode_attention_q4.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32,
+                                                i32, i32, i32, f32, i32, i64, i64, i64, i32, i32,
+                                                vp, sz, vp]
+        lib.pfa_decode_workspace_bytes_q4.argtypes = [i64, i64, i32, i32, i32, i32, i64, i32,
+                                                      ctypes.POINTER(sz)]
+        lib.pfa_prefill_attention_q4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32,
+                                                 i32, f32, i32, i64, i64, i32, i32, vp, sz, vp]
+        lib.pfa_prefill_workspace_bytes_q4.argtypes = [i64, i64, i32, i32, i32, i32, i32,
+                                                       ctypes.POINTER(sz)]
+        lib.pfa_cache_evict_q4.argtypes = [vp, vp, vp, vp, vp, i64, vp, i32, i32, i64, i64, i64,
+                                           vp, vp, vp]
+        for name in EXPORTS[-14:]:
             getattr(lib, name).restype = i32
         if path is None:
             _lib = lib

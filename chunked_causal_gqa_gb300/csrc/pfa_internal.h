@@ -223,4 +223,70 @@ int launch_decode_q8(const DecodeQ8Call& c);
 size_t q8_d128_workspace(int64_t T, int64_t start_pos, int H, int Hkv, int window, int num_sms);
 int launch_q8_d128(const DecodeQ8Call& c);
 
+// ---- operators around the 4-bit cache (checked by pfa_q4_api.cu)
+
+// A 4-bit cache: e2m1 codes [B][Hkv][max_seq_len][D / 2], two to a byte, and e4m3 scales
+// [B][Hkv][max_seq_len][D / 16] for K and for V; values are code * scale * 2^exponent.
+struct CacheQ4 {
+  void *k4, *v4, *k_scale, *v_scale;
+  int64_t max_seq_len;
+  int k_exp, v_exp;
+};
+
+struct WriteQ4Call {
+  const void *k, *v;
+  CacheQ4 cache;
+  Span span;
+  int Hkv, D, dtype;
+  int64_t k_row, v_row;
+  unsigned* err;
+  cudaStream_t stream;
+};
+int launch_cache_write_q4(const WriteQ4Call& c);
+
+struct ReadQ4Call {
+  CacheQ4 cache;
+  void *k_out, *v_out;
+  int64_t heads, start, rows;       // heads: B * Hkv blocks of max_seq_len rows
+  int64_t out_head;                 // elements from one head's rows to the next in the outputs
+  int D, dtype;
+  cudaStream_t stream;
+};
+int launch_cache_read_q4(const ReadQ4Call& c);
+
+struct DecodeQ4Call {
+  const void* q;
+  void* out;
+  float* weights;                   // null: none
+  CacheQ4 cache;
+  Span span;
+  int H, Hkv, D, window, dtype;
+  float scale;
+  int64_t q_row, out_row;
+  unsigned* err;
+  int num_sms;
+  int device;
+  void* ws;
+  cudaStream_t stream;
+};
+// Workspace bytes of launch_decode_q4 for T tokens of each of B sequences.
+size_t decode_q4_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int64_t cap,
+                           bool weights, int num_sms);
+int launch_decode_q4(const DecodeQ4Call& c);
+
+struct EvictQ4Call {
+  CacheQ4 cache;
+  float* weights;
+  int64_t B;
+  const int64_t* lengths;
+  int Hkv, D;
+  int64_t keep, recent;
+  int64_t* lengths_out;
+  int32_t* rows_out;
+  unsigned* err;
+  int num_sms;
+  cudaStream_t stream;
+};
+int launch_cache_evict_q4(const EvictQ4Call& c);
+
 }  // namespace pfa

@@ -1,49 +1,13 @@
 // pfa_q8_api.cu -- the C entry points of the operators around the 8-bit cache
 // (declared in include/pfa.h): argument checks and dispatch.  Checks that need
 // no device come first, so that a bad call is refused on any machine.
-#include "pfa_internal.h"
-
-#include "../../include/pfa.h"
+#include "pfa_checks.h"
 
 #include <algorithm>
 #include <cmath>
 
 namespace pfa {
 namespace {
-
-constexpr int64_t kMaxLen = ((int64_t)1 << 31) - 4096;  // positions and row counts
-
-size_t elem(int dtype) { return dtype == PFA_F32 ? 4 : 2; }
-bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) & (a - 1); }
-size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-// n rows of `width` bytes, `pitch` bytes apart.
-struct Rows {
-  const void* p;
-  int64_t n;
-  size_t pitch, width;
-  size_t span() const { return (size_t)(n - 1) * pitch + width; }
-};
-
-// Whether two sets of rows share a byte.  Columns of one buffer (the same
-// pitch) are told apart by their column ranges; anything else by its span.
-bool share(const Rows& a, const Rows& b) {
-  if (!overlaps(a.p, a.span(), b.p, b.span())) return false;
-  if (a.pitch != b.pitch) return true;
-  const int64_t pitch = (int64_t)a.pitch;
-  int64_t d = ((int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p))) % pitch;
-  if (d < 0) d += pitch;  // b's first column in a's rows
-  return d < (int64_t)a.width || d + (int64_t)b.width > pitch;
-}
-
-int check_span(int64_t B, int64_t T, int64_t start_pos, const int64_t* lengths) {
-  if (B < 0 || T < 0 || B > kMaxLen || T > kMaxLen || B * T > kMaxLen) return PFA_ERR_SHAPE;
-  if (lengths) return misaligned(lengths, 8) ? PFA_ERR_ALIGNMENT : PFA_OK;
-  // without lengths: one sequence, its position known to the host
-  if (B > 1 || start_pos < 0 || start_pos > kMaxLen || start_pos + T > kMaxLen)
-    return PFA_ERR_SHAPE;
-  return PFA_OK;
-}
 
 // The shape of an 8-bit cache of `heads` blocks of rows.
 int check_cache(int64_t heads, int head_dim, int64_t cap, int block) {
@@ -76,15 +40,6 @@ CacheQ8 cache_of(const void* k8, const void* v8, const float* k_scale, const flo
                  int64_t cap, int block) {
   return CacheQ8{const_cast<void*>(k8), const_cast<void*>(v8), const_cast<float*>(k_scale),
                  const_cast<float*>(v_scale), cap, block};
-}
-
-// Shapes of the attention entries.
-int check_attention(int64_t B, int64_t T, int H, int Hkv, int D, float scale, int dtype) {
-  if (dtype != PFA_F32 && dtype != PFA_BF16) return PFA_ERR_DTYPE;
-  if (B < 0 || T < 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || H / Hkv > 128) return PFA_ERR_SHAPE;
-  if (D != 128 && D != 512) return PFA_ERR_SHAPE;
-  if (!std::isfinite(scale)) return PFA_ERR_VALUE;
-  return PFA_OK;
 }
 
 // How a chunk of one sequence runs: few rows, and all of fp32, by the decode kernel; the

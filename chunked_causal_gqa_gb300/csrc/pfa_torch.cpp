@@ -1,4 +1,4 @@
-// pfa_torch.cpp -- the Python side of the operators around the 8-bit cache: a
+// pfa_torch.cpp -- the Python side of the operators around the 8-bit and 4-bit caches: a
 // CPython module that checks torch tensors, allocates outputs and workspaces from
 // torch's allocator and calls the C entry points of libpfa.so.
 //
@@ -369,6 +369,217 @@ PyObject* prefill(PyObject* const* a) {
   return fresh ? THPVariable_Wrap(out) : Py_NewRef(a[2]);
 }
 
+// ------------------------------------------------------------------ the 4-bit cache
+
+struct Cache4 {
+  void *k, *v, *ks, *vs;
+  int64_t batch, cap;  // batch 0: no batch dimension
+  int heads, D, k_exp, v_exp;
+  const at::Tensor* first;
+  bool batched() const { return first->dim() == 4; }
+};
+Cache4 cache4_of(PyObject* o) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 6) refuse("cache must be a Q4Cache");
+  const at::Tensor& k = tensor(PyTuple_GET_ITEM(o, 0));
+  const at::Tensor& v = tensor(PyTuple_GET_ITEM(o, 1));
+  const at::Tensor& ks = tensor(PyTuple_GET_ITEM(o, 2));
+  const at::Tensor& vs = tensor(PyTuple_GET_ITEM(o, 3));
+  const int64_t n = k.dim();
+  if ((n != 3 && n != 4) || v.sizes() != k.sizes() || k.size(n - 1) == 0 || k.size(n - 1) % 8)
+    refuse("cache.k and cache.v must be [(B,) Hkv, max_seq_len, D / 2] of one shape, D a multiple of 16");
+  if (k.scalar_type() != at::kByte || v.scalar_type() != at::kByte)
+    refuse("cache.k and cache.v must be uint8");
+  if (ks.scalar_type() != at::kFloat8_e4m3fn || vs.scalar_type() != at::kFloat8_e4m3fn)
+    refuse("cache.k_scale and cache.v_scale must be float8_e4m3fn");
+  if (ks.dim() != n || ks.sizes().slice(0, n - 1) != k.sizes().slice(0, n - 1) ||
+      ks.size(n - 1) != k.size(n - 1) / 8 || vs.sizes() != ks.sizes())
+    refuse("scales must be [(B,) Hkv, max_seq_len, D / 16]");
+  if (!k.is_contiguous() || !v.is_contiguous() || !ks.is_contiguous() || !vs.is_contiguous())
+    refuse("the cache's tensors must be contiguous");
+  return Cache4{k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n == 4 ? k.size(0) : 0,
+                k.size(n - 2), narrow(k.size(n - 3)), narrow(2 * k.size(n - 1)),
+                narrow(integer(PyTuple_GET_ITEM(o, 4))), narrow(integer(PyTuple_GET_ITEM(o, 5))), &k};
+}
+
+// The accumulated weights of a batch's cache.
+float* weights_of(PyObject* o, const Cache4& c) {
+  const char* why = "weights must be a contiguous float32 tensor [B, Hkv, max_seq_len]";
+  const at::Tensor& t = tensor(o, why);
+  if (t.scalar_type() != at::kFloat || t.dim() != 3 || t.size(0) != c.batch ||
+      t.size(1) != c.heads || t.size(2) != c.cap || !t.is_contiguous())
+    refuse(why);
+  return static_cast<float*>(t.data_ptr());
+}
+
+// (k, v, cache, start_pos, lengths) -> None
+PyObject* cache_write_q4(PyObject* const* a) {
+  const Cache4 c = cache4_of(a[2]);
+  const at::Tensor &k = tensor(a[0]), &v = tensor(a[1]);
+  const int64_t n = k.dim();
+  if (n != (c.batched() ? 4 : 3) || v.sizes() != k.sizes() || k.size(n - 1) != c.D ||
+      k.size(n - 2) != c.heads || (n == 4 && k.size(0) != c.batch))
+    refuse("k and v must be [(B,) T, Hkv, D] for the cache's heads and batch");
+  const char* types = "k and v must both be float32 or both bfloat16";
+  const int dt = dtype_of(k, types);
+  if (v.scalar_type() != k.scalar_type()) refuse(types);
+  const Span s = span(k, a[4], a[3]);
+  const int64_t k_row = row_of(k), v_row = row_of(v);
+  need_cuda(k);
+  const On on(k);
+  call("pfa_cache_write_q4", [&] {
+    return pfa_cache_write_q4(k.data_ptr(), v.data_ptr(), c.k, c.v, c.ks, c.vs, s.B, s.T, s.start,
+                              s.lengths, c.heads, c.D, c.cap, c.k_exp, c.v_exp, dt, k_row, v_row,
+                              on.stream);
+  });
+  Py_RETURN_NONE;
+}
+
+// (cache, start, stop or None, bf16, k_out, v_out) -> (k, v)
+PyObject* cache_read_q4(PyObject* const* a) {
+  const Cache4 c = cache4_of(a[0]);
+  const int64_t start = integer(a[1]), stop = a[2] == Py_None ? c.cap : integer(a[2]);
+  if (start < 0 || start > stop || stop > c.cap) refuse("the rows are not in the cache");
+  const at::ScalarType type = truth(a[3]) ? at::kBFloat16 : at::kFloat;
+  const int64_t rows = stop - start;
+  const int64_t shape[4] = {c.batch, c.heads, rows, c.D};
+  const at::IntArrayRef want(shape + (c.batched() ? 0 : 1), c.batched() ? 4 : 3);
+  for (int i = 4; i < 6; ++i)
+    if (a[i] != Py_None) {
+      const at::Tensor& t = tensor(a[i]);
+      if (t.sizes() != want || t.scalar_type() != type || !t.is_contiguous())
+        refuse("k_out and v_out must be contiguous [(B,) Hkv, rows, D] of dtype");
+    }
+  need_cuda(*c.first);
+  const On on(*c.first);
+  const at::Tensor k = a[4] == Py_None ? empty(want, type, *c.first) : tensor(a[4]);
+  const at::Tensor v = a[5] == Py_None ? empty(want, type, *c.first) : tensor(a[5]);
+  call("pfa_cache_read_q4", [&] {
+    return pfa_cache_read_q4(c.k, c.v, c.ks, c.vs, k.data_ptr(), v.data_ptr(),
+                             c.batched() ? c.batch * c.heads : c.heads, start, rows, c.D, c.cap,
+                             c.k_exp, c.v_exp, type == at::kFloat ? PFA_F32 : PFA_BF16,
+                             rows * c.D, on.stream);
+  });
+  PyObject* out = PyTuple_New(2);
+  if (!out) throw Raised{};
+  PyTuple_SET_ITEM(out, 0, a[4] == Py_None ? THPVariable_Wrap(k) : Py_NewRef(a[4]));
+  PyTuple_SET_ITEM(out, 1, a[5] == Py_None ? THPVariable_Wrap(v) : Py_NewRef(a[5]));
+  return out;
+}
+
+// (q, cache, lengths, out, weights, window, scale, workspace) -> out
+PyObject* decode_q4(PyObject* const* a) {
+  const Cache4 c = cache4_of(a[1]);
+  const at::Tensor& q = tensor(a[0]);
+  if (q.dim() != 4 || !c.batched() || q.size(0) != c.batch || q.size(3) != c.D)
+    refuse("q must be [B, T, H, D] for the cache's batch and head_dim");
+  const int dt = dtype_of(q, "q must be float32 or bfloat16");
+  const int H = narrow(q.size(2)), window = narrow(integer(a[5]));
+  const Span s = span(q, a[2], Py_None);
+  const bool fresh = a[3] == Py_None;
+  if (!fresh && (tensor(a[3]).sizes() != q.sizes() || tensor(a[3]).scalar_type() != q.scalar_type()))
+    refuse("out must match q in shape and dtype");
+  float* weights = a[4] == Py_None ? nullptr : weights_of(a[4], c);
+  const int64_t q_row = row_of(q);
+  const float scale = scale_of(a[6], c.D);
+  need_cuda(q);
+  const On on(q);
+  const at::Tensor out = fresh ? empty(q.sizes(), q.scalar_type(), q) : tensor(a[3]);
+  const int64_t out_row = row_of(out);
+  size_t need = 0;
+  if (a[7] == Py_None)
+    call("pfa_decode_workspace_bytes_q4", [&] {
+      return pfa_decode_workspace_bytes_q4(s.B, s.T, H, c.heads, c.D, dt, c.cap, weights != nullptr,
+                                           &need);
+    });
+  const Workspace ws(a[7], need, q);
+  call("pfa_decode_attention_q4", [&] {
+    return pfa_decode_attention_q4(q.data_ptr(), c.k, c.v, c.ks, c.vs, out.data_ptr(), weights, s.B,
+                                   s.T, s.lengths, H, c.heads, c.D, window, scale, dt, q_row,
+                                   out_row, c.cap, c.k_exp, c.v_exp, ws.p, ws.n, on.stream);
+  });
+  return fresh ? THPVariable_Wrap(out) : Py_NewRef(a[3]);
+}
+
+// (q, cache, out, start_pos, window, scale, workspace) -> out
+PyObject* prefill_q4(PyObject* const* a) {
+  const Cache4 c = cache4_of(a[1]);
+  const at::Tensor& q = tensor(a[0]);
+  if (q.dim() != 3 || c.batched() || q.size(2) != c.D)
+    refuse("q must be [T, H, D] for one sequence's cache (Q4Cache.slot)");
+  const int dt = dtype_of(q, "q must be float32 or bfloat16");
+  const int64_t T = q.size(0), start = integer(a[3]);
+  const int H = narrow(q.size(1)), window = narrow(integer(a[4]));
+  const int64_t row = row_of(q);
+  const bool fresh = a[2] == Py_None;
+  if (!fresh) {
+    const at::Tensor& o = tensor(a[2]);
+    if (o.sizes() != q.sizes() || o.scalar_type() != q.scalar_type() ||
+        (T > 1 ? o.strides() != q.strides() : row_of(o) != row))
+      refuse("out must match q in shape, strides and dtype");
+  }
+  const float scale = scale_of(a[5], c.D);
+  need_cuda(q);
+  const On on(q);
+  const at::Tensor out =
+      fresh ? at::Tensor(at::detail::empty_strided_cuda(q.sizes(), q.strides(), q.scalar_type(),
+                                                        q.device()))
+            : tensor(a[2]);
+  size_t need = 0;
+  if (a[6] == Py_None)
+    call("pfa_prefill_workspace_bytes_q4", [&] {
+      return pfa_prefill_workspace_bytes_q4(T, start, H, c.heads, c.D, window, dt, &need);
+    });
+  const Workspace ws(a[6], need, q);
+  call("pfa_prefill_attention_q4", [&] {
+    return pfa_prefill_attention_q4(q.data_ptr(), c.k, c.v, c.ks, c.vs, out.data_ptr(), T, start, H,
+                                    c.heads, c.D, window, scale, dt, row, c.cap, c.k_exp, c.v_exp,
+                                    ws.p, ws.n, on.stream);
+  });
+  return fresh ? THPVariable_Wrap(out) : Py_NewRef(a[2]);
+}
+
+// (cache, weights, lengths, keep, recent, lengths_out, rows_out) -> (lengths_out, rows_out)
+PyObject* cache_evict_q4(PyObject* const* a) {
+  const Cache4 c = cache4_of(a[0]);
+  if (!c.batched()) refuse("cache must be of a batch");
+  float* weights = weights_of(a[1], c);
+  const char* why = "lengths and lengths_out must be contiguous int64 tensors [B]";
+  auto lengths_of = [&](PyObject* o) -> const at::Tensor& {
+    const at::Tensor& t = tensor(o, why);
+    if (t.scalar_type() != at::kLong || t.dim() != 1 || t.size(0) != c.batch || !t.is_contiguous())
+      refuse(why);
+    return t;
+  };
+  const at::Tensor& n = lengths_of(a[2]);
+  const int64_t keep = integer(a[3]), recent = integer(a[4]);
+  if (keep < 1 || keep > c.cap || recent < 0 || recent > keep)
+    refuse("keep must be 1 .. max_seq_len and recent 0 .. keep");
+  if (a[5] != Py_None) lengths_of(a[5]);
+  const int64_t shape[3] = {c.batch, c.heads, keep};
+  if (a[6] != Py_None) {
+    const char* what = "rows_out must be a contiguous int32 tensor [B, Hkv, keep]";
+    const at::Tensor& t = tensor(a[6], what);
+    if (t.scalar_type() != at::kInt || t.sizes() != at::IntArrayRef(shape, 3) || !t.is_contiguous())
+      refuse(what);
+  }
+  need_cuda(*c.first);
+  const On on(*c.first);
+  const at::Tensor left = a[5] == Py_None ? empty(n.sizes(), at::kLong, *c.first) : tensor(a[5]);
+  const at::Tensor rows =
+      a[6] == Py_None ? empty(at::IntArrayRef(shape, 3), at::kInt, *c.first) : tensor(a[6]);
+  call("pfa_cache_evict_q4", [&] {
+    return pfa_cache_evict_q4(c.k, c.v, c.ks, c.vs, weights, c.batch,
+                              static_cast<const int64_t*>(n.data_ptr()), c.heads, c.D, c.cap, keep,
+                              recent, static_cast<int64_t*>(left.data_ptr()),
+                              static_cast<int32_t*>(rows.data_ptr()), on.stream);
+  });
+  PyObject* out = PyTuple_New(2);
+  if (!out) throw Raised{};
+  PyTuple_SET_ITEM(out, 0, a[5] == Py_None ? THPVariable_Wrap(left) : Py_NewRef(a[5]));
+  PyTuple_SET_ITEM(out, 1, a[6] == Py_None ? THPVariable_Wrap(rows) : Py_NewRef(a[6]));
+  return out;
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -395,7 +606,12 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<norm_rope, 12>("qk_norm_rope"), method<cache_write, 5>("cache_write"),
                            method<cache_read, 6>("cache_read"), method<decode, 7>("decode"),
-                           method<prefill, 7>("prefill"), {nullptr, nullptr, 0, nullptr}};
+                           method<prefill, 7>("prefill"),
+                           method<cache_write_q4, 5>("cache_write_q4"),
+                           method<cache_read_q4, 6>("cache_read_q4"),
+                           method<decode_q4, 8>("decode_q4"),
+                           method<prefill_q4, 7>("prefill_q4"),
+                           method<cache_evict_q4, 7>("cache_evict_q4"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_pfa_torch", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 

@@ -545,6 +545,123 @@ PFA_API int pfa_prefill_workspace_bytes_q8(int64_t T, int64_t start_pos, int num
                                            int num_kv_heads, int head_dim, int window, int dtype,
                                            size_t *bytes);
 
+/*
+ * Operators around a 4-bit KV cache
+ * =================================
+ *
+ * The 4-bit cache of B sequences holds, for K and for V,
+ *   codes   [B][num_kv_heads][max_seq_len][head_dim / 2] bytes: two e2m1 codes each
+ *           (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), channel 2 i in the low
+ *           four bits of byte i
+ *   scales  [B][num_kv_heads][max_seq_len][head_dim / 16] e4m3, one for each 16 channels
+ *           of a row
+ * and stands for code * scale * 2^exponent, with one exponent for all of K and one for all of
+ * V (k_exp, v_exp: -64 .. 64, the same in every call on a cache): 4.5 bits a value.  An e4m3
+ * scale is a full three bits fine from 2^-6 up to 448; the exponent puts the values of a layer there.
+ * Rows do not depend on one another: appending one changes no other, and a row can be
+ * moved as it is.  Scale pointers are aligned to the largest power of two in head_dim / 16 (up
+ * to 16 bytes), code pointers to eight times that (up to 16 bytes).  Everything said above of the 8-bit cache's lengths, token rows, streams and
+ * errors holds here too.
+ */
+
+/*
+ * pfa_cache_write_q4 -- quantise T new tokens of each sequence into its cache.
+ *
+ *   k, v    [B * T] rows of num_kv_heads heads of head_dim elements (dtype),
+ *           k_stride (v_stride) elements apart.  T <= max_seq_len, padding included.
+ *   k4, v4, k_scale, v_scale   the cache; written in place.
+ *   head_dim  a multiple of 16 up to 512.
+ * For each 16 channels of a row, with y = x * 2^-exponent:
+ *   scale = e4m3(max |y| / 6),  code = e2m1(y / scale)   (0 where the scale is 0)
+ * both to the nearest, ties to even, the largest value beyond it.  16 channels with one that is
+ * not finite get a NaN scale and codes of 0.  Only the new rows are written.
+ */
+PFA_API int pfa_cache_write_q4(const void *k, const void *v, void *k4, void *v4, void *k_scale,
+                               void *v_scale, int64_t B, int64_t T, int64_t start_pos,
+                               const int64_t *lengths, int num_kv_heads, int head_dim,
+                               int64_t max_seq_len, int k_exp, int v_exp, int dtype,
+                               int64_t k_stride, int64_t v_stride, void *stream);
+
+/*
+ * pfa_cache_read_q4 -- rows start .. start + rows - 1 of every head as dtype:
+ * k_out, v_out [heads] blocks of [rows][head_dim] elements, out_head_stride
+ * elements apart; heads = B * num_kv_heads.  Exact within the type's range.
+ */
+PFA_API int pfa_cache_read_q4(const void *k4, const void *v4, const void *k_scale,
+                              const void *v_scale, void *k_out, void *v_out, int64_t heads,
+                              int64_t start, int64_t rows, int head_dim, int64_t max_seq_len,
+                              int k_exp, int v_exp, int dtype, int64_t out_head_stride,
+                              void *stream);
+
+/*
+ * pfa_decode_attention_q4 -- attention of the T newest tokens of each of B
+ * sequences over its 4-bit cache: the operation of pfa_decode_attention_q8, with the same
+ * arguments but for
+ *   weights   NULL, or device fp32 [B][num_kv_heads][max_seq_len]: each row's
+ *             softmax weights, summed over the call's tokens and the query heads of the kv
+ *             head, are added to it in place.  Rows that no token sees are not touched.
+ *             A key's total is what pfa_cache_evict_q4 goes by.
+ *   workspace of pfa_decode_workspace_bytes_q4 bytes: with weights it holds each score
+ *             (4 bytes for each row of the T * num_heads / num_kv_heads and cache row).
+ * Weights of the sum over V are rounded to 11 bits (bf16) or 21 (fp32); the accumulated ones
+ * are not rounded below fp32.
+ */
+PFA_API int pfa_decode_attention_q4(const void *q, const void *k4, const void *v4,
+                                    const void *k_scale, const void *v_scale, void *out,
+                                    float *weights, int64_t B, int64_t T, const int64_t *lengths,
+                                    int num_heads, int num_kv_heads, int head_dim, int window,
+                                    float scale, int dtype, int64_t q_stride, int64_t out_stride,
+                                    int64_t max_seq_len, int k_exp, int v_exp, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+PFA_API int pfa_decode_workspace_bytes_q4(int64_t B, int64_t T, int num_heads, int num_kv_heads,
+                                          int head_dim, int dtype, int64_t max_seq_len,
+                                          int weights, size_t *bytes);
+
+/*
+ * pfa_prefill_attention_q4 -- pfa_prefill_attention_cache (linear) on one
+ * sequence's 4-bit cache: T tokens at start_pos .., whose own rows have been
+ * written.  q and out rows are qkv_dim elements apart.  Few rows T * num_heads /
+ * num_kv_heads, and all of fp32, run the kernel of pfa_decode_attention_q4; longer bf16 chunks
+ * read the visible rows back into the workspace and run the 16-bit kernels on them.
+ * workspace: pfa_prefill_workspace_bytes_q4 bytes, 256-byte aligned, not shared by calls that
+ * can run at the same time.
+ */
+PFA_API int pfa_prefill_attention_q4(const void *q, const void *k4, const void *v4,
+                                     const void *k_scale, const void *v_scale, void *out,
+                                     int64_t T, int64_t start_pos, int num_heads,
+                                     int num_kv_heads, int head_dim, int window, float scale,
+                                     int dtype, int64_t qkv_dim, int64_t max_seq_len, int k_exp,
+                                     int v_exp, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+PFA_API int pfa_prefill_workspace_bytes_q4(int64_t T, int64_t start_pos, int num_heads,
+                                           int num_kv_heads, int head_dim, int window, int dtype,
+                                           size_t *bytes);
+
+/*
+ * pfa_cache_evict_q4 -- cut each sequence of more than `keep` rows down to `keep`: for
+ * each kv head the `recent` newest rows stay, and of the others the heaviest by
+ * `weights` (equal ones: the lower row).  Kept rows move down to rows 0 .. keep - 1 in their
+ * order, codes and scales and weights; weights of rows keep .. lengths[b] - 1
+ * become 0, so that new tokens start there with none.  Rows behind are left as they
+ * are.  Sequences of at most `keep` rows are not changed.
+ *
+ *   weights      device fp32 [B][num_kv_heads][max_seq_len], updated in place.  NaN counts as
+ *                larger than any number.
+ *   lengths      device, B int64.
+ *   keep, recent 1 <= keep <= max_seq_len, 0 <= recent <= keep.
+ *   lengths_out  device, B int64: min(lengths[b], keep); may be lengths.  (A length out of
+ *                range is handed on, with PFA_ERR_LENGTHS recorded.)
+ *   rows_out     device int32 [B][num_kv_heads][keep]: the row that each kept row was,
+ *                -1 behind a shorter sequence's last.
+ *   head_dim     a multiple of 16 up to 512.
+ * Heads keep different rows, so a row's number is no position any more: positions for
+ * pfa_qk_norm_rope are counted apart, and a window counts rows.
+ */
+PFA_API int pfa_cache_evict_q4(void *k4, void *v4, void *k_scale, void *v_scale, float *weights,
+                               int64_t B, const int64_t *lengths, int num_kv_heads, int head_dim,
+                               int64_t max_seq_len, int64_t keep, int64_t recent,
+                               int64_t *lengths_out, int32_t *rows_out, void *stream);
+
 /* Human-readable name of a pfa_status value (static storage, never NULL). */
 PFA_API const char *pfa_status_string(int status);
 
@@ -553,7 +670,7 @@ PFA_API const char *pfa_status_string(int status);
  * device-side error word of the current device: PFA_OK, PFA_ERR_TIMEOUT if
  * a kernel launched since the last call gave up on a wait, or
  * PFA_ERR_LENGTHS if a pfa_prefill_attention_graph launch, or a launch of an
- * operator of the 8-bit cache, found its run-time lengths out of range (timeouts take precedence).  Returns
+ * operator of the 8-bit or 4-bit cache, found its run-time lengths out of range (timeouts take precedence).  Returns
  * PFA_ERR_DEVICE if the stream cannot be synchronised (the CUDA error is then
  * the runtime's).
  */
