@@ -51,91 +51,29 @@
 // area, 49.7 / 45.8 / 10.9.
 // A long fp32 chunk is bound by instructions: 2048 tokens at 14336, 32/8 heads of 128, 3.5 ms
 // (147 TFLOP/s; plain fp32 products run at 26).
-#include "pfa_internal.h"
-#include "pfa_ptx.cuh"
-#include "pfa_q8.cuh"
+#include "pfa_decode.cuh"
 
 #include "../../include/pfa.h"
 
-#include <algorithm>
 #include <cmath>
 
 namespace pfa {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kBlocksPerSm = 2;
-constexpr int kUnit = 32;                      // keys of a unit
 constexpr int kStages = 3;
 constexpr int kHalf = kUnit * 128;             // bytes of a warp's K (or V) part of a stage
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kMaxEntries = 1 << 14;           // (sequence, row tile) pairs of one launch
-constexpr int64_t kMaxUnits = 1 << 30;         // units that a launch can list
 constexpr int kJoinBytes = kWarps * 8 * 128 * 4;  // joins: 8 row sums of 128 floats for each warp
-// What the start and end of a head cost a block, in units: its query rows, the join.
-constexpr int kHeadCost = 8;
 constexpr float kWeightScale = 16384.f;
 
-struct Params {
-  const void* q;
-  void* out;
+struct Params : ListParams {
+  static constexpr int kHeadCost = 8;
+  static constexpr bool kSums = false;
   const uint8_t *k8, *v8;
   const float *k_scale, *v_scale;
-  const int64_t* lengths;
-  int64_t T, start_pos, q_row, out_row;
-  int64_t b0;                 // first sequence and row tile of this launch
-  int tile0;
-  int cap, Hkv, window, block_shift;
-  int rows, entries;          // T * group; entries of this launch
-  Divisor group, seqs;        // H / Hkv; sequences in this launch
-  Divisor heads, joined;      // Hkv, and the second kernel's blocks for a tile's rows
-  float scale_log2;
-  unsigned* err;
-  float* parts;               // workspace: slots of partial sums
+  int block_shift;
 };
-
-// A tile of rows of one sequence and the keys that they see.
-struct Entry {
-  int64_t b;
-  int end, r0, nr;    // sequence length; first row of the tile, rows
-  int lo, hi;         // keys [lo, hi] are seen by some row
-  int u0, n;          // units u0 .. u0 + n - 1 hold them
-  bool bad;
-  // Units of a head in the list of all: its own and its start's cost.
-  __device__ int listed() const { return n > 0 ? n + kHeadCost : 0; }
-};
-
-// L2: the length is read from there, past this SM's own cache.
-template <int RM, bool L2 = false>
-__device__ __forceinline__ Entry entry_of(const Params& p, int e) {
-  Entry x;
-  const int tile = e / p.seqs;
-  x.b = p.b0 + e - tile * (int)p.seqs.by;
-  x.r0 = (p.tile0 + tile) * RM;
-  x.nr = min(RM, p.rows - x.r0);
-  const int64_t end = !p.lengths ? p.start_pos + p.T
-                      : L2       ? __ldcg((const long long*)p.lengths + x.b)
-                                 : p.lengths[x.b];
-  x.bad = end < 0 || end > p.cap;
-  x.end = x.bad ? 0 : (int)end;
-  const int first = x.end - (int)p.T;
-  x.hi = first + (x.r0 + x.nr - 1) / p.group;
-  x.lo = p.window > 0 ? max(0, first + x.r0 / p.group - p.window + 1) : 0;
-  x.u0 = x.lo / kUnit;
-  x.n = x.bad || x.hi < 0 ? 0 : x.hi / kUnit - x.u0 + 1;
-  return x;
-}
-
-// Units of a run: those of all heads over the blocks, at least one for each of
-// a block's teams.  Block c has the list's units [c * run, (c + 1) * run).
-template <int TEAMS>
-__device__ __forceinline__ int run_of(int total, int blocks) {
-  return max((int)((uint32_t)(total + blocks - 1) / (uint32_t)blocks), TEAMS);
-}
-
-// Floats of a partial-sum slot: rows of output, then {m, l} of each row.
-template <int RM, int D>
-__host__ __device__ constexpr int slot_floats() { return RM * D + RM * 2; }
 
 // Pieces of 16 bytes of a row are permuted by its place in a group of eight, so
 // that K fragments (two rows, four pieces) and V fragments (every other row, two
@@ -150,111 +88,13 @@ __device__ __forceinline__ int join_at(int d, int row) {
   return d ^ ((((d >> 5) & 3) | ((row & 1) << 2)) << 2);
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-               :: "r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
-               :: "r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t half2_of(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// a, b -> high halves and what they leave out.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 f = __half22float2(h);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = half2_of(a - f.x, b - f.y);
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Walks the units of a run that belong to one team, piece by piece: the part of
-// a head that lies in the run.  A head's list starts with kHeadCost units of no work.
-template <int RM, int TEAMS>
-struct Cursor {
-  int at, stop;        // the run from the current piece on: [at, stop)
-  int e, h;            // entry and kv head of the piece
-  Entry x;
-  int listed;          // listed units of the piece
-  int k0, kend;        // the head's units k0 .. kend - 1 are in the piece
-  int k;               // the team's current one
-  __device__ __forceinline__ void start(const Params& p, int at_, int stop_, int e_, int into,
-                                        int team) {
-    at = at_;
-    stop = stop_;
-    e = e_;
-    x = entry_of<RM>(p, e);
-    // (the clamps matter only if the lengths change under the kernel)
-    h = min((int)((uint32_t)into / (uint32_t)max(x.listed(), 1)), p.Hkv - 1);
-    piece(min(into - h * x.listed(), x.listed()), team);
-    if (kend <= k0) next_piece(p, team);
-  }
-  __device__ __forceinline__ void piece(int first, int team) {
-    listed = min(stop - at, x.listed() - first);
-    k0 = max(first - kHeadCost, 0);
-    kend = first + listed - kHeadCost;
-    k = k0 + team;
-  }
-  __device__ __forceinline__ bool done() const { return at >= stop; }
-  __device__ __forceinline__ void next_piece(const Params& p, int team) {
-#pragma unroll 1
-    do {
-      at += listed;
-      if (at >= stop) return;
-      if (++h == p.Hkv) {
-        h = 0;
-#pragma unroll 1
-        do {
-          if (++e >= p.entries) {  // only if the lengths changed under the kernel
-            at = stop;
-            return;
-          }
-          x = entry_of<RM>(p, e);
-        } while (x.n == 0);
-      }
-      piece(0, team);
-    } while (kend <= k0);
-  }
-};
-
-template <typename E>
-__device__ __forceinline__ void store_row4(E* o, float4 v) {
-  if constexpr (sizeof(E) == 4) {
-    *reinterpret_cast<float4*>(o) = v;
-  } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                              *reinterpret_cast<const uint32_t*>(&b));
-  }
-}
-
 struct Shared {
   alignas(128) uint8_t ring[kWarps][kStages][kStageBytes];
   alignas(16) uint8_t join[kJoinBytes];   // also: score exchange
   float scales[kWarps][kStages][4];       // K and V scales of a unit's two halves
   float2 ml[kWarps][16];                  // a warp's {m, l} of each row
   float vref[kWarps];
-  int sums[kWarps];
-  int first_entry, into;
+  ListShared list;
 };
 
 static_assert(kBlocksPerSm * (sizeof(Shared) + 1024) <= 228 * 1024, "shared memory of an SM");
@@ -280,67 +120,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- the list of units, and where this block's run starts in it
   int at, stop, first_entry, into;
-  if (p.entries <= 32) {   // each warp for itself, an entry a lane
-    const Entry x = entry_of<RM>(p, min(lane, p.entries - 1));
-    const int mine = lane < p.entries ? x.listed() * p.Hkv : 0;
-    if (x.bad && blockIdx.x == 0 && warp == 0) atomicOr(p.err, kErrLengths);
-    int up = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, up, o);
-      if (lane >= o) up += v;
-    }
-    const int total = __shfl_sync(0xffffffffu, up, 31);
-    const int run = run_of<TEAMS>(total, gridDim.x);
-    at = blockIdx.x * run;
-    stop = min(total, at + run);
-    if (at >= total) return;
-    first_entry = __ffs(__ballot_sync(0xffffffffu, at < up)) - 1;
-    into = at - __shfl_sync(0xffffffffu, up - mine, first_entry);
-  } else {   // thread i has the entries [i * per, (i + 1) * per)
-    const int per = (p.entries + kThreads - 1) / kThreads;
-    int mine = 0;
-#pragma unroll 1
-    for (int e = tid * per; e < min(p.entries, (tid + 1) * per); ++e) {
-      const Entry x = entry_of<RM>(p, e);
-      mine += x.listed() * p.Hkv;
-      if (x.bad && blockIdx.x == 0) atomicOr(p.err, kErrLengths);
-    }
-    int up = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, up, o);
-      if (lane >= o) up += v;
-    }
-    if (lane == 31) sm.sums[warp] = up;
-    __syncthreads();
-    int before = up - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sm.sums[w];
-      total += sm.sums[w];
-    }
-    const int run = run_of<TEAMS>(total, gridDim.x);
-    at = blockIdx.x * run;
-    stop = min(total, at + run);
-    if (at >= total) return;
-    if (before <= at && at < before + mine) {   // one thread
-      int e = tid * per, rest = at - before;
-#pragma unroll 1
-      for (;; ++e) {
-        const int n = entry_of<RM>(p, e).listed() * p.Hkv;
-        if (rest < n || e + 1 >= min(p.entries, (tid + 1) * per)) break;
-        rest -= n;
-      }
-      sm.first_entry = e;
-      sm.into = rest;
-    }
-    __syncthreads();
-    first_entry = sm.first_entry;
-    into = sm.into;
-  }
+  if (!run_start<RM, TEAMS>(p, sm.list, at, stop, first_entry, into)) return;
 
-  Cursor<RM, TEAMS> in, cu;   // copies, products
+  Cursor<Params, RM, TEAMS> in, cu;   // copies, products
   in.start(p, at, stop, first_entry, into, team);
   cu = in;
 
@@ -401,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
     src.lo = 0;
     src.hi = -1;
     if (!in.done()) {
-      const Entry& x = in.x;
+      const auto& x = in.x;
       src.key0 = (x.u0 + in.k) * kUnit;
       src.lo = x.lo;
       src.hi = x.hi;
@@ -436,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   int stage = 0, swap = 0;
 
   while (!cu.done()) {
-    const Entry x = cu.x;
+    const auto x = cu.x;
     // ---- the piece's query rows, scaled by a power of two each
     uint32_t qf[SETS][8][4];
     float srow[2];
@@ -756,192 +539,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// A block has 128 columns of one row (GROUPS warps that take the parts in turn, in the
-// blocks' order, each with a running maximum) or, with GROUPS 1, of all rows of a
-// tile, a warp each.  It joins the parts of its head, and writes the zeros of rows
-// that see nothing.
-template <typename E, int NW, int NR, int GROUPS>
-__global__ void __launch_bounds__(512) join_kernel(const Params p, int blocks) {
-  constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = 8 * NR;
-  __shared__ float4 s_sum[GROUPS > 1 ? GROUPS - 1 : 1][32];
-  __shared__ float2 s_ml[GROUPS];
-  __shared__ int s_units[16][2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int grp = warp % GROUPS;
-  const int id = blockIdx.x / NW, d = blockIdx.x % NW * 128 + lane * 4;
-  const int eh = id / p.joined, r = id - eh * (int)p.joined.by + warp / GROUPS;
-  const int e = eh / p.heads, h = eh - e * p.Hkv;
-  asm volatile("griddepcontrol.launch_dependents;");
-  // The list of units, as the first kernel counts it, while that one runs.  Its blocks let this
-  // grid start behind their own wait: whatever wrote the lengths has ended, and its writes are in
-  // L2.  (The first kernel's own results are read behind the wait below.)
-  int before = 0, total = 0;
-#pragma unroll 1
-  for (int i = tid; i < p.entries; i += blockDim.x) {
-    const int n = entry_of<RM, true>(p, i).listed() * p.Hkv;
-    total += n;
-    if (i < e) before += n;
-  }
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 0) {
-    s_units[warp][0] = before;
-    s_units[warp][1] = total;
-  }
-  __syncthreads();
-  before = total = 0;
-  for (int w = 0; w < warps; ++w) {
-    before += s_units[w][0];
-    total += s_units[w][1];
-  }
-  const Entry x = entry_of<RM, true>(p, e);
-  const int run = run_of<TEAMS>(total, blocks);
-  const int s0 = before + h * x.listed();
-  int c0 = 0, n = 0, first = 0;
-  if (x.n > 0) {
-    c0 = (int)((uint32_t)(s0 + kHeadCost) / (uint32_t)run);
-    n = (int)((uint32_t)(s0 + x.listed() - 1) / (uint32_t)run) - c0 + 1;
-    // the first block's part is its run's last piece unless its run starts in this head
-    first = c0 * run >= s0 ? 0 : 1;
-  }
-  // Every block waits, also one with nothing to do: this grid must not end before the first.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (r >= x.nr || x.bad || n == 1) return;   // n 1: stored whole
-  const int q = x.r0 + r, t = q / p.group;
-  E* to = (E*)p.out + (x.b * p.T + t) * p.out_row +
-          (int64_t)(h * (int)p.group.by + q - t * (int)p.group.by) * D + d;
-  if (n == 0) {
-    if (grp == 0) store_row4(to, make_float4(0.f, 0.f, 0.f, 0.f));
-    return;
-  }
-  float mx = -INFINITY, l = 0.f;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-  for (int i0 = grp; i0 < n; i0 += 6 * GROUPS) {
-    float4 v[6];
-    float2 ml[6];
-#pragma unroll
-    for (int j = 0; j < 6; ++j) {
-      const int i = i0 + GROUPS * j;
-      ml[j] = make_float2(-INFINITY, 0.f);
-      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < n) {
-        const float* slot =
-            p.parts + (int64_t)(2 * (c0 + i) + (i == 0 ? first : 0)) * slot_floats<RM, D>();
-        ml[j] = *reinterpret_cast<const float2*>(slot + RM * D + 2 * r);
-        v[j] = *reinterpret_cast<const float4*>(slot + r * D + d);
-      }
-    }
-    float m = mx;
-#pragma unroll
-    for (int j = 0; j < 6; ++j) m = fmaxf(m, ml[j].x);
-    const float base = m == -INFINITY ? 0.f : m;
-    const float a = exp2_fast(mx - base);
-    mx = m;
-    l *= a;
-    sum.x *= a; sum.y *= a; sum.z *= a; sum.w *= a;
-#pragma unroll
-    for (int j = 0; j < 6; ++j) {
-      const float f = exp2_fast(ml[j].x - base);
-      l = fmaf(ml[j].y, f, l);
-      sum.x = fmaf(v[j].x, f, sum.x); sum.y = fmaf(v[j].y, f, sum.y);
-      sum.z = fmaf(v[j].z, f, sum.z); sum.w = fmaf(v[j].w, f, sum.w);
-    }
-  }
-  if constexpr (GROUPS > 1) {
-    if (grp > 0) s_sum[grp - 1][lane] = sum;
-    if (lane == 0) s_ml[grp] = make_float2(mx, l);
-    __syncthreads();   // the block has one row: no warp has returned
-    if (grp > 0) return;
-  }
-  float m = mx;
-#pragma unroll
-  for (int w = 1; w < GROUPS; ++w) m = fmaxf(m, s_ml[w].x);
-  const float base = m == -INFINITY ? 0.f : m;
-  const float a = exp2_fast(mx - base);
-  l *= a;
-  sum.x *= a; sum.y *= a; sum.z *= a; sum.w *= a;
-#pragma unroll
-  for (int w = 1; w < GROUPS; ++w) {
-    const float f = exp2_fast(s_ml[w].x - base);
-    const float4 v = s_sum[w - 1][lane];
-    l = fmaf(s_ml[w].y, f, l);
-    sum.x = fmaf(v.x, f, sum.x); sum.y = fmaf(v.y, f, sum.y);
-    sum.z = fmaf(v.z, f, sum.z); sum.w = fmaf(v.w, f, sum.w);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  store_row4(to, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
-}
-
 template <typename E, int NW, int NR>
-int launch(Params p, const DecodeQ8Call& c, int64_t B) {
-  constexpr int RM = 8 * NR;
+int launch(const Params& p, const DecodeQ8Call& c) {
   static DeviceOnce once;
   const int rc = once.run(c.device, [] {
     return cudaFuncSetAttribute(decode_kernel<E, NW, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)sizeof(Shared)) == cudaSuccess ? kOk : kErrLaunch;
   });
   if (rc != kOk) return rc;
-  // A launch takes as many (sequence, row tile) entries as its list can count.
-  const int64_t of_entry = (int64_t)p.Hkv * (p.cap / kUnit + 2 + kHeadCost);
-  if (of_entry > kMaxUnits) return kErrShape;
-  const int tiles = (p.rows + RM - 1) / RM;
-  const int most = (int)std::min<int64_t>(kMaxEntries, kMaxUnits / of_entry);
-  const int tiles_at_once = std::min(tiles, most);
-  const int64_t at_once = tiles_at_once < tiles ? 1 : most / tiles;   // sequences
-  p.parts = static_cast<float*>(c.ws);
-  p.heads = divisor(p.Hkv);
-  // The first kernel may be launched before what is in front of it has ended: it waits
-  // (griddepcontrol) before it reads anything.  The second one starts when every block of the
-  // first is past that wait, and waits for the first before it reads what that writes.
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = c.stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const int most_blocks = c.num_sms * kBlocksPerSm;
-  for (int64_t b = 0; b < B; b += at_once)
-    for (int tile = 0; tile < tiles; tile += tiles_at_once) {
-      const int here = std::min(tiles_at_once, tiles - tile);
-      p.b0 = b;
-      p.tile0 = tile;
-      const int seqs = (int)std::min(at_once, B - b);
-      p.seqs = divisor(seqs);
-      p.entries = seqs * here;
-      // The list has all sequences' first row tiles, then all second ones: with a number of
-      // blocks that the tiles divide, blocks far apart read the same keys at the same time and
-      // the cache comes from HBM once (32 sequences of 8192 keys, 32/8 heads of 128, 8 / 12 / 20
-      // tokens: 159 / 244 / 370 us; each sequence's tiles in a row 172 / 247 / -, tiles that
-      // do not divide the blocks - / 254 / 407).
-      const int blocks = here <= 16 ? most_blocks - most_blocks % here : most_blocks;
-      // A head has about blocks / heads parts: for many of them eight warps to a row, for
-      // few a warp (32 sequences of 8 heads: 49.7 us for both kernels with eight, 46.3 with one).
-      const int rows = std::min(RM, p.rows);
-      const bool many = (int64_t)p.entries * p.Hkv * 8 <= blocks;
-      p.joined = divisor(many ? rows : 1);
-      const int64_t joins = (int64_t)p.entries * p.Hkv * p.joined.by * NW;
-      if (joins > 0x7fffffff) return kErrShape;
-      cfg.gridDim = dim3((unsigned)blocks);
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = sizeof(Shared);
-      cudaError_t err = cudaLaunchKernelEx(&cfg, decode_kernel<E, NW, NR>, (const Params)p);
-      if (err == cudaSuccess) {
-        cfg.gridDim = dim3((unsigned)joins);
-        cfg.blockDim = dim3(many ? 256 : rows * 32);
-        cfg.dynamicSmemBytes = 0;
-        err = many ? cudaLaunchKernelEx(&cfg, join_kernel<E, NW, NR, 8>, (const Params)p, blocks)
-                   : cudaLaunchKernelEx(&cfg, join_kernel<E, NW, NR, 1>, (const Params)p, blocks);
-      }
-      if (err != cudaSuccess) {
-        cudaGetLastError();
-        return kErrLaunch;
-      }
-    }
-  return kOk;
+  const Kernels<Params> k = {decode_kernel<E, NW, NR>, join_kernel<Params, E, NW, 8 * NR, 8>,
+                             join_kernel<Params, E, NW, 8 * NR, 1>, 8 * NR, NW, kBlocksPerSm,
+                             sizeof(Shared)};
+  return launch_list(k, p, c.span.B, c.num_sms, c.stream);
 }
 
 }  // namespace
@@ -965,18 +574,21 @@ int launch_decode_q8(const DecodeQ8Call& c) {
   if (p.T * (c.H / c.Hkv) > (1 << 30)) return kErrShape;
   p.rows = (int)p.T * (c.H / c.Hkv);
   p.scale_log2 = c.scale * 1.4426950408889634f;
+  p.unit = 1.f;
   p.err = c.err;
+  p.parts = static_cast<float*>(c.ws);
+  p.sums = nullptr;
   const int64_t B = c.span.B;
   if (c.dtype == PFA_BF16)
-    return c.D == 128 ? launch<__nv_bfloat16, 1, 2>(p, c, B) : launch<__nv_bfloat16, 4, 2>(p, c, B);
+    return c.D == 128 ? launch<__nv_bfloat16, 1, 2>(p, c) : launch<__nv_bfloat16, 4, 2>(p, c);
   // fp32: with tiles of 16 rows each converted code serves two products, with 8 a unit is
   // through sooner.  2048 tokens at 14336, 32/8 heads of 128: 3514 us against 4183; 3 tokens of 4
   // sequences, window 1024, 8/2 heads of 512 (528 units of 8 rows): 12.6 against 10.8.
   const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
   const int64_t units = B * ((p.rows + 7) / 8) * p.Hkv * (keys / kUnit + 1);
   if (p.rows <= 8 || units < (int64_t)8 * c.num_sms * kBlocksPerSm)
-    return c.D == 128 ? launch<float, 1, 1>(p, c, B) : launch<float, 4, 1>(p, c, B);
-  return c.D == 128 ? launch<float, 1, 2>(p, c, B) : launch<float, 4, 2>(p, c, B);
+    return c.D == 128 ? launch<float, 1, 1>(p, c) : launch<float, 4, 1>(p, c);
+  return c.D == 128 ? launch<float, 1, 2>(p, c) : launch<float, 4, 2>(p, c);
 }
 
 }  // namespace pfa
