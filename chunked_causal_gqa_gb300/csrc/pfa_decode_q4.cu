@@ -1,205 +1,703 @@
-// pfa_decode_q4.cu -- attention of few tokens of a batch of sequences over their 4-bit caches.
+// pfa_decode_q4.cu -- attention of few tokens of a batch of sequences over
+// their 4-bit caches, on the tensor cores.
 //
-// For each sequence, token and query head
+// For each sequence and kv head the T * group query rows form tiles of 8 or 16 rows,
+// and for each tile
 //   s_j = scale * <q, k_j>,  out = sum_j 2^(s_j log2 e - m) v_j / sum_j 2^(s_j log2 e - m)
-// with the running maximum m, the sum and the output in fp32, and, where the caller keeps the
-// keys' weights, weights[j] += the sum of 2^(s_j log2 e - m) / l over the tokens and heads of the kv head.
-#include "pfa_internal.h"
-#include "pfa_ptx.cuh"
+// with the maximum, the sum and the output in fp32.  A cache byte is read once for all rows of a
+// tile, so with few rows HBM's bytes are the floor: 144 a key of a head of 128, 24 a clock of an
+// SM, which leaves a warp's scheduler some 24 issue slots a key.
+//
+// Products: mma.sync m16n8k16 on halves, transposed: S' = K Q' and O' = V' P', keys and channels
+// in the 16 rows of a product and the query rows in its 8 columns, so that a tile of 8 rows wastes
+// none of it (a product of 16 query rows would be half padding for a group of 8 or
+// less).  A code times its e4m3 scale is exact in half; q is scaled to 2^13..2^14 by a power of
+// two for each row, which makes bf16 q exact but for elements 2^27 below the row's largest; the
+// weights are rounded to half.  For fp32, q and the weights are a high and a low half, each with
+// products of its own.
+//
+// Fragments straight from the packed rows, as the order of a contraction is free:
+//   K: lane (g, qd) has 16 bytes, 32 channels, of the keys g and g + 8 of a product; two bytes are
+//      its part of a k16 step.  A byte converts to a half pair, one product with the scale follows.
+//   V: lane g has the 16 channels of one scale, 8 bytes, of four keys.  The products want a channel
+//      of two keys side by side: (a & 0f..) | (b & 0f..) << 4 is such pairs of codes, four in a word.
+//   P: the scores' layout is that of O', and movmatrix turns it into the second operand.
+// Keys stand in a product in the order 0 5 1 4 2 7 3 6, and the 16-byte pieces of every other
+// pair of rows in shared memory are swapped in halves, so that the reads of both are free of
+// bank conflicts.
+//
+// The exponent's base rises only when a score passes it by 2^4, so that most units need no
+// maximum across lanes and no rescaling: a weight is 2^(s - base) 2^11, at most 2^15.
+//
+// Work split and join: pfa_decode.cuh.  Four warps take a run's units of 32 keys in turn, each with
+// its own ring filled by cp.async; head_dim 512: four warps share a unit, each with 128 channels, and
+// exchange partial scores.
+//
+// Accumulated weights: the scores go to the workspace as they are made (4 bytes a row and key beside
+// the 144 of the cache); the join leaves each row's maximum and sum, and a third kernel adds up
+// 2^(s - m) / l over the rows of a key.
+#include "pfa_decode.cuh"
 #include "pfa_q4.cuh"
 
 #include "../../include/pfa.h"
 
-#include <algorithm>
 #include <cmath>
 
 namespace pfa {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kStages = 3;
+constexpr int kHalf = kUnit * 64;              // bytes of a warp's K (or V) codes of a stage
+constexpr int kScales = kUnit * 8;             // and of its scales
+constexpr int kStageBytes = 2 * (kHalf + kScales);
+constexpr int kJoinBytes = kWarps * 8 * 128 * 4;  // joins: 8 row sums of 128 floats for each warp
+constexpr float kLag = 4.f, kUp = 11.f;        // powers of two: of a score above the base; of weights
 
-struct Params {
-  const void* q;
-  void* out;
-  float* weights;
-  float2* sums;               // workspace: {m, l} of each row
+struct Params : ListParams {
+  static constexpr int kHeadCost = 16;
+  static constexpr bool kSums = true;
   const uint8_t *k4, *v4, *k_scale, *v_scale;
-  const int64_t* lengths;
-  int64_t T, start_pos, q_row, out_row, cap;
-  int Hkv, group, rows, window;
-  float scale_log2, v_unit;
-  unsigned* err;
+  float* scores;       // null, or [head][keys of whole units][row_pad]
+  float* weights;      // [head][cap]
+  int64_t score_head;  // floats of a head
+  int row_pad;
 };
 
-struct Row {
-  int64_t b;
-  int h, r, t, lo, hi;     // keys [lo, hi] are seen
+// Key of row i of a product, in its eight.
+__device__ __forceinline__ int key_at(int i) { return i & 1 ? 4 + ((i >> 1) ^ 1) : i >> 1; }
+
+// Where column d (a multiple of 4) of a row of the join area is: lanes hold 16 columns of every
+// other row.
+__device__ __forceinline__ int join_at(int d, int row) { return d ^ (((row >> 1) & 3) << 2); }
+
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+               :: "r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds2(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t b;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(b) : "r"(a));
+  return b;
+}
+
+struct Shared {
+  alignas(128) uint8_t ring[kWarps][kStages][kStageBytes];
+  alignas(16) uint8_t join[kJoinBytes];   // also: score exchange
+  float2 ml[kWarps][16];                  // a warp's {m, l} of each row
+  ListShared list;
 };
-__device__ __forceinline__ bool row_of(const Params& p, int64_t bh, int r, Row& x) {
-  x.b = bh / p.Hkv;
-  x.h = (int)(bh - x.b * p.Hkv);
-  x.r = r;
-  x.t = r / p.group;
-  const int64_t end = p.lengths ? p.lengths[x.b] : p.start_pos + p.T;
-  if (end < 0 || end > p.cap) return false;
-  x.hi = (int)(end - p.T) + x.t;
-  x.lo = p.window > 0 ? max(0, x.hi - p.window + 1) : 0;
-  return true;
-}
 
-template <typename E>
-__device__ __forceinline__ float load(const E* p) {
-  if constexpr (sizeof(E) == 4) return *p;
-  else return __bfloat162float(*p);
-}
+// fp32 tiles of 16 rows need two sets of 32 query registers and two of 32 sums.
+template <typename E, int NT>
+constexpr int kBlocks = sizeof(E) == 4 && NT == 2 ? 2 : 3;
+static_assert(3 * (sizeof(Shared) + 1024) <= 228 * 1024, "shared memory of an SM");
 
-// N consecutive values of a row.
-template <int N>
-__device__ __forceinline__ void values(const uint8_t* codes, const uint8_t* scales, int64_t row, int D, int d,
-                                       float* x) {
-  const float f = e4m3_to_float(scales[row * (D / 16) + d / 16]);
-#pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
-    const uint32_t w = *reinterpret_cast<const uint16_t*>(codes + row * (D / 2) + d / 2 + 2 * i);
-    const uint32_t a = e2m1x2_to_half<0>(w), b = e2m1x2_to_half<1>(w);
-    const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    x[4 * i] = u.x * f; x[4 * i + 1] = u.y * f; x[4 * i + 2] = v.x * f; x[4 * i + 3] = v.y * f;
-  }
-}
+// NW: warps of a unit (head_dim / 128).  NT: products a tile, tiles of 8 NT rows.
+template <typename E, int NW, int NT>
+__global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(const Params p) {
+  // A team is a warp or the block, so that every barrier is the block's: it does not count
+  // warps that have ended, and no lengths, not even changing ones, leave a warp waiting.
+  static_assert(NW == 1 || NW == kWarps, "barriers are the block's");
+  constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = 8 * NT;
+  constexpr bool F32 = sizeof(E) == 4;
+  constexpr int SETS = F32 ? 2 : 1;   // high and low halves
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, qd = lane & 3;
+  const int team = warp / NW, part = warp % NW;
 
-template <int N>
-__device__ __forceinline__ float score(const float* q, const float* k) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) s = fmaf(q[i], k[i], s);
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// A block for each row of queries: four warps take its keys in turn, a lane has D / 32 channels.
-template <typename E, int D>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const Params p) {
-  constexpr int N = D / 32;
-  __shared__ float s_o[kWarps][D];
-  __shared__ float2 s_ml[kWarps];
-  asm volatile("griddepcontrol.launch_dependents;");
+  // What ran before has written its results; only then may the join start (it reads the lengths
+  // before its own wait).
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t bh = blockIdx.x / p.rows;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = lane * N;
-  Row x;
-  if (!row_of(p, bh, (int)(blockIdx.x - bh * p.rows), x)) {
-    if (threadIdx.x == 0) atomicOr(p.err, kErrLengths);
-    return;
-  }
-  const int64_t head = (int64_t)x.h * p.group + x.r - x.t * p.group;
-  const E* qr = (const E*)p.q + (x.b * p.T + x.t) * p.q_row + head * D + d;
-  float q[N], o[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = load(qr + i) * p.scale_log2;
-    o[i] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = x.lo + warp; j <= x.hi; j += kWarps) {
-    float k[N], v[N];
-    values<N>(p.k4, p.k_scale, bh * p.cap + j, D, d, k);
-    values<N>(p.v4, p.v_scale, bh * p.cap + j, D, d, v);
-    const float s = score<N>(q, k), to = fmaxf(m, s);
-    const float base = to == -INFINITY ? 0.f : to;
-    const float a = exp2f(m - base), e = exp2f(s - base);
-    m = to;
-    l = l * a + e;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = o[i] * a + e * v[i];
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) s_o[warp][d + i] = o[i];
-  if (lane == 0) s_ml[warp] = make_float2(m, l);
-  __syncthreads();
-  m = -INFINITY;
-  l = 0.f;
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w].x);
-  const float base = m == -INFINITY ? 0.f : m;
-  for (int w = 0; w < kWarps; ++w) l += s_ml[w].y * exp2f(s_ml[w].x - base);
-  const float inv = l == 0.f ? 0.f : p.v_unit / l;
-  E* to = (E*)p.out + (x.b * p.T + x.t) * p.out_row + head * D;
-  for (int i = threadIdx.x; i < D; i += kThreads) {
-    float sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) sum += s_o[w][i] * exp2f(s_ml[w].x - base);
-    to[i] = (E)(sum * inv);
-  }
-  if (p.weights && threadIdx.x == 0) p.sums[bh * p.rows + x.r] = make_float2(base, l);
-}
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-// A warp for each key of a head: the scores again, their weights added up over the rows.
-template <typename E, int D>
-__global__ void __launch_bounds__(kThreads) weights_kernel(const Params p, int chunks) {
-  constexpr int N = D / 32;
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t bh = blockIdx.x / chunks;
-  const int lane = threadIdx.x & 31, d = lane * N;
-  const int first = (int)(blockIdx.x - bh * chunks) * kWarps + (threadIdx.x >> 5);
-  Row x;
-  if (!row_of(p, bh, 0, x)) return;
-  Row last;
-  row_of(p, bh, p.rows - 1, last);
-  for (int j = x.lo + first; j <= last.hi; j += chunks * kWarps) {
-    float k[N], sum = 0.f;
-    values<N>(p.k4, p.k_scale, bh * p.cap + j, D, d, k);
-    for (int r = 0; r < p.rows; ++r) {
-      row_of(p, bh, r, x);
-      if (j < x.lo || j > x.hi) continue;
-      const E* qr = (const E*)p.q + (x.b * p.T + x.t) * p.q_row + ((int64_t)x.h * p.group + r - x.t * p.group) * D + d;
-      float q[N];
+  int at, stop, first_entry, into;
+  if (!run_start<RM, TEAMS>(p, sm.list, at, stop, first_entry, into)) return;
+
+  Cursor<Params, RM, TEAMS> in, cu;   // copies, products
+  in.start(p, at, stop, first_entry, into, team);
+  cu = in;
+
+  // Query rows of a piece as they are stored, this warp's columns: the lane's 32
+  // elements of its rows.  Rows past the tile repeat its last.
+  // They are asked for under the prologue or the join before, but for two fp32 rows, which
+  // would need 64 registers across the join.
+  constexpr int RV = F32 ? 8 : 4;   // 16-byte vectors of a row
+  constexpr bool EARLY = NT * RV <= 8;
+  uint4 raw[EARLY ? NT * RV : RV];
+  auto load_row = [&](int i) {
+    const int r = cu.x.r0 + min(g + 8 * i, cu.x.nr - 1);
+    const int t = r / p.group;   // its token
+    const E* row = (const E*)p.q + (cu.x.b * p.T + t) * p.q_row +
+                   (int64_t)(cu.h * (int)p.group.by + r - t * (int)p.group.by) * D + part * 128 + qd * 32;
 #pragma unroll
-      for (int i = 0; i < N; ++i) q[i] = load(qr + i) * p.scale_log2;
-      const float2 ml = p.sums[bh * p.rows + r];
-      sum += exp2f(score<N>(q, k) - ml.x) / ml.y;
+    for (int j = 0; j < RV; ++j)
+      raw[(EARLY ? i * RV : 0) + j] = *reinterpret_cast<const uint4*>(row + j * (16 / (int)sizeof(E)));
+  };
+  auto load_early = [&]() {
+    if constexpr (EARLY) {
+      if (cu.done()) return;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) load_row(i);
     }
-    if (lane == 0) p.weights[bh * p.cap + j] += sum;
+  };
+  load_early();
+
+  const uint32_t ring = smem_u32(sm.ring[warp]);
+  // Copies of a unit: K's codes and scales, then V's, each a group of its own: K's place is free
+  // for a later unit when the scores are done, V's when its sum is.  Copy c of 4 is row
+  // 8 c + lane / 4, piece lane % 4; and the scales of row `lane`.
+  const uint32_t dst = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 2) & 2)) << 4);
+  struct Source {
+    int64_t row;           // cache row of key0, all heads counted
+    int key0, lo, hi;      // on: hi >= lo
+  } src = {};
+  auto copy_half = [&](uint32_t to, const uint8_t* codes, const uint8_t* scales) {
+    const uint8_t* from = codes + (src.row + (lane >> 2)) * (D / 2) + part * 64 + (lane & 3) * 16;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int key = src.key0 + 8 * c + (lane >> 2);
+      const bool on = key >= src.lo && key <= src.hi;
+      copy16(to + c * 512 + dst, on ? from + c * 8 * (D / 2) : codes, on);
+    }
+    const int key = src.key0 + lane;
+    const bool on = key >= src.lo && key <= src.hi;
+    copy8(to + kHalf + lane * 8, on ? scales + (src.row + lane) * (D / 16) + part * 8 : scales, on);
+  };
+  auto copy_k = [&](int stage) {
+    while (!in.done() && in.k >= in.kend) in.next_piece(p, team);
+    src.lo = 0;
+    src.hi = -1;
+    if (!in.done()) {
+      src.key0 = (in.x.u0 + in.k) * kUnit;
+      src.lo = in.x.lo;
+      src.hi = in.x.hi;
+      src.row = (in.x.b * p.Hkv + in.h) * p.cap + src.key0;
+      copy_half(ring + stage * kStageBytes, p.k4, p.k_scale);
+      in.k += TEAMS;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto copy_v = [&](int stage) {
+    if (src.hi >= src.lo) copy_half(ring + stage * kStageBytes + kHalf + kScales, p.v4, p.v_scale);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int s = 0; s < kStages; ++s) {
+    copy_k(s);
+    copy_v(s);
+  }
+
+  // K: key g of a product; V: keys 2 qd and 2 qd + 1
+  const uint32_t k_row = key_at(g), v_row0 = key_at(2 * qd), v_row1 = key_at(2 * qd + 1);
+  const uint32_t k_at = k_row * 64 + ((qd ^ (k_row & 2)) << 4);
+  const uint32_t v_at0 = v_row0 * 64 + (((g >> 1) ^ (v_row0 & 2)) << 4) + (g & 1) * 8;
+  const uint32_t v_at1 = v_row1 * 64 + (((g >> 1) ^ (v_row1 & 2)) << 4) + (g & 1) * 8;
+  int stage = 0, swap = 0;
+
+  while (!cu.done()) {
+    const auto x = cu.x;
+    // ---- the piece's query rows, scaled by a power of two each
+    uint32_t qf[NT][SETS][8][2];
+    float srow[NT][2];     // rows 2 qd, 2 qd + 1 of each product
+    int hi[NT][2], lo[NT][2];
+    auto raw_at = [&](int i, int j) -> float {   // element j of the lane's 32 of row i
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+      if constexpr (F32) {
+        return __uint_as_float(w[(EARLY ? i * 32 : 0) + j]);
+      } else {
+        const uint32_t v = w[i * 16 + j / 2];
+        return __uint_as_float(j % 2 ? v & 0xffff0000u : v << 16);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if constexpr (!EARLY) load_row(i);
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(raw_at(i, j)));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      if constexpr (NW > 1) {   // over the team's columns
+        if (qd == 0) sm.ml[warp][g + 8 * i].x = amax;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) amax = fmaxf(amax, sm.ml[team * NW + w][g + 8 * i].x);
+      }
+      int ex = 13 + 127 - (int)(__float_as_uint(amax) >> 23);
+      if (amax == 0.f || !(amax <= 3.402823466e38f)) ex = 0;
+      ex = min(ex, 120);
+      const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+      const float down = __uint_as_float((uint32_t)(127 - ex) << 23) * p.scale_log2;
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float w0 = raw_at(i, 4 * s + 2 * c) * up, w1 = raw_at(i, 4 * s + 2 * c + 1) * up;
+          if constexpr (F32)
+            split2(w0, w1, qf[i][0][s][c], qf[i][1][s][c]);
+          else
+            qf[i][0][s][c] = half2_of(w0, w1);
+        }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        srow[i][c] = __shfl_sync(0xffffffffu, down, (2 * qd + c) * 4);
+        const int r = x.r0 + min(8 * i + 2 * qd + c, x.nr - 1);
+        hi[i][c] = x.end - (int)p.T + r / p.group;
+        lo[i][c] = p.window > 0 ? hi[i][c] - p.window + 1 : 0;
+      }
+    }
+    // keys that every row of the tile sees need no mask
+    const int all_hi = x.end - (int)p.T + x.r0 / p.group;
+    const int all_lo = p.window > 0 ? x.hi - p.window + 1 : 0;
+    float* const scores = p.scores ? p.scores + (x.b * p.Hkv + cu.h) * p.score_head : nullptr;
+
+    // Channels 16 g + 2 t, + 1 of rows 2 qd, + 1: {channel, row} 00, 01, 10, 11 of product t.
+    float o[NT][8][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][t][c] = 0.f;
+    float m[NT][2], l[NT][2];   // base; this lane's part of the sum
+#pragma unroll
+    for (int i = 0; i < NT; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+
+#pragma unroll 1
+    for (; cu.k < cu.kend; cu.k += TEAMS) {
+      asm volatile("cp.async.wait_group %0;" :: "n"(2 * kStages - 1) : "memory");
+      __syncwarp();
+      const uint32_t kb = ring + stage * kStageBytes, vb = kb + kHalf + kScales;
+      // ---- scores: [product of 16 keys][tile]{key g, row 2 qd, + 1; key g + 8, the same rows}
+      float s[2][NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float acc[NT][SETS][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int b = 0; b < SETS; ++b) acc[i][b][0] = acc[i][b][1] = acc[i][b][2] = acc[i][b][3] = 0.f;
+        const uint4 ka = lds16(kb + h * 1024 + k_at), kc = lds16(kb + h * 1024 + 512 + k_at);
+        const uint32_t sa = e4m3x2_to_half(lds2(kb + kHalf + (h * 16 + k_row) * 8 + 2 * qd));
+        const uint32_t sc = e4m3x2_to_half(lds2(kb + kHalf + (h * 16 + 8 + k_row) * 8 + 2 * qd));
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t fa = __byte_perm(sa, sa, w < 2 ? 0x1010 : 0x3232);
+          const uint32_t fc = __byte_perm(sc, sc, w < 2 ? 0x1010 : 0x3232);
+          uint32_t a[2][4];
+          a[0][0] = mul2(e2m1x2_to_half<0>(wa[w]), fa);
+          a[0][1] = mul2(e2m1x2_to_half<0>(wc[w]), fc);
+          a[0][2] = mul2(e2m1x2_to_half<1>(wa[w]), fa);
+          a[0][3] = mul2(e2m1x2_to_half<1>(wc[w]), fc);
+          a[1][0] = mul2(e2m1x2_to_half<2>(wa[w]), fa);
+          a[1][1] = mul2(e2m1x2_to_half<2>(wc[w]), fc);
+          a[1][2] = mul2(e2m1x2_to_half<3>(wa[w]), fa);
+          a[1][3] = mul2(e2m1x2_to_half<3>(wc[w]), fc);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int b = 0; b < SETS; ++b) mma(acc[i][b], a[c], qf[i][b][2 * w + c][0], qf[i][b][2 * w + c][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[h][i][c] = F32 ? acc[i][0][c] + acc[i][SETS - 1][c] : acc[i][0][c];
+      }
+      __syncwarp();
+      copy_k(stage);
+      if constexpr (NW > 1) {
+        // the team's partial scores, summed in the same order by each warp
+        float4* ex = reinterpret_cast<float4*>(sm.join) + swap * (NW * 2 * NT * 32);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            ex[(part * 2 * NT + h * NT + i) * 32 + lane] =
+                make_float4(s[h][i][0], s[h][i][1], s[h][i][2], s[h][i][3]);
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            float4 t = ex[(h * NT + i) * 32 + lane];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) {
+              const float4 v = ex[(w * 2 * NT + h * NT + i) * 32 + lane];
+              t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+            }
+            s[h][i][0] = t.x; s[h][i][1] = t.y; s[h][i][2] = t.z; s[h][i][3] = t.w;
+          }
+        swap ^= 1;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[h][i][c] *= srow[i][c & 1];
+      const int key0 = (x.u0 + cu.k) * kUnit;
+      if (key0 < all_lo || key0 + kUnit - 1 > all_hi) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int key = key0 + h * 16 + (c >> 1) * 8 + (int)k_row;
+              if (key < lo[i][c & 1] || key > hi[i][c & 1]) s[h][i][c] = -INFINITY;
+            }
+      }
+      if (scores && part == 0) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const int r = x.r0 + 8 * i + 2 * qd;
+          if (r < p.rows) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                *reinterpret_cast<float2*>(scores + (int64_t)(key0 + h * 16 + c * 8 + (int)k_row) * p.row_pad + r) =
+                    make_float2(s[h][i][2 * c], s[h][i][2 * c + 1]);
+          }
+        }
+      }
+      // ---- the base rises where a score is far above it
+      bool rises = false;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          rises |= fmaxf(fmaxf(s[0][i][c], s[0][i][c + 2]), fmaxf(s[1][i][c], s[1][i][c + 2])) > m[i][c] + kLag;
+      if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(fmaxf(s[0][i][c], s[0][i][c + 2]), fmaxf(s[1][i][c], s[1][i][c + 2]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            mx = fmaxf(mx, m[i][c]);
+            const float a = exp2_fast(m[i][c] - (mx == -INFINITY ? 0.f : mx));
+            m[i][c] = mx;
+            l[i][c] *= a;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+              o[i][t][c] *= a;
+              o[i][t][c + 2] *= a;
+            }
+          }
+      }
+      // ---- weights and their sums; the weights as the second operand
+      uint32_t pf[2][NT][SETS][2];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float b0 = m[i][0] == -INFINITY ? 0.f : m[i][0] - kUp, b1 = m[i][1] == -INFINITY ? 0.f : m[i][1] - kUp;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float e0 = exp2_fast(s[h][i][2 * c] - b0), e1 = exp2_fast(s[h][i][2 * c + 1] - b1);
+            l[i][0] += e0;
+            l[i][1] += e1;
+            if constexpr (F32) {
+              uint32_t u, v;
+              split2(e0, e1, u, v);
+              pf[h][i][0][c] = transposed(u);
+              pf[h][i][1][c] = transposed(v);
+            } else {
+              pf[h][i][0][c] = transposed(half2_of(e0, e1));
+            }
+          }
+      }
+      // ---- weighted sum of V
+      asm volatile("cp.async.wait_group %0;" :: "n"(2 * kStages - 1) : "memory");
+      __syncwarp();
+      // pairs of a channel of two keys, even channels and odd ones
+      auto pairs = [&](uint32_t a, uint32_t b, uint32_t& even, uint32_t& odd) {
+        even = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+        odd = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+      };
+      auto load_v = [&](int h, uint32_t (&w)[2][4], uint32_t (&f)[2]) {
+        const uint32_t at = vb + h * 1024;
+        const uint2 a = lds8(at + v_at0), b = lds8(at + v_at1);
+        const uint2 c = lds8(at + 512 + v_at0), d = lds8(at + 512 + v_at1);
+        pairs(a.x, b.x, w[0][0], w[0][1]);
+        pairs(c.x, d.x, w[0][2], w[0][3]);
+        pairs(a.y, b.y, w[1][0], w[1][1]);
+        pairs(c.y, d.y, w[1][2], w[1][3]);
+        const uint32_t sb = vb + kHalf + h * 128 + g;
+        f[0] = e4m3x2_to_half(lds1(sb + v_row0 * 8) | lds1(sb + v_row1 * 8) << 8);
+        f[1] = e4m3x2_to_half(lds1(sb + 64 + v_row0 * 8) | lds1(sb + 64 + v_row1 * 8) << 8);
+      };
+      auto fragment = [&](const uint32_t (&w)[4], const uint32_t (&f)[2], int i, uint32_t (&a)[4]) {
+        switch (i) {
+          case 0:
+            a[0] = e2m1x2_to_half<0>(w[0]); a[1] = e2m1x2_to_half<0>(w[1]);
+            a[2] = e2m1x2_to_half<0>(w[2]); a[3] = e2m1x2_to_half<0>(w[3]);
+            break;
+          case 1:
+            a[0] = e2m1x2_to_half<1>(w[0]); a[1] = e2m1x2_to_half<1>(w[1]);
+            a[2] = e2m1x2_to_half<1>(w[2]); a[3] = e2m1x2_to_half<1>(w[3]);
+            break;
+          case 2:
+            a[0] = e2m1x2_to_half<2>(w[0]); a[1] = e2m1x2_to_half<2>(w[1]);
+            a[2] = e2m1x2_to_half<2>(w[2]); a[3] = e2m1x2_to_half<2>(w[3]);
+            break;
+          default:
+            a[0] = e2m1x2_to_half<3>(w[0]); a[1] = e2m1x2_to_half<3>(w[1]);
+            a[2] = e2m1x2_to_half<3>(w[2]); a[3] = e2m1x2_to_half<3>(w[3]);
+        }
+        a[0] = mul2(a[0], f[0]); a[1] = mul2(a[1], f[0]);
+        a[2] = mul2(a[2], f[1]); a[3] = mul2(a[3], f[1]);
+      };
+      if constexpr (F32) {
+        // The tensor cores truncate as they accumulate: over thousands of keys that is a bias of
+        // 1e-5 of the output.  So they add up one unit only, and rounding adds do the rest.
+        uint32_t w[2][2][4], f[2][2];
+        load_v(0, w[0], f[0]);
+        load_v(1, w[1], f[1]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          uint32_t a[2][4];
+          fragment(w[0][t / 4], f[0], t % 4, a[0]);
+          fragment(w[1][t / 4], f[1], t % 4, a[1]);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int b = SETS - 1; b >= 0; --b) {
+              mma(c, a[0], pf[0][i][b][0], pf[0][i][b][1]);
+              mma(c, a[1], pf[1][i][b][0], pf[1][i][b][1]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i][t][k] += c[k];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[2][4], f[2];
+          load_v(h, w, f);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            uint32_t a[4];
+            fragment(w[t / 4], f, t % 4, a);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) mma(o[i][t], a, pf[h][i][0][0], pf[h][i][0][1]);
+          }
+        }
+      }
+      __syncwarp();
+      copy_v(stage);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    }
+
+    // ---- join the block's teams, rows in rounds of eight
+    const bool whole = cu.k0 == 0 && cu.kend == x.n;
+    float* slot = p.parts + (int64_t)(2 * blockIdx.x + (cu.at == at ? 0 : 1)) * slot_floats<RM, D>();
+    const int h = cu.h;
+    cu.next_piece(p, team);
+    load_early();   // arrives while the join runs
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[i][c] += __shfl_xor_sync(0xffffffffu, l[i][c], d);
+        if (g == 0) sm.ml[warp][8 * i + 2 * qd + c] = make_float2(m[i][c], l[i][c]);
+      }
+    float* join = reinterpret_cast<float*>(sm.join);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (8 * i >= x.nr) break;
+      __syncthreads();   // ml is complete; what used the join area before is done
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int rr = 2 * qd + c, r = rr + 8 * i;
+        if (r < x.nr) {
+          float mx = -INFINITY;
+          for (int w = 0; w < TEAMS; ++w) mx = fmaxf(mx, sm.ml[w * NW][r].x);
+          const float f = exp2_fast(m[i][c] - (mx == -INFINITY ? 0.f : mx) - kUp);
+          float* to = join + (team * 8 + rr) * D;
+#pragma unroll
+          for (int t = 0; t < 8; t += 2)
+            *reinterpret_cast<float4*>(to + join_at(part * 128 + g * 16 + 2 * t, rr)) =
+                make_float4(o[i][t][c] * f, o[i][t][c + 2] * f, o[i][t + 1][c] * f, o[i][t + 1][c + 2] * f);
+        }
+      }
+      __syncthreads();
+      const int rows = min(8, x.nr - 8 * i);
+#pragma unroll 1
+      for (int c = tid; c < rows * (D / 4); c += kThreads) {
+        const int rr = c / (D / 4), d = c % (D / 4) * 4, r = rr + 8 * i;
+        float4 sum = *reinterpret_cast<const float4*>(join + rr * D + join_at(d, rr));
+        for (int w = 1; w < TEAMS; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(join + (w * 8 + rr) * D + join_at(d, rr));
+          sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+        }
+        float mx = -INFINITY, ls = 0.f;
+        for (int w = 0; w < TEAMS; ++w) mx = fmaxf(mx, sm.ml[w * NW][r].x);
+        for (int w = 0; w < TEAMS; ++w)
+          ls += sm.ml[w * NW][r].y * exp2_fast(sm.ml[w * NW][r].x - (mx == -INFINITY ? 0.f : mx) - kUp);
+        if (whole) {
+          const float n = ls == 0.f ? 0.f : p.unit / ls;
+          const int q = x.r0 + r, t = q / p.group;
+          E* to = (E*)p.out + (x.b * p.T + t) * p.out_row +
+                  (int64_t)(h * (int)p.group.by + q - t * (int)p.group.by) * D + d;
+          store_row4(to, make_float4(sum.x * n, sum.y * n, sum.z * n, sum.w * n));
+          if (p.sums && d == 0) p.sums[(x.b * p.Hkv + h) * p.rows + q] = row_sums(mx, ls);
+        } else {
+          *reinterpret_cast<float4*>(slot + r * D + d) = sum;
+          if (d == 0) *reinterpret_cast<float2*>(slot + RM * D + 2 * r) = make_float2(mx, ls);
+        }
+      }
+    }
+    __syncthreads();   // the join area and ml are free again
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// A thread for each key of a head: its rows' weights from their scores, added up in order.
+constexpr int kWeightThreads = 256, kMaxRows = PFA_DECODE_MAX_ROWS;
+
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const Params p, const Divisor chunks) {
+  __shared__ float2 s_sum[kMaxRows];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int bh = blockIdx.x / chunks, chunk = blockIdx.x - bh * (int)chunks.by, b = bh / p.heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t end = p.lengths[b];
+  if (end < 0 || end > p.cap) return;
+  const int first = (int)(end - p.T);               // position of the first token
+  const int lo = p.window > 0 ? max(0, max(first, 0) - p.window + 1) : 0;
+  if (lo + (int64_t)chunk * kWeightThreads >= end) return;
+  for (int r = threadIdx.x; r < p.rows; r += kWeightThreads) s_sum[r] = p.sums[(int64_t)bh * p.rows + r];
+  __syncthreads();
+  for (int j = lo + chunk * kWeightThreads + threadIdx.x; j < (int)end; j += chunks.by * kWeightThreads) {
+    const float* row = p.scores + bh * p.score_head + (int64_t)j * p.row_pad;
+    float sum = 0.f;
+    // tokens that see the key: at or behind it, and not a window behind
+    const int t0 = max(max(0, j - first), -first), t1 = p.window > 0 ? min((int)p.T - 1, j - first + p.window - 1) : (int)p.T - 1;
+    const int r1 = (t1 + 1) * (int)p.group.by;
+    for (int r = t0 * (int)p.group.by; r < r1; ++r) sum += exp2_fast(row[r] - s_sum[r].x) * s_sum[r].y;
+    p.weights[(int64_t)bh * p.cap + j] += sum;
   }
 }
 
-template <typename E, int D>
-int launch(const Params& p, int64_t heads, cudaStream_t stream) {
-  if (heads * p.rows > 0x7fffffff) return kErrShape;
-  decode_kernel<E, D><<<(unsigned)(heads * p.rows), kThreads, 0, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return kErrLaunch;
-  if (!p.weights) return kOk;
-  const int chunks = (int)std::min<int64_t>((p.cap + kWarps - 1) / kWarps, 0x7fffffff / heads);
-  weights_kernel<E, D><<<(unsigned)(heads * chunks), kThreads, 0, stream>>>(p, chunks);
-  return cudaGetLastError() == cudaSuccess ? kOk : kErrLaunch;
+template <typename E, int NW, int NT>
+int launch(const Params& p, const DecodeQ4Call& c) {
+  static DeviceOnce once;
+  const int rc = once.run(c.device, [] {
+    return cudaFuncSetAttribute(decode_kernel<E, NW, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(Shared)) == cudaSuccess ? kOk : kErrLaunch;
+  });
+  if (rc != kOk) return rc;
+  const Kernels<Params> k = {decode_kernel<E, NW, NT>, join_kernel<Params, E, NW, 8 * NT, 8>,
+                             join_kernel<Params, E, NW, 8 * NT, 1>, 8 * NT, NW, kBlocks<E, NT>,
+                             sizeof(Shared)};
+  return launch_list(k, p, c.span.B, c.num_sms, c.stream);
+}
+
+// Workspace: partial sums, two slots a run; with weights each row's sums and each score.
+struct Layout {
+  size_t sums, scores, total;
+  int64_t score_head;
+  int row_pad;
+};
+Layout layout(int64_t heads, int rows, int D, int dtype, int64_t cap, bool weights, int num_sms) {
+  Layout w = {};
+  const int rm = rows <= 8 ? 8 : 16;   // most rows of a tile
+  const size_t parts = 2 * (size_t)num_sms * 3 * (rm * D + rm * 2) * sizeof(float);
+  w.sums = (parts + 255) & ~(size_t)255;
+  w.scores = w.total = w.sums;
+  if (!weights) return w;
+  w.row_pad = (rows + 3) & ~3;
+  w.score_head = (cap + kUnit - 1) / kUnit * kUnit * w.row_pad;
+  w.scores += ((size_t)heads * rows * sizeof(float2) + 255) & ~(size_t)255;
+  w.total = w.scores + (((size_t)heads * w.score_head * sizeof(float) + 255) & ~(size_t)255);
+  return w;
 }
 
 }  // namespace
 
 size_t decode_q4_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int64_t cap,
                            bool weights, int num_sms) {
-  return weights ? ((size_t)B * T * H * sizeof(float2) + 255) & ~(size_t)255 : 0;
+  return layout(B * Hkv, (int)std::min<int64_t>(T * (H / Hkv), 1 << 30), D, dtype, cap, weights, num_sms).total;
 }
 
 int launch_decode_q4(const DecodeQ4Call& c) {
   Params p;
-  p.q = c.q; p.out = c.out; p.weights = c.weights; p.sums = (float2*)c.ws;
+  p.q = c.q; p.out = c.out;
   p.k4 = (const uint8_t*)c.cache.k4; p.v4 = (const uint8_t*)c.cache.v4;
   p.k_scale = (const uint8_t*)c.cache.k_scale; p.v_scale = (const uint8_t*)c.cache.v_scale;
   p.lengths = c.span.lengths;
   p.T = c.span.T; p.start_pos = c.span.start_pos;
   p.q_row = c.q_row; p.out_row = c.out_row;
-  p.cap = c.cache.max_seq_len;
-  p.Hkv = c.Hkv; p.group = c.H / c.Hkv; p.window = c.window;
-  if (p.T * p.group > (1 << 30)) return kErrShape;
-  p.rows = (int)p.T * p.group;
+  p.cap = (int)c.cache.max_seq_len;
+  p.Hkv = c.Hkv; p.group = divisor(c.H / c.Hkv); p.window = c.window;
+  if (p.T * (c.H / c.Hkv) > (1 << 30)) return kErrShape;
+  p.rows = (int)p.T * (c.H / c.Hkv);
   p.scale_log2 = std::ldexp(c.scale * 1.4426950408889634f, c.cache.k_exp);
-  p.v_unit = std::ldexp(1.f, c.cache.v_exp);
+  p.unit = std::ldexp(1.f, c.cache.v_exp);
   p.err = c.err;
   const int64_t heads = c.span.B * c.Hkv;
+  if (c.weights && heads > 0x7fffffff) return kErrShape;
+  const Layout w = layout(heads, p.rows, c.D, c.dtype, p.cap, c.weights != nullptr, c.num_sms);
+  char* ws = static_cast<char*>(c.ws);
+  p.parts = reinterpret_cast<float*>(ws);
+  p.sums = c.weights ? reinterpret_cast<float2*>(ws + w.sums) : nullptr;
+  p.scores = c.weights ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
+  p.score_head = w.score_head;
+  p.row_pad = w.row_pad;
+  p.weights = c.weights;
+  const bool few = p.rows <= 8;
+  int rc;
   if (c.dtype == PFA_BF16)
-    return c.D == 128 ? launch<__nv_bfloat16, 128>(p, heads, c.stream)
-                      : launch<__nv_bfloat16, 512>(p, heads, c.stream);
-  return c.D == 128 ? launch<float, 128>(p, heads, c.stream) : launch<float, 512>(p, heads, c.stream);
+    rc = c.D == 128 ? (few ? launch<__nv_bfloat16, 1, 1>(p, c) : launch<__nv_bfloat16, 1, 2>(p, c))
+                    : (few ? launch<__nv_bfloat16, 4, 1>(p, c) : launch<__nv_bfloat16, 4, 2>(p, c));
+  else
+    rc = c.D == 128 ? (few ? launch<float, 1, 1>(p, c) : launch<float, 1, 2>(p, c))
+                    : (few ? launch<float, 4, 1>(p, c) : launch<float, 4, 2>(p, c));
+  if (rc != kOk || !c.weights) return rc;
+  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
+  const int64_t chunks = std::min<int64_t>((keys + kWeightThreads - 1) / kWeightThreads, 0x7fffffff / heads);
+  p.heads = divisor(p.Hkv);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(heads * chunks));
+  cfg.blockDim = dim3(kWeightThreads);
+  cfg.stream = c.stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, weights_kernel, (const Params)p, divisor((uint32_t)chunks)) == cudaSuccess)
+    return kOk;
+  cudaGetLastError();
+  return kErrLaunch;
 }
 
 }  // namespace pfa
