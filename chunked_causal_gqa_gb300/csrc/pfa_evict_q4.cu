@@ -3,35 +3,68 @@
 // For a sequence of n > keep rows, of each kv head: the `recent` newest rows stay, and the keep - recent
 // largest of the others' weights (equal ones: the lower row).
 //
-// select_kernel, a block for each head: the key of a weight is its bits, turned so that unsigned order
-// is the order of numbers.  Four passes over the candidates find the smallest key that
-// is kept, eight bits at a time, from a histogram; a last pass lists the kept rows in
-// order, counting equal keys, and moves their weights down.
+// select_kernel, a cluster of up to eight blocks for each head, each with a run of its rows in shared memory:
+// the key of a weight is its bits, turned so that unsigned order is the order of
+// numbers.  Three passes over the candidates find the smallest key that is kept, 11, 11 and 10 bits at
+// a time, from histograms that the blocks add up over distributed shared memory; then the kept rows
+// are listed in order, each warp counting the kept rows in front of its own.
 //
-// move_kernel, a block for each head and part of a row: kept rows move down in place.
-// A row never moves up, so what is written in one round (rows 0 .. below the round's end) has no source
-// left in a later one; a barrier stands between a round's reads and its writes.
+// move_kernel, a cluster for each head and array: kept rows move down in place.  A row never moves
+// up, so what a round writes (rows 0 .. below its end) is no source of a later one; in a
+// round, which takes up to a megabyte, the cluster's barrier stands between the reads and the writes.
+// The weights, 4 bytes a row, are moved by a cluster for each sequence, a block for each head, which
+// also knows when every block has read the sequence's length.
 #include "pfa_internal.h"
 #include "pfa_ptx.cuh"
 #include "pfa_q4.cuh"
 
+#include <algorithm>
+
 namespace pfa {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kHeld = 16384;     // weights of a block in shared memory; others are read again
+constexpr int kPieces = 8;       // of a thread in a round
+constexpr int kMaxCluster = 8;
 
 struct Params {
   uint8_t* part[4];     // codes of K and V, scales of K and V
-  int bytes[4];         // of a row
   float* weights;
   const int64_t* lengths;
   int64_t* lengths_out;
   int32_t* rows;
   int64_t cap;
   int keep, recent;
-  int Hkv;
+  int Hkv, heads;       // of a sequence, in all
+  int held;             // weights of a block in shared memory
+  int code_bytes, scale_bytes;   // of a row
   unsigned* err;
 };
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of all blocks of the cluster; memory accesses before it come before those behind it.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of block `rank`'s shared memory.
+__device__ __forceinline__ int remote(const int* p, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
 
 // Unsigned order of the result is the order of the weights; NaN is the largest, -0 is 0.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -40,149 +73,276 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
 
-// Exclusive sum of x over the block's threads, and the total.
-__device__ __forceinline__ int block_scan(int x, int* s_sum, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int up = x;
+__device__ __forceinline__ int warp_scan(int x) {   // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, up, o);
-    if (lane >= o) up += v;
+    const int v = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += v;
   }
-  __syncthreads();
-  if (lane == 31) s_sum[warp] = up;
-  __syncthreads();
-  int before = up - x;
-  total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
-  }
-  return before;
+  return x;
 }
 
-__global__ void __launch_bounds__(kThreads) select_kernel(const Params p) {
-  __shared__ int hist[256];
-  __shared__ int s_sum[kWarps];
-  __shared__ uint32_t s_digit;
-  __shared__ int s_left;
+struct Select {
+  int hist[3][kBins];                // a pass each: other blocks may still read the last one
+  int sums[kWarps];
+  int above[kWarps], ties[kWarps];   // rows of a warp that stay for sure, and at the border
+  int total[2];
+  int digit, left;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Select& sm = *reinterpret_cast<Select*>(smem_raw);
+  float* const held = reinterpret_cast<float*>(smem_raw + sizeof(Select));
   asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t bh = blockIdx.x, b = bh / p.Hkv;
-  const int tid = threadIdx.x;
+  const uint32_t rank = cluster_rank(), size = cluster_size();
+  const int bh = blockIdx.x / size, b = bh / p.Hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t len = p.lengths[b];
   const bool bad = len < 0 || len > p.cap;
   const int n = bad ? 0 : (int)len;
-  int32_t* rows = p.rows + bh * p.keep;
-  if (bad && tid == 0 && bh == b * p.Hkv) atomicOr(p.err, kErrLengths);
-  if (n <= p.keep) {
-    for (int i = tid; i < p.keep; i += kThreads) rows[i] = i < n ? i : -1;
+  int32_t* const rows = p.rows + (int64_t)bh * p.keep;
+  if (bad && tid == 0 && rank == 0 && bh == b * p.Hkv) atomicOr(p.err, kErrLengths);
+  if (n <= p.keep) {   // the same for the whole cluster
+    for (int64_t i = rank * kThreads + tid; i < p.keep; i += size * kThreads) rows[i] = i < n ? (int)i : -1;
     return;
   }
-  float* w = p.weights + bh * p.cap;
+  // This block's rows [j0, j1), a whole number of them for each warp.
+  const int per_warp = (int)(((int64_t)n + size * kThreads - 1) / (size * kThreads)) * 32;
+  const int64_t begin = (int64_t)rank * per_warp * kWarps;
+  const int j0 = (int)min(begin, (int64_t)n), j1 = (int)min(begin + (int64_t)per_warp * kWarps, (int64_t)n);
   const int m = n - p.recent;          // candidates; more of them than places
+  const float* const w = p.weights + (int64_t)bh * p.cap;
+  const int cached = min(j1 - j0, p.held);
+#pragma unroll 8
+  for (int i = tid; i < cached; i += kThreads) held[i] = w[j0 + i];
+  for (int i = tid; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  __syncthreads();
+  auto weight = [&](int i) { return i < cached ? held[i] : w[j0 + i]; };   // row j0 + i
+
   uint32_t key = 0, mask = 0;
   int left = p.keep - p.recent;        // of the candidates that agree with key so far
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    for (int j = tid; j < m; j += kThreads) {
-      const uint32_t k = key_of(w[j]);
-      if ((k & mask) == key) atomicAdd(&hist[k >> shift & 255], 1);
+  if (left > 0) {
+    const int mine = min(j1, m) - j0;  // candidates of this block (or fewer than none)
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      int* const hist = sm.hist[pass];
+#pragma unroll 4
+      for (int i = tid; i < mine; i += kThreads) {
+        const uint32_t k = key_of(weight(i));
+        if ((k & mask) == key) atomicAdd(&hist[k >> shift & (kBins - 1)], 1);
+      }
+      cluster_barrier();
+      // thread t has bins 2047 - 2 t and the one below
+      const int hi = kBins - 1 - 2 * tid;
+      int c0 = 0, c1 = 0;
+      for (uint32_t r = 0; r < size; ++r) {
+        c0 += remote(&hist[hi], r);
+        c1 += remote(&hist[hi - 1], r);
+      }
+      const int up = warp_scan(c0 + c1);
+      if (lane == 31) sm.sums[warp] = up;
+      __syncthreads();
+      const int before_warp = warp_scan(sm.sums[lane]) - sm.sums[lane];
+      const int above = __shfl_sync(0xffffffffu, before_warp, warp) + up - c0 - c1;
+      if (above < left && left <= above + c0) {
+        sm.digit = hi;
+        sm.left = left - above;
+      } else if (above + c0 < left && left <= above + c0 + c1) {
+        sm.digit = hi - 1;
+        sm.left = left - above - c0;
+      }
+      __syncthreads();
+      key |= (uint32_t)sm.digit << shift;
+      mask |= (uint32_t)(pass == 2 ? 1023 : kBins - 1) << shift;
+      left = sm.left;
     }
-    __syncthreads();
-    if (tid == 0) {
-      int d = 255, rest = left;
-      while (d > 0 && hist[d] < rest) rest -= hist[d--];
-      s_digit = d;
-      s_left = rest;
-    }
-    __syncthreads();
-    key |= s_digit << shift;
-    mask |= 255u << shift;
-    left = s_left;
   }
-  // left of the rows whose weight is the smallest kept one stay (none if nothing but the newest does)
-  const bool any = p.keep > p.recent;
-  int ties = 0, at = 0;
-  for (int j0 = 0; j0 < n; j0 += kThreads) {
-    const int j = j0 + tid;
-    const float x = j < n ? w[j] : 0.f;
-    const uint32_t k = key_of(x);
-    const bool tie = j < m && any && k == key;
-    int total;
-    const int rank = ties + block_scan(tie, s_sum, total);
-    ties += total;
-    const bool kept = j < n && (j >= m || (any && k > key) || (tie && rank < left));
-    const int to = at + block_scan(kept, s_sum, total);   // (its barriers: every w[j] has been read)
-    at += total;
-    if (kept) {
-      rows[to] = j;
-      w[to] = x;
+  // Of the rows with that key the `left` lowest stay (with left 0: none), above it all.
+  const bool any = left > 0;
+  const int i0 = warp * per_warp;
+  auto look = [&](int i, uint32_t& sure, uint32_t& tie) {   // of the warp's rows i .. i + 31
+    const int j = j0 + i + lane;
+    bool s = false, t = false;
+    if (j < j1) {
+      if (j >= m) {
+        s = true;
+      } else if (any) {
+        const uint32_t k = key_of(weight(i + lane));
+        s = k > key;
+        t = k == key;
+      }
     }
+    sure = __ballot_sync(0xffffffffu, s);
+    tie = __ballot_sync(0xffffffffu, t);
+  };
+  int sure = 0, ties = 0;
+  for (int i = i0; i < i0 + per_warp && j0 + i < j1; i += 32) {
+    uint32_t s, t;
+    look(i, s, t);
+    sure += __popc(s);
+    ties += __popc(t);
   }
-  for (int j = p.keep + tid; j < n; j += kThreads) w[j] = 0.f;
+  if (lane == 0) {
+    sm.above[warp] = sure;
+    sm.ties[warp] = ties;
+  }
+  __syncthreads();
+  int s_before = warp_scan(sm.above[lane]), t_before = warp_scan(sm.ties[lane]);
+  if (tid == 31) {
+    sm.total[0] = s_before;
+    sm.total[1] = t_before;
+  }
+  s_before = __shfl_sync(0xffffffffu, s_before - sm.above[lane], warp);
+  t_before = __shfl_sync(0xffffffffu, t_before - sm.ties[lane], warp);
+  cluster_barrier();
+  for (uint32_t r = 0; r < rank; ++r) {
+    s_before += remote(&sm.total[0], r);
+    t_before += remote(&sm.total[1], r);
+  }
+  const uint32_t below = (1u << lane) - 1;
+  for (int i = i0; i < i0 + per_warp && j0 + i < j1; i += 32) {
+    uint32_t s, t;
+    look(i, s, t);
+    const int rank_t = t_before + __popc(t & below);
+    if ((s >> lane & 1) || ((t >> lane & 1) && rank_t < left))
+      rows[s_before + __popc(s & below) + min(rank_t, left)] = j0 + i + lane;
+    s_before += __popc(s);
+    t_before += __popc(t);
+  }
+  cluster_barrier();   // the others have read this block's totals
 }
 
-__global__ void __launch_bounds__(kThreads) move_kernel(const Params p) {
+// Rows `rows` of `width` pieces move to 0 .. keep - 1, in place.  `rank` of `size` blocks; barrier(): theirs.
+template <typename T, typename B>
+__device__ __forceinline__ void move_rows(T* base, const int32_t* rows, int keep, int width, int rank, int size,
+                                          B&& barrier) {
+  const int64_t all = (int64_t)keep * width, round = (int64_t)size * kThreads * kPieces;
+  // consecutive pieces for the threads of a block, runs of kThreads for the blocks in turn
+#pragma unroll 1
+  for (int64_t at = 0; at < all; at += round) {
+    T x[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t e = at + (int64_t)(i * size + rank) * kThreads + threadIdx.x;
+      if (e < all) {
+        const int64_t r = width == 1 ? e : width == 4 ? e >> 2 : e / width;
+        x[i] = base[(int64_t)rows[r] * width + (e - r * width)];
+      }
+    }
+    barrier();
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t e = at + (int64_t)(i * size + rank) * kThreads + threadIdx.x;
+      if (e < all) base[e] = x[i];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) move_kernel(const Params p) {
   asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t bh = blockIdx.x >> 2, b = bh / p.Hkv;
-  const int part = blockIdx.x & 3, tid = threadIdx.x;
+  const int rank = (int)cluster_rank(), size = (int)cluster_size();
+  // first the codes of K and of V, a head each; then the weights, a sequence each; then the scales
+  int id = blockIdx.x / size;
+  const int B = p.heads / p.Hkv;
+  int part = id / p.heads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (part == 0 && bh == b * p.Hkv && tid == 0) {
+  if (id >= 2 * p.heads && id < 2 * p.heads + B) {
+    const int b = id - 2 * p.heads;
     const int64_t n = p.lengths[b];
-    p.lengths_out[b] = n <= p.keep || n > p.cap ? n : p.keep;
+    cluster_barrier();   // lengths_out may be lengths
+    const bool cut = n > p.keep && n <= p.cap;
+    if (rank == 0 && threadIdx.x == 0) p.lengths_out[b] = cut ? p.keep : n;
+    if (!cut) return;
+    for (int h = rank; h < p.Hkv; h += size) {
+      const int64_t bh = (int64_t)b * p.Hkv + h;
+      float* const w = p.weights + bh * p.cap;
+      move_rows(w, p.rows + bh * p.keep, p.keep, 1, 0, 1, [] { __syncthreads(); });
+      __syncthreads();
+      for (int64_t j = p.keep + threadIdx.x; j < n; j += kThreads) w[j] = 0.f;
+    }
+    return;
   }
-  const int32_t* rows = p.rows + bh * p.keep;
-  if (rows[p.keep - 1] < p.keep) return;   // nothing moves
-  const int width = part == 0 ? p.bytes[0] : part == 1 ? p.bytes[1] : part == 2 ? p.bytes[2] : p.bytes[3];
-  uint8_t* base = (part == 0 ? p.part[0] : part == 1 ? p.part[1] : part == 2 ? p.part[2] : p.part[3]) +
-                  bh * p.cap * width;
-  const int64_t all = (int64_t)p.keep * width;
-  for (int64_t e0 = 0; e0 < all; e0 += kThreads) {
-    const int64_t e = e0 + tid;
-    const int64_t r = e / width;
-    uint8_t x = 0;
-    if (e < all) x = base[(int64_t)rows[r] * width + (e - r * width)];
-    __syncthreads();
-    if (e < all) base[e] = x;
-    __syncthreads();
-  }
+  if (id >= 2 * p.heads) part = 2 + (id - 2 * p.heads - B) / p.heads, id -= B;
+  const int64_t bh = id % p.heads;
+  const int32_t* const rows = p.rows + bh * p.keep;
+  if (rows[p.keep - 1] < p.keep) return;   // nothing moves (the same for the whole cluster)
+  const int bytes = part < 2 ? p.code_bytes : p.scale_bytes;
+  uint8_t* const base = (part == 0 ? p.part[0] : part == 1 ? p.part[1] : part == 2 ? p.part[2] : p.part[3]) +
+                        bh * p.cap * bytes;
+  auto barrier = [] { cluster_barrier(); };
+  if (bytes % 16 == 0)
+    move_rows(reinterpret_cast<uint4*>(base), rows, p.keep, bytes / 16, rank, size, barrier);
+  else if (bytes % 8 == 0)
+    move_rows(reinterpret_cast<uint2*>(base), rows, p.keep, bytes / 8, rank, size, barrier);
+  else if (bytes % 4 == 0)
+    move_rows(reinterpret_cast<uint32_t*>(base), rows, p.keep, bytes / 4, rank, size, barrier);
+  else if (bytes % 2 == 0)
+    move_rows(reinterpret_cast<uint16_t*>(base), rows, p.keep, bytes / 2, rank, size, barrier);
+  else
+    move_rows(base, rows, p.keep, bytes, rank, size, barrier);
 }
 
-template <typename P>
-int launch(void (*kernel)(const P), int64_t grid, const P& p, cudaStream_t stream) {
-  if (grid > 0x7fffffff) return kErrShape;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+int launch(void (*kernel)(const Params), int64_t clusters, int size, size_t smem, const Params& p,
+           cudaStream_t stream) {
+  if (clusters * size > 0x7fffffff) return kErrShape;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)size;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)(clusters * size));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return kOk;
   cudaGetLastError();
   return kErrLaunch;
 }
 
+// The smallest power of two of blocks, up to a cluster's, that leaves each at most `most` of n.
+int blocks_for(int64_t n, int64_t most) {
+  int c = 1;
+  while (c < kMaxCluster && n > most * c) c *= 2;
+  return c;
+}
+
 }  // namespace
 
 int launch_cache_evict_q4(const EvictQ4Call& c) {
+  static DeviceOnce once;
+  int rc = once.run(c.device, [] {
+    return cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(sizeof(Select) + kHeld * sizeof(float))) == cudaSuccess
+               ? kOk : kErrLaunch;
+  });
+  if (rc != kOk) return rc;
   Params p;
   p.part[0] = (uint8_t*)c.cache.k4; p.part[1] = (uint8_t*)c.cache.v4;
   p.part[2] = (uint8_t*)c.cache.k_scale; p.part[3] = (uint8_t*)c.cache.v_scale;
-  p.bytes[0] = p.bytes[1] = c.D / 2;
-  p.bytes[2] = p.bytes[3] = c.D / 16;
+  p.code_bytes = c.D / 2; p.scale_bytes = c.D / 16;
   p.weights = c.weights;
   p.lengths = c.lengths; p.lengths_out = c.lengths_out; p.rows = c.rows_out;
   p.cap = c.cache.max_seq_len;
   p.keep = (int)c.keep; p.recent = (int)c.recent;
   p.Hkv = c.Hkv;
   p.err = c.err;
-  if (c.B * c.Hkv * 4 > 0x7fffffff) return kErrShape;
-  const int rc = launch(select_kernel, c.B * c.Hkv, p, c.stream);
-  return rc != kOk ? rc : launch(move_kernel, c.B * c.Hkv * 4, p, c.stream);
+  const int64_t heads = c.B * c.Hkv;
+  if ((4 * heads + c.B) * kMaxCluster > 0x7fffffff) return kErrShape;
+  p.heads = (int)heads;
+  const int sel = blocks_for(p.cap, 8192);
+  p.held = (int)std::min<int64_t>(kHeld, (p.cap + (int64_t)sel * kThreads - 1) / ((int64_t)sel * kThreads) * kThreads);
+  rc = launch(select_kernel, heads, sel, sizeof(Select) + p.held * sizeof(float), p, c.stream);
+  if (rc != kOk) return rc;
+  const int mov = blocks_for(c.keep * p.code_bytes, (int64_t)kThreads * kPieces * 16);
+  return launch(move_kernel, 4 * heads + c.B, mov, 0, p, c.stream);
 }
 
 }  // namespace pfa
