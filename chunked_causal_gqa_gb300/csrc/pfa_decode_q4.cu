@@ -581,30 +581,94 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(cons
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// A thread for each key of a head: its rows' weights from their scores, added up in order.
+// G lanes for each key of a head, four of its rows' scores at a time: their weights, added up.
 constexpr int kWeightThreads = 256, kMaxRows = PFA_DECODE_MAX_ROWS;
+constexpr int kWeightKeys = 4, kWeightRounds = 2;   // keys of a thread in flight, rounds of them
 
+template <int G>
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const Params p, const Divisor chunks) {
-  __shared__ float2 s_sum[kMaxRows];
+  constexpr int kStep = kWeightThreads / G, kBlock = kStep * kWeightKeys * kWeightRounds;   // keys
+  __shared__ float4 s_m[kMaxRows / 4], s_inv[kMaxRows / 4];   // of each row, 0 and 0 behind the last
+  __shared__ int4 s_pos[kMaxRows / 4];
   asm volatile("griddepcontrol.launch_dependents;");
   const int bh = blockIdx.x / chunks, chunk = blockIdx.x - bh * (int)chunks.by, b = bh / p.heads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t end = p.lengths[b];
-  if (end < 0 || end > p.cap) return;
-  const int first = (int)(end - p.T);               // position of the first token
+  const int64_t len = p.lengths[b];
+  if (len < 0 || len > p.cap) return;
+  const int end = (int)len, first = end - (int)p.T;
   const int lo = p.window > 0 ? max(0, max(first, 0) - p.window + 1) : 0;
-  if (lo + (int64_t)chunk * kWeightThreads >= end) return;
-  for (int r = threadIdx.x; r < p.rows; r += kWeightThreads) s_sum[r] = p.sums[(int64_t)bh * p.rows + r];
-  __syncthreads();
-  for (int j = lo + chunk * kWeightThreads + threadIdx.x; j < (int)end; j += chunks.by * kWeightThreads) {
-    const float* row = p.scores + bh * p.score_head + (int64_t)j * p.row_pad;
-    float sum = 0.f;
-    // tokens that see the key: at or behind it, and not a window behind
-    const int t0 = max(max(0, j - first), -first), t1 = p.window > 0 ? min((int)p.T - 1, j - first + p.window - 1) : (int)p.T - 1;
-    const int r1 = (t1 + 1) * (int)p.group.by;
-    for (int r = t0 * (int)p.group.by; r < r1; ++r) sum += exp2_fast(row[r] - s_sum[r].x) * s_sum[r].y;
-    p.weights[(int64_t)bh * p.cap + j] += sum;
+  if (lo + (int64_t)chunk * kBlock >= end) return;
+  for (int r = threadIdx.x; r < p.row_pad; r += kWeightThreads) {
+    const float2 ml = r < p.rows ? p.sums[(int64_t)bh * p.rows + r] : make_float2(0.f, 0.f);
+    reinterpret_cast<float*>(s_m)[r] = ml.x;
+    reinterpret_cast<float*>(s_inv)[r] = ml.y;
+    reinterpret_cast<int*>(s_pos)[r] = r < p.rows ? first + r / p.group : -1;   // -1 sees nothing
   }
+  __syncthreads();
+  const int sub = threadIdx.x % G, quads = p.row_pad / 4;
+  const float* const scores = p.scores + bh * p.score_head;
+  float* const weights = p.weights + (int64_t)bh * p.cap;
+#pragma unroll 1
+  for (int64_t at = lo + (int64_t)chunk * kBlock; at < end; at += (int64_t)chunks.by * kBlock)
+#pragma unroll 1
+    for (int round = 0; round < kWeightRounds; ++round) {
+      const int64_t j0 = at + round * (kStep * kWeightKeys) + threadIdx.x / G;
+      float sum[kWeightKeys], was[kWeightKeys];
+#pragma unroll
+      for (int i = 0; i < kWeightKeys; ++i) {
+        sum[i] = was[i] = 0.f;
+        if (sub == 0 && j0 + i * kStep < end) was[i] = weights[j0 + i * kStep];
+      }
+#pragma unroll 1
+      for (int q = sub; q < quads; q += G) {
+        float4 v[kWeightKeys];
+#pragma unroll
+        for (int i = 0; i < kWeightKeys; ++i)
+          if (j0 + i * kStep < end)
+            v[i] = *reinterpret_cast<const float4*>(scores + (j0 + i * kStep) * p.row_pad + 4 * q);
+        const float4 m = s_m[q], inv = s_inv[q];
+        const int4 pos = s_pos[q];
+#pragma unroll
+        for (int i = 0; i < kWeightKeys; ++i) {
+          const int64_t j = j0 + i * kStep;
+          // (what a row does not see may not have been written)
+          auto add = [&](float s, float m, float inv, int pos) {
+            if (j <= pos && (p.window <= 0 || j > pos - p.window)) sum[i] += exp2_fast(s - m) * inv;
+          };
+          add(v[i].x, m.x, inv.x, pos.x);
+          add(v[i].y, m.y, inv.y, pos.y);
+          add(v[i].z, m.z, inv.z, pos.z);
+          add(v[i].w, m.w, inv.w, pos.w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kWeightKeys; ++i) {
+#pragma unroll
+        for (int d = 1; d < G; d <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+        if (sub == 0 && j0 + i * kStep < end) weights[j0 + i * kStep] = was[i] + sum[i];
+      }
+    }
+}
+
+template <int G>
+int launch_weights(Params p, int64_t heads, cudaStream_t stream) {
+  constexpr int kBlock = kWeightThreads / G * kWeightKeys * kWeightRounds;
+  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
+  const int64_t chunks = std::min<int64_t>((keys + kBlock - 1) / kBlock, 0x7fffffff / heads);
+  p.heads = divisor(p.Hkv);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(heads * chunks));
+  cfg.blockDim = dim3(kWeightThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, weights_kernel<G>, (const Params)p, divisor((uint32_t)chunks)) == cudaSuccess)
+    return kOk;
+  cudaGetLastError();
+  return kErrLaunch;
 }
 
 template <typename E, int NW, int NT>
@@ -682,22 +746,13 @@ int launch_decode_q4(const DecodeQ4Call& c) {
     rc = c.D == 128 ? (few ? launch<float, 1, 1>(p, c) : launch<float, 1, 2>(p, c))
                     : (few ? launch<float, 4, 1>(p, c) : launch<float, 4, 2>(p, c));
   if (rc != kOk || !c.weights) return rc;
-  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
-  const int64_t chunks = std::min<int64_t>((keys + kWeightThreads - 1) / kWeightThreads, 0x7fffffff / heads);
-  p.heads = divisor(p.Hkv);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(heads * chunks));
-  cfg.blockDim = dim3(kWeightThreads);
-  cfg.stream = c.stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, weights_kernel, (const Params)p, divisor((uint32_t)chunks)) == cudaSuccess)
-    return kOk;
-  cudaGetLastError();
-  return kErrLaunch;
+  // as many lanes to a key as it has four rows
+  const int quads = p.row_pad / 4;
+  return quads <= 1   ? launch_weights<1>(p, heads, c.stream)
+         : quads <= 2 ? launch_weights<2>(p, heads, c.stream)
+         : quads <= 4 ? launch_weights<4>(p, heads, c.stream)
+         : quads <= 8 ? launch_weights<8>(p, heads, c.stream)
+                      : launch_weights<32>(p, heads, c.stream);
 }
 
 }  // namespace pfa

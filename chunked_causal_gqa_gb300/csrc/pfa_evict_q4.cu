@@ -9,11 +9,12 @@
 // a time, from histograms that the blocks add up over distributed shared memory; then the kept rows
 // are listed in order, each warp counting the kept rows in front of its own.
 //
+// Weights move and become zero there too: every block has read its own by then.
+//
 // move_kernel, a cluster for each head and array: kept rows move down in place.  A row never moves
 // up, so what a round writes (rows 0 .. below its end) is no source of a later one; in a
-// round, which takes up to a megabyte, the cluster's barrier stands between the reads and the writes.
-// The weights, 4 bytes a row, are moved by a cluster for each sequence, a block for each head, which
-// also knows when every block has read the sequence's length.
+// round, which takes up to half a megabyte, the cluster's barrier stands between the reads and the
+// writes.
 #include "pfa_internal.h"
 #include "pfa_ptx.cuh"
 #include "pfa_q4.cuh"
@@ -23,8 +24,8 @@
 namespace pfa {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 4 * kThreads;
 constexpr int kHeld = 16384;     // weights of a block in shared memory; others are read again
 constexpr int kPieces = 8;       // of a thread in a round
 constexpr int kMaxCluster = 8;
@@ -40,6 +41,7 @@ struct Params {
   int Hkv, heads;       // of a sequence, in all
   int held;             // weights of a block in shared memory
   int code_bytes, scale_bytes;   // of a row
+  Divisor code_pieces, scale_pieces, one;   // of a row
   unsigned* err;
 };
 
@@ -57,12 +59,22 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A word of block `rank`'s shared memory.
-__device__ __forceinline__ int remote(const int* p, uint32_t rank) {
+// Words of block `rank`'s shared memory.
+__device__ __forceinline__ uint32_t remote_address(const void* p, uint32_t rank) {
   uint32_t a;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ int4 remote4(const int* p, uint32_t rank) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(remote_address(p, rank)));
+  return v;
+}
+__device__ __forceinline__ int2 remote2(const int* p, uint32_t rank) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y) : "r"(remote_address(p, rank)));
   return v;
 }
 
@@ -83,15 +95,48 @@ __device__ __forceinline__ int warp_scan(int x) {   // inclusive
   return x;
 }
 
+// Rows `rows` of width.by pieces move to 0 .. keep - 1, in place.  `rank` of `size` blocks; barrier(): theirs.
+template <typename T, typename B>
+__device__ __forceinline__ void move_rows(T* base, const int32_t* rows, int keep, const Divisor& width, int rank,
+                                          int size, B&& barrier) {
+  const int w = (int)width.by, per_round = size * (kThreads * kPieces) / width;   // rows of a round
+#pragma unroll 1
+  for (int at = 0; at < keep;) {
+    const int here = min(per_round, keep - at), pieces = here * w;
+    // consecutive pieces for the threads of a block, runs of kThreads for the blocks in turn
+    const int e0 = rank * kThreads + (int)threadIdx.x;
+    T x[kPieces];
+    int from[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int e = e0 + i * size * kThreads;
+      if (e < pieces) from[i] = rows[at + e / width];
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int e = e0 + i * size * kThreads;
+      if (e < pieces) x[i] = base[(int64_t)from[i] * w + (e - e / width * w)];
+    }
+    barrier();
+    T* const to = base + (int64_t)at * w;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int e = e0 + i * size * kThreads;
+      if (e < pieces) to[e] = x[i];
+    }
+    at += here;
+  }
+}
+
 struct Select {
-  int hist[3][kBins];                // a pass each: other blocks may still read the last one
-  int sums[kWarps];
-  int above[kWarps], ties[kWarps];   // rows of a warp that stay for sure, and at the border
-  int total[2];
+  alignas(16) int hist[3][kBins];    // a pass each: other blocks may still read the last one
+  int sums[32];
+  int sure[32], ties[32];            // rows of a warp that stay for sure, and at the border
+  alignas(8) int total[2];           // and of the block
   int digit, left;
 };
 
-__global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Select& sm = *reinterpret_cast<Select*>(smem_raw);
   float* const held = reinterpret_cast<float*>(smem_raw + sizeof(Select));
@@ -114,46 +159,50 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
   const int64_t begin = (int64_t)rank * per_warp * kWarps;
   const int j0 = (int)min(begin, (int64_t)n), j1 = (int)min(begin + (int64_t)per_warp * kWarps, (int64_t)n);
   const int m = n - p.recent;          // candidates; more of them than places
-  const float* const w = p.weights + (int64_t)bh * p.cap;
+  float* const w = p.weights + (int64_t)bh * p.cap;
   const int cached = min(j1 - j0, p.held);
 #pragma unroll 8
   for (int i = tid; i < cached; i += kThreads) held[i] = w[j0 + i];
   for (int i = tid; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  if (tid < 32) sm.sums[tid] = sm.sure[tid] = sm.ties[tid] = 0;
   __syncthreads();
   auto weight = [&](int i) { return i < cached ? held[i] : w[j0 + i]; };   // row j0 + i
 
   uint32_t key = 0, mask = 0;
   int left = p.keep - p.recent;        // of the candidates that agree with key so far
   if (left > 0) {
-    const int mine = min(j1, m) - j0;  // candidates of this block (or fewer than none)
+    const int candidates = min(j1, m) - j0;  // of this block (or fewer than none)
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       int* const hist = sm.hist[pass];
 #pragma unroll 4
-      for (int i = tid; i < mine; i += kThreads) {
+      for (int i = tid; i < candidates; i += kThreads) {
         const uint32_t k = key_of(weight(i));
         if ((k & mask) == key) atomicAdd(&hist[k >> shift & (kBins - 1)], 1);
       }
       cluster_barrier();
-      // thread t has bins 2047 - 2 t and the one below
-      const int hi = kBins - 1 - 2 * tid;
-      int c0 = 0, c1 = 0;
-      for (uint32_t r = 0; r < size; ++r) {
-        c0 += remote(&hist[hi], r);
-        c1 += remote(&hist[hi - 1], r);
-      }
-      const int up = warp_scan(c0 + c1);
+      // thread t has bins top - 3 .. top; larger digits are those of the threads below it
+      const int top = kBins - 1 - 4 * tid;
+      int4 v[kMaxCluster];
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxCluster; ++r)
+        v[r] = r < size ? remote4(&hist[top - 3], r) : make_int4(0, 0, 0, 0);
+      int c[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) c[0] += v[r].w, c[1] += v[r].z, c[2] += v[r].y, c[3] += v[r].x;
+      const int mine = c[0] + c[1] + c[2] + c[3], up = warp_scan(mine);
       if (lane == 31) sm.sums[warp] = up;
       __syncthreads();
-      const int before_warp = warp_scan(sm.sums[lane]) - sm.sums[lane];
-      const int above = __shfl_sync(0xffffffffu, before_warp, warp) + up - c0 - c1;
-      if (above < left && left <= above + c0) {
-        sm.digit = hi;
+      int above = warp_scan(sm.sums[lane]) - sm.sums[lane];
+      above = __shfl_sync(0xffffffffu, above, warp) + up - mine;
+      if (above < left && left <= above + mine) {   // one thread
+        int d = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (d == i && left > above + c[i]) above += c[i], ++d;
+        sm.digit = top - d;
         sm.left = left - above;
-      } else if (above + c0 < left && left <= above + c0 + c1) {
-        sm.digit = hi - 1;
-        sm.left = left - above - c0;
       }
       __syncthreads();
       key |= (uint32_t)sm.digit << shift;
@@ -187,103 +236,70 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
     ties += __popc(t);
   }
   if (lane == 0) {
-    sm.above[warp] = sure;
+    sm.sure[warp] = sure;
     sm.ties[warp] = ties;
   }
   __syncthreads();
-  int s_before = warp_scan(sm.above[lane]), t_before = warp_scan(sm.ties[lane]);
+  int s_before = warp_scan(sm.sure[lane]), t_before = warp_scan(sm.ties[lane]);
   if (tid == 31) {
     sm.total[0] = s_before;
     sm.total[1] = t_before;
   }
-  s_before = __shfl_sync(0xffffffffu, s_before - sm.above[lane], warp);
+  s_before = __shfl_sync(0xffffffffu, s_before - sm.sure[lane], warp);
   t_before = __shfl_sync(0xffffffffu, t_before - sm.ties[lane], warp);
   cluster_barrier();
-  for (uint32_t r = 0; r < rank; ++r) {
-    s_before += remote(&sm.total[0], r);
-    t_before += remote(&sm.total[1], r);
+#pragma unroll
+  for (uint32_t r = 0; r < kMaxCluster; ++r) {
+    const int2 v = r < rank ? remote2(sm.total, r) : make_int2(0, 0);
+    s_before += v.x;
+    t_before += v.y;
   }
+  // Weights that are all in shared memory go to their places at once: no block reads its own from
+  // global memory any more.
+  const bool all_held = (int64_t)per_warp * kWarps <= p.held;
   const uint32_t below = (1u << lane) - 1;
   for (int i = i0; i < i0 + per_warp && j0 + i < j1; i += 32) {
     uint32_t s, t;
     look(i, s, t);
     const int rank_t = t_before + __popc(t & below);
-    if ((s >> lane & 1) || ((t >> lane & 1) && rank_t < left))
-      rows[s_before + __popc(s & below) + min(rank_t, left)] = j0 + i + lane;
+    if ((s >> lane & 1) || ((t >> lane & 1) && rank_t < left)) {
+      const int to = s_before + __popc(s & below) + min(rank_t, left);
+      rows[to] = j0 + i + lane;
+      if (all_held) w[to] = held[i + lane];
+    }
     s_before += __popc(s);
     t_before += __popc(t);
   }
-  cluster_barrier();   // the others have read this block's totals
+  cluster_barrier();   // the others have read this block's totals, and written their part of the list
+  if (!all_held) move_rows(w, rows, p.keep, p.one, (int)rank, (int)size, [] { cluster_barrier(); });
+  for (int64_t j = p.keep + (int64_t)rank * kThreads + tid; j < n; j += size * kThreads)
+    w[j] = 0.f;
 }
 
-// Rows `rows` of `width` pieces move to 0 .. keep - 1, in place.  `rank` of `size` blocks; barrier(): theirs.
-template <typename T, typename B>
-__device__ __forceinline__ void move_rows(T* base, const int32_t* rows, int keep, int width, int rank, int size,
-                                          B&& barrier) {
-  const int64_t all = (int64_t)keep * width, round = (int64_t)size * kThreads * kPieces;
-  // consecutive pieces for the threads of a block, runs of kThreads for the blocks in turn
-#pragma unroll 1
-  for (int64_t at = 0; at < all; at += round) {
-    T x[kPieces];
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int64_t e = at + (int64_t)(i * size + rank) * kThreads + threadIdx.x;
-      if (e < all) {
-        const int64_t r = width == 1 ? e : width == 4 ? e >> 2 : e / width;
-        x[i] = base[(int64_t)rows[r] * width + (e - r * width)];
-      }
-    }
-    barrier();
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int64_t e = at + (int64_t)(i * size + rank) * kThreads + threadIdx.x;
-      if (e < all) base[e] = x[i];
-    }
-  }
-}
-
-__global__ void __launch_bounds__(kThreads, 1) move_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 2) move_kernel(const Params p) {
   asm volatile("griddepcontrol.launch_dependents;");
   const int rank = (int)cluster_rank(), size = (int)cluster_size();
-  // first the codes of K and of V, a head each; then the weights, a sequence each; then the scales
-  int id = blockIdx.x / size;
-  const int B = p.heads / p.Hkv;
-  int part = id / p.heads;
+  const int id = blockIdx.x / size, part = id / p.heads;
+  const int64_t bh = id - part * p.heads, b = bh / p.Hkv;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (id >= 2 * p.heads && id < 2 * p.heads + B) {
-    const int b = id - 2 * p.heads;
+  if (part == 0 && bh == b * p.Hkv && rank == 0 && threadIdx.x == 0) {   // lengths_out may be lengths
     const int64_t n = p.lengths[b];
-    cluster_barrier();   // lengths_out may be lengths
-    const bool cut = n > p.keep && n <= p.cap;
-    if (rank == 0 && threadIdx.x == 0) p.lengths_out[b] = cut ? p.keep : n;
-    if (!cut) return;
-    for (int h = rank; h < p.Hkv; h += size) {
-      const int64_t bh = (int64_t)b * p.Hkv + h;
-      float* const w = p.weights + bh * p.cap;
-      move_rows(w, p.rows + bh * p.keep, p.keep, 1, 0, 1, [] { __syncthreads(); });
-      __syncthreads();
-      for (int64_t j = p.keep + threadIdx.x; j < n; j += kThreads) w[j] = 0.f;
-    }
-    return;
+    p.lengths_out[b] = n > p.keep && n <= p.cap ? p.keep : n;
   }
-  if (id >= 2 * p.heads) part = 2 + (id - 2 * p.heads - B) / p.heads, id -= B;
-  const int64_t bh = id % p.heads;
   const int32_t* const rows = p.rows + bh * p.keep;
   if (rows[p.keep - 1] < p.keep) return;   // nothing moves (the same for the whole cluster)
   const int bytes = part < 2 ? p.code_bytes : p.scale_bytes;
   uint8_t* const base = (part == 0 ? p.part[0] : part == 1 ? p.part[1] : part == 2 ? p.part[2] : p.part[3]) +
                         bh * p.cap * bytes;
+  const Divisor& pieces = part < 2 ? p.code_pieces : p.scale_pieces;
   auto barrier = [] { cluster_barrier(); };
-  if (bytes % 16 == 0)
-    move_rows(reinterpret_cast<uint4*>(base), rows, p.keep, bytes / 16, rank, size, barrier);
-  else if (bytes % 8 == 0)
-    move_rows(reinterpret_cast<uint2*>(base), rows, p.keep, bytes / 8, rank, size, barrier);
-  else if (bytes % 4 == 0)
-    move_rows(reinterpret_cast<uint32_t*>(base), rows, p.keep, bytes / 4, rank, size, barrier);
-  else if (bytes % 2 == 0)
-    move_rows(reinterpret_cast<uint16_t*>(base), rows, p.keep, bytes / 2, rank, size, barrier);
-  else
-    move_rows(base, rows, p.keep, bytes, rank, size, barrier);
+  switch (bytes / (int)pieces.by) {
+    case 16: move_rows(reinterpret_cast<uint4*>(base), rows, p.keep, pieces, rank, size, barrier); break;
+    case 8: move_rows(reinterpret_cast<uint2*>(base), rows, p.keep, pieces, rank, size, barrier); break;
+    case 4: move_rows(reinterpret_cast<uint32_t*>(base), rows, p.keep, pieces, rank, size, barrier); break;
+    case 2: move_rows(reinterpret_cast<uint16_t*>(base), rows, p.keep, pieces, rank, size, barrier); break;
+    default: move_rows(base, rows, p.keep, pieces, rank, size, barrier);
+  }
 }
 
 int launch(void (*kernel)(const Params), int64_t clusters, int size, size_t smem, const Params& p,
@@ -314,6 +330,13 @@ int blocks_for(int64_t n, int64_t most) {
   return c;
 }
 
+// Pieces of a row of n bytes, as large as its alignment lets them be, up to 16 bytes.
+Divisor pieces_of(int n) {
+  int size = 16;
+  while (n % size) size /= 2;
+  return divisor((uint32_t)(n / size));
+}
+
 }  // namespace
 
 int launch_cache_evict_q4(const EvictQ4Call& c) {
@@ -328,6 +351,8 @@ int launch_cache_evict_q4(const EvictQ4Call& c) {
   p.part[0] = (uint8_t*)c.cache.k4; p.part[1] = (uint8_t*)c.cache.v4;
   p.part[2] = (uint8_t*)c.cache.k_scale; p.part[3] = (uint8_t*)c.cache.v_scale;
   p.code_bytes = c.D / 2; p.scale_bytes = c.D / 16;
+  p.code_pieces = pieces_of(p.code_bytes); p.scale_pieces = pieces_of(p.scale_bytes);
+  p.one = divisor(1);
   p.weights = c.weights;
   p.lengths = c.lengths; p.lengths_out = c.lengths_out; p.rows = c.rows_out;
   p.cap = c.cache.max_seq_len;
@@ -335,14 +360,14 @@ int launch_cache_evict_q4(const EvictQ4Call& c) {
   p.Hkv = c.Hkv;
   p.err = c.err;
   const int64_t heads = c.B * c.Hkv;
-  if ((4 * heads + c.B) * kMaxCluster > 0x7fffffff) return kErrShape;
+  if (4 * heads * kMaxCluster > 0x7fffffff) return kErrShape;
   p.heads = (int)heads;
   const int sel = blocks_for(p.cap, 8192);
   p.held = (int)std::min<int64_t>(kHeld, (p.cap + (int64_t)sel * kThreads - 1) / ((int64_t)sel * kThreads) * kThreads);
   rc = launch(select_kernel, heads, sel, sizeof(Select) + p.held * sizeof(float), p, c.stream);
   if (rc != kOk) return rc;
   const int mov = blocks_for(c.keep * p.code_bytes, (int64_t)kThreads * kPieces * 16);
-  return launch(move_kernel, 4 * heads + c.B, mov, 0, p, c.stream);
+  return launch(move_kernel, 4 * heads, mov, 0, p, c.stream);
 }
 
 }  // namespace pfa
