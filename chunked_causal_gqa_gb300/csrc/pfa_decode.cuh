@@ -1,7 +1,7 @@
 // pfa_decode.cuh -- what the decode kernels over the 8-bit and the 4-bit cache share: the list
 // of work and its split over the blocks, and the kernel that joins partial sums.
 //
-// Work split: tiles of 32 keys ("units") of all row tiles, sequences and heads form one
+// Work split: tiles of P::kUnit keys ("units") of all row tiles, sequences and heads form one
 // list, cut into equal runs, one for each block.  What covers a head alone is stored as
 // output by the block, what covers part of it goes to the workspace, and a second kernel,
 // launched so that its start overlaps, joins the parts in order.
@@ -18,12 +18,11 @@ namespace pfa {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kUnit = 32;                      // keys of a unit
 constexpr int kMaxEntries = 1 << 14;           // (sequence, row tile) pairs of one launch
 constexpr int64_t kMaxUnits = 1 << 30;         // units that a launch can list
 
 // What the list and the join need of a launch.  A kernel's own parameters derive from it and
-// say P::kHeadCost, what the start and end of a head cost a block, in units (its query rows, the
+// say P::kUnit, P::kHeadCost, what the start and end of a head cost a block, in units (its query rows, the
 // join), and P::kSums, whether row sums can be asked for.
 struct ListParams {
   const void* q;
@@ -70,8 +69,8 @@ __device__ __forceinline__ Entry<P::kHeadCost> entry_of(const P& p, int e) {
   const int first = x.end - (int)p.T;
   x.hi = first + (x.r0 + x.nr - 1) / p.group;
   x.lo = p.window > 0 ? max(0, first + x.r0 / p.group - p.window + 1) : 0;
-  x.u0 = x.lo / kUnit;
-  x.n = x.bad || x.hi < 0 ? 0 : x.hi / kUnit - x.u0 + 1;
+  x.u0 = x.lo / P::kUnit;
+  x.n = x.bad || x.hi < 0 ? 0 : x.hi / P::kUnit - x.u0 + 1;
   return x;
 }
 
@@ -393,7 +392,7 @@ struct Kernels {
 // its list can count.
 template <typename P>
 int launch_list(const Kernels<P>& k, P p, int64_t B, int num_sms, cudaStream_t stream) {
-  const int64_t of_entry = (int64_t)p.Hkv * (p.cap / kUnit + 2 + P::kHeadCost);
+  const int64_t of_entry = (int64_t)p.Hkv * (p.cap / P::kUnit + 2 + P::kHeadCost);
   if (of_entry > kMaxUnits) return kErrShape;
   const int tiles = (p.rows + k.rm - 1) / k.rm;
   const int most = (int)std::min<int64_t>(kMaxEntries, kMaxUnits / of_entry);

@@ -29,7 +29,7 @@
 // The exponent's base rises only when a score passes it by 2^4, so that most units need no
 // maximum across lanes and no rescaling: a weight is 2^(s - base) 2^11, at most 2^15.
 //
-// Work split and join: pfa_decode.cuh.  Four warps take a run's units of 32 keys in turn, each with
+// Work split and join: pfa_decode.cuh.  Four warps take a run's units of 64 keys in turn, each with
 // its own ring filled by cp.async; head_dim 512: four warps share a unit, each with 128 channels, and
 // exchange partial scores.
 //
@@ -46,15 +46,17 @@
 namespace pfa {
 namespace {
 
-constexpr int kStages = 3;
+constexpr int kUnit = 64, kTiles = kUnit / 16;   // keys of a unit; products that hold them
+constexpr int kStages = 2;
 constexpr int kHalf = kUnit * 64;              // bytes of a warp's K (or V) codes of a stage
 constexpr int kScales = kUnit * 8;             // and of its scales
 constexpr int kStageBytes = 2 * (kHalf + kScales);
-constexpr int kJoinBytes = kWarps * 8 * 128 * 4;  // joins: 8 row sums of 128 floats for each warp
+// Joins: 8 row sums of 128 floats for each warp.  Score exchange: twice those of a unit and 16 rows.
+constexpr int kJoinBytes = 2 * kWarps * kUnit * 16 * 4;
 constexpr float kLag = 4.f, kUp = 11.f;        // powers of two: of a score above the base; of weights
 
 struct Params : ListParams {
-  static constexpr int kHeadCost = 16;
+  static constexpr int kUnit = pfa::kUnit, kHeadCost = 8;
   static constexpr bool kSums = true;
   const uint8_t *k4, *v4, *k_scale, *v_scale;
   float* scores;       // null, or [head][keys of whole units][row_pad]
@@ -106,20 +108,19 @@ struct Shared {
   ListShared list;
 };
 
-// fp32 tiles of 16 rows need two sets of 32 query registers and two of 32 sums.
-template <typename E, int NT>
-constexpr int kBlocks = sizeof(E) == 4 && NT == 2 ? 2 : 3;
-static_assert(3 * (sizeof(Shared) + 1024) <= 228 * 1024, "shared memory of an SM");
+constexpr int kBlocksPerSm = 2;
+static_assert(kBlocksPerSm * (sizeof(Shared) + 1024) <= 228 * 1024, "shared memory of an SM");
 
 // NW: warps of a unit (head_dim / 128).  NT: products a tile, tiles of 8 NT rows.
 template <typename E, int NW, int NT>
-__global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Params p) {
   // A team is a warp or the block, so that every barrier is the block's: it does not count
   // warps that have ended, and no lengths, not even changing ones, leave a warp waiting.
   static_assert(NW == 1 || NW == kWarps, "barriers are the block's");
   constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = 8 * NT;
   constexpr bool F32 = sizeof(E) == 4;
   constexpr int SETS = F32 ? 2 : 1;   // high and low halves
+  static_assert(kJoinBytes >= kWarps * 8 * 128 * 4 && kJoinBytes >= 2 * NW * kTiles * NT * 32 * 16, "join area");
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -165,43 +166,69 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(cons
 
   const uint32_t ring = smem_u32(sm.ring[warp]);
   // Copies of a unit: K's codes and scales, then V's, each a group of its own: K's place is free
-  // for a later unit when the scores are done, V's when its sum is.  Copy c of 4 is row
-  // 8 c + lane / 4, piece lane % 4; and the scales of row `lane`.
-  const uint32_t dst = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 2) & 2)) << 4);
+  // for a later unit when the scores are done, V's when its sum is.  Copy c of codes
+  // is row 8 c + lane / 4, piece lane % 4; of scales, row 32 c + lane.
+  // What moves from unit to unit is one offset of codes and one of scales, the same for K and V.
+  const uint32_t dst = ring + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 2) & 2)) << 4);
+  const uint32_t dst_scales = ring + kHalf + lane * 8;
   struct Source {
-    int64_t row;           // cache row of key0, all heads counted
-    int key0, lo, hi;      // on: hi >= lo
+    int64_t codes, scales;   // of this lane
+    int lo, hi;              // rows [lo, hi] of the unit are copied
   } src = {};
-  auto copy_half = [&](uint32_t to, const uint8_t* codes, const uint8_t* scales) {
-    const uint8_t* from = codes + (src.row + (lane >> 2)) * (D / 2) + part * 64 + (lane & 3) * 16;
+  auto copy_half = [&](int stage_at, const uint8_t* codes, const uint8_t* scales) {
+    const uint8_t* from = codes + src.codes;
+    if (src.lo <= 0 && src.hi >= kUnit - 1) {   // all rows
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int key = src.key0 + 8 * c + (lane >> 2);
-      const bool on = key >= src.lo && key <= src.hi;
-      copy16(to + c * 512 + dst, on ? from + c * 8 * (D / 2) : codes, on);
+      for (int c = 0; c < kUnit / 8; ++c) copy16(dst + stage_at + c * 512, from + c * 8 * (D / 2), true);
+#pragma unroll
+      for (int c = 0; c < kUnit / 32; ++c)
+        copy8(dst_scales + stage_at + c * 256, scales + src.scales + c * 32 * (D / 16), true);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kUnit / 8; ++c) {
+        const int row = 8 * c + (lane >> 2);
+        const bool on = row >= src.lo && row <= src.hi;
+        copy16(dst + stage_at + c * 512, on ? from + c * 8 * (D / 2) : codes, on);
+      }
+#pragma unroll
+      for (int c = 0; c < kUnit / 32; ++c) {
+        const int row = 32 * c + lane;
+        const bool on = row >= src.lo && row <= src.hi;
+        copy8(dst_scales + stage_at + c * 256, on ? scales + src.scales + c * 32 * (D / 16) : scales, on);
+      }
     }
-    const int key = src.key0 + lane;
-    const bool on = key >= src.lo && key <= src.hi;
-    copy8(to + kHalf + lane * 8, on ? scales + (src.row + lane) * (D / 16) + part * 8 : scales, on);
+  };
+  auto source = [&]() {   // of the first unit of a piece that is this team's
+    const int64_t row = (in.x.b * p.Hkv + in.h) * p.cap + (int64_t)(in.x.u0 + in.k) * kUnit;
+    src.codes = (row + (lane >> 2)) * (D / 2) + part * 64 + (lane & 3) * 16;
+    src.scales = (row + lane) * (D / 16) + part * 8;
+    src.lo = in.x.lo - (in.x.u0 + in.k) * kUnit;
+    src.hi = in.x.hi - (in.x.u0 + in.k) * kUnit;
   };
   auto copy_k = [&](int stage) {
-    while (!in.done() && in.k >= in.kend) in.next_piece(p, team);
-    src.lo = 0;
-    src.hi = -1;
+    if (!in.done() && in.k >= in.kend) {
+#pragma unroll 1
+      do in.next_piece(p, team);
+      while (!in.done() && in.k >= in.kend);
+      if (!in.done()) source();
+    }
+    if (!in.done()) copy_half(stage * kStageBytes, p.k4, p.k_scale);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // (after copy_k of the same unit: on to the team's next one)
+  auto copy_v = [&](int stage) {
     if (!in.done()) {
-      src.key0 = (in.x.u0 + in.k) * kUnit;
-      src.lo = in.x.lo;
-      src.hi = in.x.hi;
-      src.row = (in.x.b * p.Hkv + in.h) * p.cap + src.key0;
-      copy_half(ring + stage * kStageBytes, p.k4, p.k_scale);
+      copy_half(stage * kStageBytes + kHalf + kScales, p.v4, p.v_scale);
       in.k += TEAMS;
+      src.codes += TEAMS * kUnit * (D / 2);
+      src.scales += TEAMS * kUnit * (D / 16);
+      src.lo -= TEAMS * kUnit;
+      src.hi -= TEAMS * kUnit;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto copy_v = [&](int stage) {
-    if (src.hi >= src.lo) copy_half(ring + stage * kStageBytes + kHalf + kScales, p.v4, p.v_scale);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
+  // (a team may have nothing in its run's first piece)
+  if (in.k < in.kend) source();
 #pragma unroll 1
   for (int s = 0; s < kStages; ++s) {
     copy_k(s);
@@ -280,9 +307,13 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(cons
       for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[i][t][c] = 0.f;
-    float m[NT][2], l[NT][2];   // base; this lane's part of the sum
+    // Base, kUp - base (0 for none), this lane's part of the sum; what an exponent may be before
+    // the bases are looked at.
+    float m[NT][2], up[NT][2], l[NT][2], limit = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) m[i][c] = -INFINITY, up[i][c] = l[i][c] = 0.f;
 
 #pragma unroll 1
     for (; cu.k < cu.kend; cu.k += TEAMS) {
@@ -290,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(cons
       __syncwarp();
       const uint32_t kb = ring + stage * kStageBytes, vb = kb + kHalf + kScales;
       // ---- scores: [product of 16 keys][tile]{key g, row 2 qd, + 1; key g + 8, the same rows}
-      float s[2][NT][4];
+      float s[kTiles][NT][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kTiles; ++h) {
         float acc[NT][SETS][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -331,38 +362,40 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(cons
       copy_k(stage);
       if constexpr (NW > 1) {
         // the team's partial scores, summed in the same order by each warp
-        float4* ex = reinterpret_cast<float4*>(sm.join) + swap * (NW * 2 * NT * 32);
+        float4* ex = reinterpret_cast<float4*>(sm.join) + swap * (NW * kTiles * NT * 32);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kTiles; ++h)
 #pragma unroll
           for (int i = 0; i < NT; ++i)
-            ex[(part * 2 * NT + h * NT + i) * 32 + lane] =
+            ex[(part * kTiles * NT + h * NT + i) * 32 + lane] =
                 make_float4(s[h][i][0], s[h][i][1], s[h][i][2], s[h][i][3]);
         __syncthreads();
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kTiles; ++h)
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             float4 t = ex[(h * NT + i) * 32 + lane];
 #pragma unroll
             for (int w = 1; w < NW; ++w) {
-              const float4 v = ex[(w * 2 * NT + h * NT + i) * 32 + lane];
+              const float4 v = ex[(w * kTiles * NT + h * NT + i) * 32 + lane];
               t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
             }
             s[h][i][0] = t.x; s[h][i][1] = t.y; s[h][i][2] = t.z; s[h][i][3] = t.w;
           }
         swap ^= 1;
       }
+      const int key0 = (x.u0 + cu.k) * kUnit;
+      const bool masked = key0 < all_lo || key0 + kUnit - 1 > all_hi;
+      // ---- scores become exponents over the base, up = kUp - base; hidden ones -infinity
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kTiles; ++h)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[h][i][c] *= srow[i][c & 1];
-      const int key0 = (x.u0 + cu.k) * kUnit;
-      if (key0 < all_lo || key0 + kUnit - 1 > all_hi) {
+          for (int c = 0; c < 4; ++c) s[h][i][c] = fmaf(s[h][i][c], srow[i][c & 1], up[i][c & 1]);
+      if (masked) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kTiles; ++h)
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -376,33 +409,48 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(cons
         for (int i = 0; i < NT; ++i) {
           const int r = x.r0 + 8 * i + 2 * qd;
           if (r < p.rows) {
+            float* to = scores + (int64_t)(key0 + (int)k_row) * p.row_pad + r;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kTiles; ++h)
 #pragma unroll
               for (int c = 0; c < 2; ++c)
-                *reinterpret_cast<float2*>(scores + (int64_t)(key0 + h * 16 + c * 8 + (int)k_row) * p.row_pad + r) =
-                    make_float2(s[h][i][2 * c], s[h][i][2 * c + 1]);
+                *reinterpret_cast<float2*>(to + (h * 16 + c * 8) * p.row_pad) =
+                    make_float2(s[h][i][2 * c] - up[i][0], s[h][i][2 * c + 1] - up[i][1]);
           }
         }
       }
       // ---- the base rises where a score is far above it
-      bool rises = false;
+      auto largest = [&](int i, int c) {
+        float mx = fmaxf(s[0][i][c], s[0][i][c + 2]);
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+        for (int h = 1; h < kTiles; ++h) mx = fmaxf(mx, fmaxf(s[h][i][c], s[h][i][c + 2]));
+        return mx;
+      };
+      float most = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          rises |= fmaxf(fmaxf(s[0][i][c], s[0][i][c + 2]), fmaxf(s[1][i][c], s[1][i][c + 2])) > m[i][c] + kLag;
-      if (__any_sync(0xffffffffu, rises)) {
+      for (int i = 0; i < NT; ++i) most = fmaxf(most, fmaxf(largest(i, 0), largest(i, 1)));
+      if (__any_sync(0xffffffffu, most > limit)) {
+        limit = kUp + kLag;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(fmaxf(s[0][i][c], s[0][i][c + 2]), fmaxf(s[1][i][c], s[1][i][c + 2]));
+            float mx = largest(i, c);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            mx = fmaxf(mx, m[i][c]);
-            const float a = exp2_fast(m[i][c] - (mx == -INFINITY ? 0.f : mx));
+            mx = fmaxf(mx - up[i][c], m[i][c]);
+            if (mx == -INFINITY) {   // nothing seen yet: the next unit asks again
+              limit = -INFINITY;
+              continue;
+            }
+            const float a = exp2_fast(m[i][c] - mx), by = kUp - mx - up[i][c];
             m[i][c] = mx;
+            up[i][c] = kUp - mx;
+#pragma unroll
+            for (int h = 0; h < kTiles; ++h) {
+              s[h][i][c] += by;
+              s[h][i][c + 2] += by;
+            }
             l[i][c] *= a;
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
@@ -412,27 +460,25 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(cons
           }
       }
       // ---- weights and their sums; the weights as the second operand
-      uint32_t pf[2][NT][SETS][2];
+      uint32_t pf[kTiles][NT][SETS][2];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const float b0 = m[i][0] == -INFINITY ? 0.f : m[i][0] - kUp, b1 = m[i][1] == -INFINITY ? 0.f : m[i][1] - kUp;
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kTiles; ++h)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float e0 = exp2_fast(s[h][i][2 * c] - b0), e1 = exp2_fast(s[h][i][2 * c + 1] - b1);
-            l[i][0] += e0;
-            l[i][1] += e1;
+            const float w0 = exp2_fast(s[h][i][2 * c]), w1 = exp2_fast(s[h][i][2 * c + 1]);
+            l[i][0] += w0;
+            l[i][1] += w1;
             if constexpr (F32) {
               uint32_t u, v;
-              split2(e0, e1, u, v);
+              split2(w0, w1, u, v);
               pf[h][i][0][c] = transposed(u);
               pf[h][i][1][c] = transposed(v);
             } else {
-              pf[h][i][0][c] = transposed(half2_of(e0, e1));
+              pf[h][i][0][c] = transposed(half2_of(w0, w1));
             }
           }
-      }
       // ---- weighted sum of V
       asm volatile("cp.async.wait_group %0;" :: "n"(2 * kStages - 1) : "memory");
       __syncwarp();
@@ -476,30 +522,33 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<E, NT>)) decode_kernel(cons
       };
       if constexpr (F32) {
         // The tensor cores truncate as they accumulate: over thousands of keys that is a bias of
-        // 1e-5 of the output.  So they add up one unit only, and rounding adds do the rest.
-        uint32_t w[2][2][4], f[2][2];
-        load_v(0, w[0], f[0]);
-        load_v(1, w[1], f[1]);
+        // 1e-5 of the output.  So they add up 32 keys only, and rounding adds do the rest.
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          uint32_t a[2][4];
-          fragment(w[0][t / 4], f[0], t % 4, a[0]);
-          fragment(w[1][t / 4], f[1], t % 4, a[1]);
+        for (int h = 0; h < kTiles; h += 2) {
+          uint32_t w[2][2][4], f[2][2];
+          load_v(h, w[0], f[0]);
+          load_v(h + 1, w[1], f[1]);
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int t = 0; t < 8; ++t) {
+            uint32_t a[2][4];
+            fragment(w[0][t / 4], f[0], t % 4, a[0]);
+            fragment(w[1][t / 4], f[1], t % 4, a[1]);
 #pragma unroll
-            for (int b = SETS - 1; b >= 0; --b) {
-              mma(c, a[0], pf[0][i][b][0], pf[0][i][b][1]);
-              mma(c, a[1], pf[1][i][b][0], pf[1][i][b][1]);
+            for (int i = 0; i < NT; ++i) {
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int b = SETS - 1; b >= 0; --b) {
+                mma(c, a[0], pf[h][i][b][0], pf[h][i][b][1]);
+                mma(c, a[1], pf[h + 1][i][b][0], pf[h + 1][i][b][1]);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[i][t][k] += c[k];
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[i][t][k] += c[k];
           }
         }
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kTiles; ++h) {
           uint32_t w[2][4], f[2];
           load_v(h, w, f);
 #pragma unroll
@@ -680,7 +729,7 @@ int launch(const Params& p, const DecodeQ4Call& c) {
   });
   if (rc != kOk) return rc;
   const Kernels<Params> k = {decode_kernel<E, NW, NT>, join_kernel<Params, E, NW, 8 * NT, 8>,
-                             join_kernel<Params, E, NW, 8 * NT, 1>, 8 * NT, NW, kBlocks<E, NT>,
+                             join_kernel<Params, E, NW, 8 * NT, 1>, 8 * NT, NW, kBlocksPerSm,
                              sizeof(Shared)};
   return launch_list(k, p, c.span.B, c.num_sms, c.stream);
 }
@@ -694,7 +743,7 @@ struct Layout {
 Layout layout(int64_t heads, int rows, int D, int dtype, int64_t cap, bool weights, int num_sms) {
   Layout w = {};
   const int rm = rows <= 8 ? 8 : 16;   // most rows of a tile
-  const size_t parts = 2 * (size_t)num_sms * 3 * (rm * D + rm * 2) * sizeof(float);
+  const size_t parts = 2 * (size_t)num_sms * kBlocksPerSm * (rm * D + rm * 2) * sizeof(float);
   w.sums = (parts + 255) & ~(size_t)255;
   w.scores = w.total = w.sums;
   if (!weights) return w;

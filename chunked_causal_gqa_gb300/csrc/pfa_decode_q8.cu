@@ -62,12 +62,14 @@ namespace {
 
 constexpr int kBlocksPerSm = 2;
 constexpr int kStages = 3;
+constexpr int kUnit = 32;                      // keys of a unit
 constexpr int kHalf = kUnit * 128;             // bytes of a warp's K (or V) part of a stage
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kJoinBytes = kWarps * 8 * 128 * 4;  // joins: 8 row sums of 128 floats for each warp
 constexpr float kWeightScale = 16384.f;
 
 struct Params : ListParams {
+  static constexpr int kUnit = pfa::kUnit;
   static constexpr int kHeadCost = 8;
   static constexpr bool kSums = false;
   const uint8_t *k8, *v8;
