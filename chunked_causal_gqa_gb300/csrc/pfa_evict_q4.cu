@@ -3,7 +3,7 @@
 // For a sequence of n > keep rows, of each kv head: the `recent` newest rows stay, and the keep - recent
 // largest of the others' weights (equal ones: the lower row).
 //
-// select_kernel, a cluster of up to eight blocks for each head, each with a run of its rows in shared memory:
+// select_kernel, a cluster of up to eight blocks for each head, each with a run of its rows in registers:
 // the key of a weight is its bits, turned so that unsigned order is the order of
 // numbers.  Three passes over the candidates find the smallest key that is kept, 11, 11 and 10 bits at
 // a time, from histograms that the blocks add up over distributed shared memory; then the kept rows
@@ -26,7 +26,6 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 4 * kThreads;
-constexpr int kHeld = 16384;     // weights of a block in shared memory; others are read again
 constexpr int kPieces = 8;       // of a thread in a round
 constexpr int kMaxCluster = 8;
 
@@ -39,7 +38,6 @@ struct Params {
   int64_t cap;
   int keep, recent;
   int Hkv, heads;       // of a sequence, in all
-  int held;             // weights of a block in shared memory
   int code_bytes, scale_bytes;   // of a row
   Divisor code_pieces, scale_pieces, one;   // of a row
   unsigned* err;
@@ -83,6 +81,10 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   const uint32_t u = __float_as_uint(w + 0.f);
   if (w != w) return 0xffffffffu;
   return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
+}
+
+__device__ __forceinline__ float weight_of(uint32_t key) {   // (a NaN, but not which; 0 for -0)
+  return __uint_as_float(key ^ (key >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
 __device__ __forceinline__ int warp_scan(int x) {   // inclusive
@@ -136,14 +138,16 @@ struct Select {
   int digit, left;
 };
 
-__global__ void __launch_bounds__(kThreads, 2) select_kernel(const Params p) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  Select& sm = *reinterpret_cast<Select*>(smem_raw);
-  float* const held = reinterpret_cast<float*>(smem_raw + sizeof(Select));
+// R: rows of a lane that stay in registers, their keys; 0: none do, and weights are read in each pass.
+template <int R>
+__global__ void __launch_bounds__(kThreads, R == 32 ? 1 : 2) select_kernel(const Params p) {
+  __shared__ Select sm;
   asm volatile("griddepcontrol.launch_dependents;");
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const int bh = blockIdx.x / size, b = bh / p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  if (tid < 32) sm.sums[tid] = sm.sure[tid] = sm.ties[tid] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t len = p.lengths[b];
   const bool bad = len < 0 || len > p.cap;
@@ -154,33 +158,47 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Params p) {
     for (int64_t i = rank * kThreads + tid; i < p.keep; i += size * kThreads) rows[i] = i < n ? (int)i : -1;
     return;
   }
-  // This block's rows [j0, j1), a whole number of them for each warp.
-  const int per_warp = (int)(((int64_t)n + size * kThreads - 1) / (size * kThreads)) * 32;
-  const int64_t begin = (int64_t)rank * per_warp * kWarps;
-  const int j0 = (int)min(begin, (int64_t)n), j1 = (int)min(begin + (int64_t)per_warp * kWarps, (int64_t)n);
+  // The warp's rows [j0, j1), a whole number of them for each lane; row j0 + 32 i + lane is its i-th.
+  const int per_lane = (int)(((int64_t)n + size * kThreads - 1) / (size * kThreads));
+  const int64_t begin = ((int64_t)rank * kWarps + warp) * per_lane * 32;
+  const int j0 = (int)min(begin, (int64_t)n), j1 = (int)min(begin + per_lane * 32, (int64_t)n);
   const int m = n - p.recent;          // candidates; more of them than places
   float* const w = p.weights + (int64_t)bh * p.cap;
-  const int cached = min(j1 - j0, p.held);
-#pragma unroll 8
-  for (int i = tid; i < cached; i += kThreads) held[i] = w[j0 + i];
-  for (int i = tid; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
-  if (tid < 32) sm.sums[tid] = sm.sure[tid] = sm.ties[tid] = 0;
+  uint32_t held[R > 0 ? R : 1];
+  if constexpr (R > 0) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int j = j0 + 32 * i + lane;
+      held[i] = j < j1 ? __float_as_uint(w[j]) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) held[i] = key_of(__uint_as_float(held[i]));
+  }
   __syncthreads();
-  auto weight = [&](int i) { return i < cached ? held[i] : w[j0 + i]; };   // row j0 + i
+  // f(i, j, key) for each row of the warp's, whole warps at a time: j may be behind j1
+  auto each = [&](auto&& f) {
+    if constexpr (R > 0) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (32 * i < j1 - j0) f(j0 + 32 * i + lane, held[i]);
+    } else {
+#pragma unroll 4
+      for (int j = j0 + lane; j - lane < j1; j += 32) f(j, j < j1 ? key_of(w[j]) : 0u);
+    }
+  };
 
-  uint32_t key = 0, mask = 0;
+  uint32_t key = 0;
   int left = p.keep - p.recent;        // of the candidates that agree with key so far
   if (left > 0) {
-    const int candidates = min(j1, m) - j0;  // of this block (or fewer than none)
+    const int stop = min(j1, m);       // of the warp's candidates
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       int* const hist = sm.hist[pass];
-#pragma unroll 4
-      for (int i = tid; i < candidates; i += kThreads) {
-        const uint32_t k = key_of(weight(i));
-        if ((k & mask) == key) atomicAdd(&hist[k >> shift & (kBins - 1)], 1);
-      }
+      each([&](int j, uint32_t k) {
+        if (j < stop && (pass == 0 || (k ^ key) >> (shift + bits) == 0))
+          atomicAdd(&hist[k >> shift & ((1 << bits) - 1)], 1);
+      });
       cluster_barrier();
       // thread t has bins top - 3 .. top; larger digits are those of the threads below it
       const int top = kBins - 1 - 4 * tid;
@@ -206,35 +224,22 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Params p) {
       }
       __syncthreads();
       key |= (uint32_t)sm.digit << shift;
-      mask |= (uint32_t)(pass == 2 ? 1023 : kBins - 1) << shift;
       left = sm.left;
     }
   }
   // Of the rows with that key the `left` lowest stay (with left 0: none), above it all.
   const bool any = left > 0;
-  const int i0 = warp * per_warp;
-  auto look = [&](int i, uint32_t& sure, uint32_t& tie) {   // of the warp's rows i .. i + 31
-    const int j = j0 + i + lane;
-    bool s = false, t = false;
-    if (j < j1) {
-      if (j >= m) {
-        s = true;
-      } else if (any) {
-        const uint32_t k = key_of(weight(i + lane));
-        s = k > key;
-        t = k == key;
-      }
-    }
-    sure = __ballot_sync(0xffffffffu, s);
-    tie = __ballot_sync(0xffffffffu, t);
+  auto look = [&](int j, uint32_t k, uint32_t& sure, uint32_t& tie) {
+    sure = __ballot_sync(0xffffffffu, j < j1 && (j >= m || (any && k > key)));
+    tie = __ballot_sync(0xffffffffu, j < min(j1, m) && any && k == key);
   };
   int sure = 0, ties = 0;
-  for (int i = i0; i < i0 + per_warp && j0 + i < j1; i += 32) {
+  each([&](int j, uint32_t k) {
     uint32_t s, t;
-    look(i, s, t);
+    look(j, k, s, t);
     sure += __popc(s);
     ties += __popc(t);
-  }
+  });
   if (lane == 0) {
     sm.sure[warp] = sure;
     sm.ties[warp] = ties;
@@ -254,24 +259,22 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Params p) {
     s_before += v.x;
     t_before += v.y;
   }
-  // Weights that are all in shared memory go to their places at once: no block reads its own from
-  // global memory any more.
-  const bool all_held = (int64_t)per_warp * kWarps <= p.held;
   const uint32_t below = (1u << lane) - 1;
-  for (int i = i0; i < i0 + per_warp && j0 + i < j1; i += 32) {
+  each([&](int j, uint32_t k) {
     uint32_t s, t;
-    look(i, s, t);
+    look(j, k, s, t);
     const int rank_t = t_before + __popc(t & below);
     if ((s >> lane & 1) || ((t >> lane & 1) && rank_t < left)) {
       const int to = s_before + __popc(s & below) + min(rank_t, left);
-      rows[to] = j0 + i + lane;
-      if (all_held) w[to] = held[i + lane];
+      rows[to] = j;
+      // Weights in registers go to their places at once: no block reads its own from memory any more.
+      if (R > 0) w[to] = weight_of(k);
     }
     s_before += __popc(s);
     t_before += __popc(t);
-  }
+  });
   cluster_barrier();   // the others have read this block's totals, and written their part of the list
-  if (!all_held) move_rows(w, rows, p.keep, p.one, (int)rank, (int)size, [] { cluster_barrier(); });
+  if (R == 0) move_rows(w, rows, p.keep, p.one, (int)rank, (int)size, [] { cluster_barrier(); });
   for (int64_t j = p.keep + (int64_t)rank * kThreads + tid; j < n; j += size * kThreads)
     w[j] = 0.f;
 }
@@ -302,8 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) move_kernel(const Params p) {
   }
 }
 
-int launch(void (*kernel)(const Params), int64_t clusters, int size, size_t smem, const Params& p,
-           cudaStream_t stream) {
+int launch(void (*kernel)(const Params), int64_t clusters, int size, const Params& p, cudaStream_t stream) {
   if (clusters * size > 0x7fffffff) return kErrShape;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -314,7 +316,6 @@ int launch(void (*kernel)(const Params), int64_t clusters, int size, size_t smem
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * size));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -340,13 +341,6 @@ Divisor pieces_of(int n) {
 }  // namespace
 
 int launch_cache_evict_q4(const EvictQ4Call& c) {
-  static DeviceOnce once;
-  int rc = once.run(c.device, [] {
-    return cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)(sizeof(Select) + kHeld * sizeof(float))) == cudaSuccess
-               ? kOk : kErrLaunch;
-  });
-  if (rc != kOk) return rc;
   Params p;
   p.part[0] = (uint8_t*)c.cache.k4; p.part[1] = (uint8_t*)c.cache.v4;
   p.part[2] = (uint8_t*)c.cache.k_scale; p.part[3] = (uint8_t*)c.cache.v_scale;
@@ -362,12 +356,14 @@ int launch_cache_evict_q4(const EvictQ4Call& c) {
   const int64_t heads = c.B * c.Hkv;
   if (4 * heads * kMaxCluster > 0x7fffffff) return kErrShape;
   p.heads = (int)heads;
-  const int sel = blocks_for(p.cap, 8192);
-  p.held = (int)std::min<int64_t>(kHeld, (p.cap + (int64_t)sel * kThreads - 1) / ((int64_t)sel * kThreads) * kThreads);
-  rc = launch(select_kernel, heads, sel, sizeof(Select) + p.held * sizeof(float), p, c.stream);
+  // Rows of a block by registers: 16 a lane, 32 where a cluster's eight blocks do not suffice, else none.
+  const int sel = blocks_for(p.cap, 16 * kThreads);
+  const int64_t per_lane = (p.cap + (int64_t)sel * kThreads - 1) / ((int64_t)sel * kThreads);
+  const int rc = launch(per_lane <= 16 ? select_kernel<16> : per_lane <= 32 ? select_kernel<32> : select_kernel<0>,
+                        heads, sel, p, c.stream);
   if (rc != kOk) return rc;
   const int mov = blocks_for(c.keep * p.code_bytes, (int64_t)kThreads * kPieces * 16);
-  return launch(move_kernel, 4 * heads, mov, 0, p, c.stream);
+  return launch(move_kernel, 4 * heads, mov, p, c.stream);
 }
 
 }  // namespace pfa

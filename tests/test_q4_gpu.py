@@ -364,6 +364,8 @@ EVICT = [  # lens, Hkv, D, cap, keep, recent
     ([2000], 1, 496, 2000, 1999, 7),
     ([40000, 20000], 2, 128, 40001, 16385, 3),
     ([300] * 50, 4, 128, 300, 100, 10),
+    ([70000, 99999, 3], 1, 16, 100001, 30000, 11),
+    ([140000, 150001], 1, 32, 150001, 70001, 5),
 ]
 
 
