@@ -5,11 +5,10 @@
 //
 // select_kernel, a cluster of up to eight blocks for each head, each with a run of its rows in registers:
 // the key of a weight is its bits, turned so that unsigned order is the order of
-// numbers.  Three passes over the candidates find the smallest key that is kept, 11, 11 and 10 bits at
+// numbers.  Up to four passes over the candidates find the smallest key that is kept, eight bits at
 // a time, from histograms that the blocks add up over distributed shared memory; then the kept rows
-// are listed in order, each warp counting the kept rows in front of its own.
-//
-// Weights move and become zero there too: every block has read its own by then.
+// are listed in order, each lane counting the kept rows in front of its own.  Weights move and become
+// zero there too: every block has read its own by then.
 //
 // move_kernel, a cluster for each head and array: kept rows move down in place.  A row never moves
 // up, so what a round writes (rows 0 .. below its end) is no source of a later one; in a
@@ -25,7 +24,8 @@ namespace pfa {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 4 * kThreads;
+constexpr int kBins = 256;
+constexpr int kLane = 16, kTile = kThreads * kLane;   // rows of a lane and of a block at a time
 constexpr int kPieces = 8;       // of a thread in a round
 constexpr int kMaxCluster = 8;
 
@@ -57,22 +57,26 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Words of block `rank`'s shared memory.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of block `rank`'s shared memory.
 __device__ __forceinline__ uint32_t remote_address(const void* p, uint32_t rank) {
   uint32_t a;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ int4 remote4(const int* p, uint32_t rank) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(remote_address(p, rank)));
+__device__ __forceinline__ int remote(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote_address(p, rank)));
   return v;
 }
-__device__ __forceinline__ int2 remote2(const int* p, uint32_t rank) {
-  int2 v;
-  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y) : "r"(remote_address(p, rank)));
+__device__ __forceinline__ int64_t remote(const int64_t* p, uint32_t rank) {
+  int64_t v;
+  asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(remote_address(p, rank)));
   return v;
 }
 
@@ -87,14 +91,26 @@ __device__ __forceinline__ float weight_of(uint32_t key) {   // (a NaN, but not 
   return __uint_as_float(key ^ (key >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
-__device__ __forceinline__ int warp_scan(int x) {   // inclusive
+template <typename T>
+__device__ __forceinline__ T warp_scan(T x) {   // inclusive
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, x, o);
+    const T v = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += v;
   }
   return x;
+}
+// Exclusive sum over the block's threads, and the total; sums is zero behind the block's warps.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sums, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t up = warp_scan(x);
+  __syncthreads();
+  if (lane == 31) sums[warp] = up;
+  __syncthreads();
+  const int64_t all = warp_scan(sums[lane]);
+  total = __shfl_sync(0xffffffffu, all, 31);
+  return __shfl_sync(0xffffffffu, all - sums[lane], warp) + up - x;
 }
 
 // Rows `rows` of width.by pieces move to 0 .. keep - 1, in place.  `rank` of `size` blocks; barrier(): theirs.
@@ -131,23 +147,23 @@ __device__ __forceinline__ void move_rows(T* base, const int32_t* rows, int keep
 }
 
 struct Select {
-  alignas(16) int hist[3][kBins];    // a pass each: other blocks may still read the last one
-  int sums[32];
-  int sure[32], ties[32];            // rows of a warp that stay for sure, and at the border
-  alignas(8) int total[2];           // and of the block
-  int digit, left;
+  int hist[4][kBins];                // a pass each: other blocks may still read the last one
+  int sums[32];                      // of the warps; zero behind the last
+  int64_t pairs[32], total;          // rows that stay for sure, and 2^32 times those at the border
+  int digit, count, left;
+  uint32_t keys[kWarps][32][kLane + 1];   // a lane's rows, one word apart from the next lane's
+  uint16_t kept[kWarps][32 * kLane];      // of a warp, in order
 };
 
-// R: rows of a lane that stay in registers, their keys; 0: none do, and weights are read in each pass.
-template <int R>
-__global__ void __launch_bounds__(kThreads, R == 32 ? 1 : 2) select_kernel(const Params p) {
-  __shared__ Select sm;
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const Params p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Select& sm = *reinterpret_cast<Select*>(smem_raw);
   asm volatile("griddepcontrol.launch_dependents;");
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const int bh = blockIdx.x / size, b = bh / p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
-  if (tid < 32) sm.sums[tid] = sm.sure[tid] = sm.ties[tid] = 0;
+  for (int i = tid; i < 4 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  if (tid < 32) sm.sums[tid] = 0, sm.pairs[tid] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t len = p.lengths[b];
   const bool bad = len < 0 || len > p.cap;
@@ -158,123 +174,139 @@ __global__ void __launch_bounds__(kThreads, R == 32 ? 1 : 2) select_kernel(const
     for (int64_t i = rank * kThreads + tid; i < p.keep; i += size * kThreads) rows[i] = i < n ? (int)i : -1;
     return;
   }
-  // The warp's rows [j0, j1), a whole number of them for each lane; row j0 + 32 i + lane is its i-th.
-  const int per_lane = (int)(((int64_t)n + size * kThreads - 1) / (size * kThreads));
-  const int64_t begin = ((int64_t)rank * kWarps + warp) * per_lane * 32;
-  const int j0 = (int)min(begin, (int64_t)n), j1 = (int)min(begin + per_lane * 32, (int64_t)n);
+  // The block's rows come in tiles; a lane has kLane consecutive rows of each, in registers.  With one
+  // tile, which is the rule, they are read once.
+  const int tiles = (int)(((int64_t)n + (int64_t)size * kTile - 1) / ((int64_t)size * kTile));
   const int m = n - p.recent;          // candidates; more of them than places
   float* const w = p.weights + (int64_t)bh * p.cap;
-  uint32_t held[R > 0 ? R : 1];
-  if constexpr (R > 0) {
+  uint32_t keys[kLane];
+  int64_t j0;                          // this lane's first row of the tile
+  auto load = [&](int tile) {
+    const int64_t first = ((int64_t)rank * tiles + tile) * kTile + warp * (32 * kLane);   // the warp's
+    j0 = first + lane * kLane;
+    float x[kLane];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int j = j0 + 32 * i + lane;
-      held[i] = j < j1 ? __float_as_uint(w[j]) : 0u;
-    }
+    for (int i = 0; i < kLane; ++i) x[i] = first + 32 * i + lane < n ? w[first + 32 * i + lane] : 0.f;
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < R; ++i) held[i] = key_of(__uint_as_float(held[i]));
-  }
-  __syncthreads();
-  // f(i, j, key) for each row of the warp's, whole warps at a time: j may be behind j1
-  auto each = [&](auto&& f) {
-    if constexpr (R > 0) {
+    for (int i = 0; i < kLane; ++i) sm.keys[warp][(32 * i + lane) / kLane][lane % kLane] = key_of(x[i]);
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (32 * i < j1 - j0) f(j0 + 32 * i + lane, held[i]);
-    } else {
-#pragma unroll 4
-      for (int j = j0 + lane; j - lane < j1; j += 32) f(j, j < j1 ? key_of(w[j]) : 0u);
-    }
+    for (int i = 0; i < kLane; ++i) keys[i] = sm.keys[warp][lane][i];
   };
+  auto lane_rows = [&](int end) { return (int)max((int64_t)0, min((int64_t)kLane, end - j0)); };
+  load(0);
+  __syncthreads();
 
   uint32_t key = 0;
+  bool inclusive = false;              // rows with a key above `key` stay, or not below it
   int left = p.keep - p.recent;        // of the candidates that agree with key so far
   if (left > 0) {
-    const int stop = min(j1, m);       // of the warp's candidates
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+#pragma unroll 1
+    for (int pass = 0; pass < 4 && !inclusive; ++pass) {
+      const int shift = 24 - 8 * pass;
       int* const hist = sm.hist[pass];
-      each([&](int j, uint32_t k) {
-        if (j < stop && (pass == 0 || (k ^ key) >> (shift + bits) == 0))
-          atomicAdd(&hist[k >> shift & ((1 << bits) - 1)], 1);
-      });
+#pragma unroll 1
+      for (int tile = 0; tile < tiles; ++tile) {
+        if (tiles > 1) load(tile);
+        const int here = lane_rows(m);
+        const uint32_t agree = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
+#pragma unroll
+        for (int i = 0; i < kLane; ++i)
+          if (i < here && ((keys[i] ^ key) & agree) == 0) atomicAdd(&hist[keys[i] >> shift & 255], 1);
+      }
       cluster_barrier();
-      // thread t has bins top - 3 .. top; larger digits are those of the threads below it
-      const int top = kBins - 1 - 4 * tid;
-      int4 v[kMaxCluster];
+      // thread t has bin 255 - t; larger digits are those of the threads below it
+      int v[kMaxCluster];
 #pragma unroll
       for (uint32_t r = 0; r < kMaxCluster; ++r)
-        v[r] = r < size ? remote4(&hist[top - 3], r) : make_int4(0, 0, 0, 0);
-      int c[4] = {0, 0, 0, 0};
+        v[r] = tid < kBins && r < size ? remote(&hist[kBins - 1 - tid], r) : 0;
+      int mine = 0;
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) c[0] += v[r].w, c[1] += v[r].z, c[2] += v[r].y, c[3] += v[r].x;
-      const int mine = c[0] + c[1] + c[2] + c[3], up = warp_scan(mine);
+      for (int r = 0; r < kMaxCluster; ++r) mine += v[r];
+      const int up = warp_scan(mine);
       if (lane == 31) sm.sums[warp] = up;
       __syncthreads();
       int above = warp_scan(sm.sums[lane]) - sm.sums[lane];
       above = __shfl_sync(0xffffffffu, above, warp) + up - mine;
       if (above < left && left <= above + mine) {   // one thread
-        int d = 0;
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-          if (d == i && left > above + c[i]) above += c[i], ++d;
-        sm.digit = top - d;
+        sm.digit = kBins - 1 - tid;
+        sm.count = mine;
         sm.left = left - above;
       }
       __syncthreads();
       key |= (uint32_t)sm.digit << shift;
       left = sm.left;
+      inclusive = sm.count == left;   // all that agree so far stay: the digits behind do not matter
     }
+    if (inclusive) left = 0;
   }
-  // Of the rows with that key the `left` lowest stay (with left 0: none), above it all.
-  const bool any = left > 0;
-  auto look = [&](int j, uint32_t k, uint32_t& sure, uint32_t& tie) {
-    sure = __ballot_sync(0xffffffffu, j < j1 && (j >= m || (any && k > key)));
-    tie = __ballot_sync(0xffffffffu, j < min(j1, m) && any && k == key);
-  };
-  int sure = 0, ties = 0;
-  each([&](int j, uint32_t k) {
-    uint32_t s, t;
-    look(j, k, s, t);
-    sure += __popc(s);
-    ties += __popc(t);
-  });
-  if (lane == 0) {
-    sm.sure[warp] = sure;
-    sm.ties[warp] = ties;
-  }
-  __syncthreads();
-  int s_before = warp_scan(sm.sure[lane]), t_before = warp_scan(sm.ties[lane]);
-  if (tid == 31) {
-    sm.total[0] = s_before;
-    sm.total[1] = t_before;
-  }
-  s_before = __shfl_sync(0xffffffffu, s_before - sm.sure[lane], warp);
-  t_before = __shfl_sync(0xffffffffu, t_before - sm.ties[lane], warp);
-  cluster_barrier();
+  const bool any = p.keep > p.recent;
+  // Of the rows with that key the `left` lowest stay, above it all.  Bits of this lane's rows:
+  auto look = [&](uint32_t& sure, uint32_t& tie) {
+    const uint32_t rows = (1u << lane_rows(n)) - 1, candidates = (1u << lane_rows(m)) - 1;
+    uint32_t least = 0, equal = 0;
 #pragma unroll
-  for (uint32_t r = 0; r < kMaxCluster; ++r) {
-    const int2 v = r < rank ? remote2(sm.total, r) : make_int2(0, 0);
-    s_before += v.x;
-    t_before += v.y;
-  }
-  const uint32_t below = (1u << lane) - 1;
-  each([&](int j, uint32_t k) {
-    uint32_t s, t;
-    look(j, k, s, t);
-    const int rank_t = t_before + __popc(t & below);
-    if ((s >> lane & 1) || ((t >> lane & 1) && rank_t < left)) {
-      const int to = s_before + __popc(s & below) + min(rank_t, left);
-      rows[to] = j;
-      // Weights in registers go to their places at once: no block reads its own from memory any more.
-      if (R > 0) w[to] = weight_of(k);
+    for (int i = 0; i < kLane; ++i) {
+      least |= keys[i] >= key ? 1u << i : 0u;
+      equal |= keys[i] == key ? 1u << i : 0u;
     }
-    s_before += __popc(s);
-    t_before += __popc(t);
-  });
-  cluster_barrier();   // the others have read this block's totals, and written their part of the list
-  if (R == 0) move_rows(w, rows, p.keep, p.one, (int)rank, (int)size, [] { cluster_barrier(); });
+    sure = (any ? candidates & (inclusive ? least : least & ~equal) : 0u) | (rows & ~candidates);
+    tie = any && !inclusive ? candidates & equal : 0u;
+  };
+  auto counts = [&](uint32_t sure, uint32_t tie) { return (int64_t)__popc(sure) | (int64_t)__popc(tie) << 32; };
+  uint32_t sure, tie;
+  int64_t mine = 0, total;
+#pragma unroll 1
+  for (int tile = 0; tile < tiles; ++tile) {
+    if (tiles > 1) load(tile);
+    look(sure, tie);
+    mine += counts(sure, tie);
+  }
+  int64_t before = block_scan(mine, sm.pairs, total);
+  if (tid == 0) sm.total = total;
+  cluster_barrier();
+  int64_t base = 0;
+#pragma unroll
+  for (uint32_t r = 0; r < kMaxCluster; ++r)
+    if (r < rank) base += remote(&sm.total, r);
+  cluster_arrive();   // this block has read the others' totals
+#pragma unroll 1
+  for (int tile = 0; tile < tiles; ++tile) {
+    if (tiles > 1) {
+      load(tile);
+      look(sure, tie);
+      before = block_scan(counts(sure, tie), sm.pairs, total);
+    }
+    const int ties = (int)((base + before) >> 32);
+    int at = (int)(base + before) + min(ties, left);
+#pragma unroll 1
+    while (ties + __popc(tie) > left && tie != 0) tie &= ~(0x80000000u >> __clz(tie));
+    const uint32_t kept = sure | tie;
+    // through shared memory, so that a warp writes its part of the list in one piece
+    const int warp_at = __shfl_sync(0xffffffffu, at, 0);
+    int to = at - warp_at;
+#pragma unroll
+    for (int i = 0; i < kLane; ++i)
+      if (kept >> i & 1) sm.kept[warp][to++] = (uint16_t)(lane * kLane + i);
+    const int count = __shfl_sync(0xffffffffu, to, 31);
+    const int first = (int)__shfl_sync(0xffffffffu, j0, 0);
+    __syncwarp();
+#pragma unroll 4
+    for (int t = lane; t < count; t += 32) {
+      const int i = sm.kept[warp][t];
+      rows[warp_at + t] = first + i;
+      // No block reads weights from memory any more, where there is one tile: they move at once.
+      if (tiles == 1) w[warp_at + t] = weight_of(sm.keys[warp][i / kLane][i % kLane]);
+    }
+    __syncwarp();
+    base += total;
+  }
+  cluster_wait();
+  if (tiles > 1) {
+    cluster_barrier();   // the list is whole
+    move_rows(w, rows, p.keep, p.one, (int)rank, (int)size, [] { cluster_barrier(); });
+  }
   for (int64_t j = p.keep + (int64_t)rank * kThreads + tid; j < n; j += size * kThreads)
     w[j] = 0.f;
 }
@@ -305,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, 2) move_kernel(const Params p) {
   }
 }
 
-int launch(void (*kernel)(const Params), int64_t clusters, int size, const Params& p, cudaStream_t stream) {
+int launch(void (*kernel)(const Params), int64_t clusters, int size, size_t smem, const Params& p,
+           cudaStream_t stream) {
   if (clusters * size > 0x7fffffff) return kErrShape;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -316,6 +349,7 @@ int launch(void (*kernel)(const Params), int64_t clusters, int size, const Param
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * size));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -341,6 +375,12 @@ Divisor pieces_of(int n) {
 }  // namespace
 
 int launch_cache_evict_q4(const EvictQ4Call& c) {
+  static DeviceOnce once;
+  int rc = once.run(c.device, [] {
+    return cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(Select)) == cudaSuccess ? kOk : kErrLaunch;
+  });
+  if (rc != kOk) return rc;
   Params p;
   p.part[0] = (uint8_t*)c.cache.k4; p.part[1] = (uint8_t*)c.cache.v4;
   p.part[2] = (uint8_t*)c.cache.k_scale; p.part[3] = (uint8_t*)c.cache.v_scale;
@@ -356,14 +396,10 @@ int launch_cache_evict_q4(const EvictQ4Call& c) {
   const int64_t heads = c.B * c.Hkv;
   if (4 * heads * kMaxCluster > 0x7fffffff) return kErrShape;
   p.heads = (int)heads;
-  // Rows of a block by registers: 16 a lane, 32 where a cluster's eight blocks do not suffice, else none.
-  const int sel = blocks_for(p.cap, 16 * kThreads);
-  const int64_t per_lane = (p.cap + (int64_t)sel * kThreads - 1) / ((int64_t)sel * kThreads);
-  const int rc = launch(per_lane <= 16 ? select_kernel<16> : per_lane <= 32 ? select_kernel<32> : select_kernel<0>,
-                        heads, sel, p, c.stream);
+  rc = launch(select_kernel, heads, blocks_for(p.cap, kTile), sizeof(Select), p, c.stream);
   if (rc != kOk) return rc;
   const int mov = blocks_for(c.keep * p.code_bytes, (int64_t)kThreads * kPieces * 16);
-  return launch(move_kernel, 4 * heads, mov, p, c.stream);
+  return launch(move_kernel, 4 * heads, mov, 0, p, c.stream);
 }
 
 }  // namespace pfa

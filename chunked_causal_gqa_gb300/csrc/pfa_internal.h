@@ -284,6 +284,7 @@ struct EvictQ4Call {
   int64_t* lengths_out;
   int32_t* rows_out;
   unsigned* err;
+  int device;
   cudaStream_t stream;
 };
 int launch_cache_evict_q4(const EvictQ4Call& c);
