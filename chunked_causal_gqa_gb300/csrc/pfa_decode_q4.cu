@@ -46,23 +46,22 @@
 namespace pfa {
 namespace {
 
-constexpr int kUnit = 64, kTiles = kUnit / 16;   // keys of a unit; products that hold them
-constexpr int kStages = 2;
-constexpr int kHalf = kUnit * 64;              // bytes of a warp's K (or V) codes of a stage
-constexpr int kScales = kUnit * 8;             // and of its scales
-constexpr int kStageBytes = 2 * (kHalf + kScales);
-// Joins: 8 row sums of 128 floats for each warp.  Score exchange: twice those of a unit and 16 rows.
-constexpr int kJoinBytes = 2 * kWarps * kUnit * 16 * 4;
+constexpr int kBlocksPerSm = 2;
 constexpr float kLag = 4.f, kUp = 11.f;        // powers of two: of a score above the base; of weights
 
-struct Params : ListParams {
-  static constexpr int kUnit = pfa::kUnit, kHeadCost = 8;
-  static constexpr bool kSums = true;
-  const uint8_t *k4, *v4, *k_scale, *v_scale;
+struct Scores : ListParams {
   float* scores;       // null, or [head][keys of whole units][row_pad]
   float* weights;      // [head][cap]
   int64_t score_head;  // floats of a head
   int row_pad;
+};
+
+// UNIT: keys of a unit, in products of 16.  A ring holds 128 keys a warp.
+template <int UNIT>
+struct Params : Scores {
+  static constexpr int kUnit = UNIT, kHeadCost = 512 / UNIT;
+  static constexpr bool kSums = true;
+  const uint8_t *k4, *v4, *k_scale, *v_scale;
 };
 
 // Key of row i of a product, in its eight.
@@ -101,28 +100,36 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   return b;
 }
 
+template <int UNIT>
 struct Shared {
+  static constexpr int kStages = 128 / UNIT;
+  static constexpr int kHalf = UNIT * 64;        // bytes of a warp's K (or V) codes of a stage
+  static constexpr int kScales = UNIT * 8;       // and of its scales
+  static constexpr int kStageBytes = 2 * (kHalf + kScales);
+  // Joins: 8 row sums of 128 floats for each warp.  Score exchange: twice those of a unit and 16 rows.
+  static constexpr int kJoinBytes = kWarps * UNIT * 128;
   alignas(128) uint8_t ring[kWarps][kStages][kStageBytes];
-  alignas(16) uint8_t join[kJoinBytes];   // also: score exchange
-  float2 ml[kWarps][16];                  // a warp's {m, l} of each row
+  alignas(16) uint8_t join[kJoinBytes];
+  float2 ml[kWarps][16];                         // a warp's {m, l} of each row
   ListShared list;
+  static_assert(kJoinBytes >= kWarps * 8 * 128 * 4, "join area");
 };
-
-constexpr int kBlocksPerSm = 2;
-static_assert(kBlocksPerSm * (sizeof(Shared) + 1024) <= 228 * 1024, "shared memory of an SM");
+static_assert(kBlocksPerSm * (sizeof(Shared<64>) + 1024) <= 228 * 1024, "shared memory of an SM");
 
 // NW: warps of a unit (head_dim / 128).  NT: products a tile, tiles of 8 NT rows.
-template <typename E, int NW, int NT>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Params p) {
+template <typename E, int NW, int NT, int UNIT>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Params<UNIT> p) {
   // A team is a warp or the block, so that every barrier is the block's: it does not count
   // warps that have ended, and no lengths, not even changing ones, leave a warp waiting.
   static_assert(NW == 1 || NW == kWarps, "barriers are the block's");
   constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = 8 * NT;
   constexpr bool F32 = sizeof(E) == 4;
   constexpr int SETS = F32 ? 2 : 1;   // high and low halves
-  static_assert(kJoinBytes >= kWarps * 8 * 128 * 4 && kJoinBytes >= 2 * NW * kTiles * NT * 32 * 16, "join area");
+  constexpr int kUnit = UNIT, kTiles = UNIT / 16, kStages = Shared<UNIT>::kStages;
+  constexpr int kHalf = Shared<UNIT>::kHalf, kScales = Shared<UNIT>::kScales, kStageBytes = Shared<UNIT>::kStageBytes;
+  static_assert(NW == 1 || Shared<UNIT>::kJoinBytes >= 2 * NW * kTiles * NT * 32 * 16, "score exchange");
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
+  Shared<UNIT>& sm = *reinterpret_cast<Shared<UNIT>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, qd = lane & 3;
   const int team = warp / NW, part = warp % NW;
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   int at, stop, first_entry, into;
   if (!run_start<RM, TEAMS>(p, sm.list, at, stop, first_entry, into)) return;
 
-  Cursor<Params, RM, TEAMS> in, cu;   // copies, products
+  Cursor<Params<UNIT>, RM, TEAMS> in, cu;   // copies, products
   in.start(p, at, stop, first_entry, into, team);
   cu = in;
 
@@ -635,7 +642,7 @@ constexpr int kWeightThreads = 256, kMaxRows = PFA_DECODE_MAX_ROWS;
 constexpr int kWeightKeys = 4, kWeightRounds = 2;   // keys of a thread in flight, rounds of them
 
 template <int G>
-__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const Params p, const Divisor chunks) {
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const Scores p, const Divisor chunks) {
   constexpr int kStep = kWeightThreads / G, kBlock = kStep * kWeightKeys * kWeightRounds;   // keys
   __shared__ float4 s_m[kMaxRows / 4], s_inv[kMaxRows / 4];   // of each row, 0 and 0 behind the last
   __shared__ int4 s_pos[kMaxRows / 4];
@@ -700,7 +707,7 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const Params p,
 }
 
 template <int G>
-int launch_weights(Params p, int64_t heads, cudaStream_t stream) {
+int launch_weights(Scores p, int64_t heads, cudaStream_t stream) {
   constexpr int kBlock = kWeightThreads / G * kWeightKeys * kWeightRounds;
   const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
   const int64_t chunks = std::min<int64_t>((keys + kBlock - 1) / kBlock, 0x7fffffff / heads);
@@ -714,23 +721,27 @@ int launch_weights(Params p, int64_t heads, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, weights_kernel<G>, (const Params)p, divisor((uint32_t)chunks)) == cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, weights_kernel<G>, p, divisor((uint32_t)chunks)) == cudaSuccess)
     return kOk;
   cudaGetLastError();
   return kErrLaunch;
 }
 
-template <typename E, int NW, int NT>
-int launch(const Params& p, const DecodeQ4Call& c) {
+template <typename E, int NW, int NT, int UNIT>
+int launch(const Params<64>& all, const DecodeQ4Call& c) {
+  using P = Params<UNIT>;
+  P p;
+  static_cast<Scores&>(p) = all;
+  p.k4 = all.k4; p.v4 = all.v4; p.k_scale = all.k_scale; p.v_scale = all.v_scale;
   static DeviceOnce once;
   const int rc = once.run(c.device, [] {
-    return cudaFuncSetAttribute(decode_kernel<E, NW, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(Shared)) == cudaSuccess ? kOk : kErrLaunch;
+    return cudaFuncSetAttribute(decode_kernel<E, NW, NT, UNIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(Shared<UNIT>)) == cudaSuccess ? kOk : kErrLaunch;
   });
   if (rc != kOk) return rc;
-  const Kernels<Params> k = {decode_kernel<E, NW, NT>, join_kernel<Params, E, NW, 8 * NT, 8>,
-                             join_kernel<Params, E, NW, 8 * NT, 1>, 8 * NT, NW, kBlocksPerSm,
-                             sizeof(Shared)};
+  const Kernels<P> k = {decode_kernel<E, NW, NT, UNIT>, join_kernel<P, E, NW, 8 * NT, 8>,
+                        join_kernel<P, E, NW, 8 * NT, 1>, 8 * NT, NW, kBlocksPerSm,
+                        sizeof(Shared<UNIT>)};
   return launch_list(k, p, c.span.B, c.num_sms, c.stream);
 }
 
@@ -748,7 +759,7 @@ Layout layout(int64_t heads, int rows, int D, int dtype, int64_t cap, bool weigh
   w.scores = w.total = w.sums;
   if (!weights) return w;
   w.row_pad = (rows + 3) & ~3;
-  w.score_head = (cap + kUnit - 1) / kUnit * kUnit * w.row_pad;
+  w.score_head = (cap + 63) / 64 * 64 * w.row_pad;
   w.scores += ((size_t)heads * rows * sizeof(float2) + 255) & ~(size_t)255;
   w.total = w.scores + (((size_t)heads * w.score_head * sizeof(float) + 255) & ~(size_t)255);
   return w;
@@ -762,7 +773,7 @@ size_t decode_q4_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtyp
 }
 
 int launch_decode_q4(const DecodeQ4Call& c) {
-  Params p;
+  Params<64> p;
   p.q = c.q; p.out = c.out;
   p.k4 = (const uint8_t*)c.cache.k4; p.v4 = (const uint8_t*)c.cache.v4;
   p.k_scale = (const uint8_t*)c.cache.k_scale; p.v_scale = (const uint8_t*)c.cache.v_scale;
@@ -786,22 +797,30 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   p.score_head = w.score_head;
   p.row_pad = w.row_pad;
   p.weights = c.weights;
-  const bool few = p.rows <= 8;
+  // With tiles of 16 rows a converted code serves two products; with 8 there are twice as many units
+  // to spread, and less code to fetch.  16 rows, bf16 (us, tiles of 8 / of 16):
+  //   one sequence, 32/8 heads of 128, 512 / 4096 / 16384 keys     7.0 / 8.5   8.3 / 10.1   13.2 / 13.2
+  //   16 sequences of 512 / 2048 keys                              11.2 / 12.7   19.9 / 19.6
+  //   one sequence of 131072 keys                                  51.0 / 43.4
+  //   8/2 heads of 512, 16 sequences of 2048, 4 of 32768 keys      26.3 / 31.6   65.9 / 53.7
+  // fp32: 9.5 / 11.9 at 4096 keys, 23.2 / 23.8 at 32768, 8 sequences of 8192 keys 43.8 / 38.9.
+  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
+  const int64_t units = heads * ((p.rows + 7) / 8) * (keys / 64 + 1);
+  const bool few = p.rows <= 8 || units < (int64_t)12 * c.num_sms * kBlocksPerSm;
   int rc;
   if (c.dtype == PFA_BF16)
-    rc = c.D == 128 ? (few ? launch<__nv_bfloat16, 1, 1>(p, c) : launch<__nv_bfloat16, 1, 2>(p, c))
-                    : (few ? launch<__nv_bfloat16, 4, 1>(p, c) : launch<__nv_bfloat16, 4, 2>(p, c));
-  else
-    rc = c.D == 128 ? (few ? launch<float, 1, 1>(p, c) : launch<float, 1, 2>(p, c))
-                    : (few ? launch<float, 4, 1>(p, c) : launch<float, 4, 2>(p, c));
+    rc = c.D == 128 ? (few ? launch<__nv_bfloat16, 1, 1, 64>(p, c) : launch<__nv_bfloat16, 1, 2, 64>(p, c))
+                    : (few ? launch<__nv_bfloat16, 4, 1, 64>(p, c) : launch<__nv_bfloat16, 4, 2, 64>(p, c));
+  else   // (16 fp32 rows and units of 64 keys need more registers than there are: 16.7 us for 14.9)
+    rc = c.D == 128 ? (few ? launch<float, 1, 1, 64>(p, c) : launch<float, 1, 2, 32>(p, c))
+                    : (few ? launch<float, 4, 1, 64>(p, c) : launch<float, 4, 2, 32>(p, c));
   if (rc != kOk || !c.weights) return rc;
-  // as many lanes to a key as it has four rows
+  // Lanes to a key: as many as it has four rows, or four or eight that take turns.
   const int quads = p.row_pad / 4;
-  return quads <= 1   ? launch_weights<1>(p, heads, c.stream)
-         : quads <= 2 ? launch_weights<2>(p, heads, c.stream)
-         : quads <= 4 ? launch_weights<4>(p, heads, c.stream)
-         : quads <= 8 ? launch_weights<8>(p, heads, c.stream)
-                      : launch_weights<32>(p, heads, c.stream);
+  return quads <= 1                      ? launch_weights<1>(p, heads, c.stream)
+         : quads <= 3                    ? launch_weights<2>(p, heads, c.stream)
+         : quads % 8 == 0 || quads >= 24 ? launch_weights<8>(p, heads, c.stream)
+                                         : launch_weights<4>(p, heads, c.stream);
 }
 
 }  // namespace pfa
