@@ -2,11 +2,15 @@
 //
 // Write: for each 16 channels of a new row, with y = x * 2^-exponent,
 //   scale = e4m3(max |y| / 6),  code = e2m1(y / scale)
-// and both roundings are those of the exact quotients.  Division rounds to the nearest
-// float, so it could only move a quotient onto a border between two codes (or two scales).
-// The borders t have at most five significant bits and the divisors s at most four, so s t
-// is a float, and a y that differs from it does so by an ulp(y) at least; s being under
-// 1.875 * 2^e, the quotient is then 1 / 1.875 > 1/2 ulp or more away from t.
+// and both roundings are those of the exact quotients, though these are rounded to a float in
+// between: that could only move a quotient onto a border t between two codes (or scales).  The
+// borders have at most five significant bits and the divisors s at most four, so s t is a
+// float, and a y that differs from it does so by an ulp(y) at least; s being at most 1.875 * 2^e, the
+// quotient is then 0.533 ulp(t) or more away from t, and the nearest float to it another one.
+// y / s is y * (1 / s) with one correction by its residual y - q s, which is exact in a fused
+// multiply-add: off by 2^-22 of a last place before its rounding, so exact where the quotient is a float
+// (a border among them) and on the right side of every border elsewhere.
+//
 #include "pfa_internal.h"
 #include "pfa_ptx.cuh"
 #include "pfa_q4.cuh"
@@ -83,8 +87,12 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const WriteParams p) {
   const float f = e4m3_to_float(s);
   uint2 w = make_uint2(0u, 0u);
   if (finite && f > 0.f) {
+    const float r = __frcp_rn(f), most = 8.f * f;   // (beyond 8 the largest code, and no infinite product)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], f);
+    for (int i = 0; i < 16; ++i) {
+      const float y = fminf(fmaxf(x[i], -most), most), q = y * r;
+      x[i] = copysignf(fmaf(fmaf(-q, f, y), r, q), y);   // (-0 stays -0)
+    }
     w = make_uint2(float_to_e2m1x8(x), float_to_e2m1x8(x + 8));
   }
   reinterpret_cast<uint2*>(isv ? p.v4 : p.k4)[at] = w;

@@ -122,6 +122,29 @@ def test_write_one_sequence_at_the_edges(dt, e):
     ok()
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_write_beside_every_border(dt):
+    """For every scale the floats on and beside each border between two codes, of both signs, and a wide mixture."""
+    s = torch.arange(1, 127, dtype=torch.uint8).view(F8).double()
+    t = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64)
+    near = [(s[:, None] * t).float()]
+    up = down = near[0]
+    for _ in range(4):
+        up, down = torch.nextafter(up, torch.tensor(1e30)), torch.nextafter(down, torch.tensor(0.0))
+        near += [up, down]
+    v = torch.nn.functional.pad(torch.stack(near, -1).reshape(126, -1), (0, 12)).reshape(126, 5, 15)
+    v = torch.cat((v, 6 * s.float()[:, None, None].expand(126, 5, 1)), -1).reshape(-1, 16)
+    g = torch.Generator().manual_seed(1)
+    mix = torch.randn(40000, 16, generator=g) * (3 * torch.randn(40000, 1, generator=g)).exp()
+    x = torch.cat((v, -v, mix)).to(dt).to(G.dev())
+    x = x[:x.shape[0] // 8 * 8].reshape(-1, 1, 128)
+    cache = pkg.q4_cache(1, x.shape[0], 128)
+    pkg.cache_write_q4(x, x, cache, start_pos=0)
+    codes, scale = R.quantise(x, 0)
+    assert torch.equal(cache.k_scale.view(torch.uint8)[0], scale[:, 0]) and torch.equal(cache.k[0], codes[:, 0])
+    ok()
+
+
 def test_write_refuses_lengths_beyond_the_cache_on_the_device():
     cache = pkg.Q4Cache(*R.make_cache(2, 64, 128, batch=3, seed=1, device=G.dev()))
     before = raw(cache)
