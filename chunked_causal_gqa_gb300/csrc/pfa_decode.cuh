@@ -23,7 +23,8 @@ constexpr int64_t kMaxUnits = 1 << 30;         // units that a launch can list
 
 // What the list and the join need of a launch.  A kernel's own parameters derive from it and
 // say P::kUnit, P::kHeadCost, what the start and end of a head cost a block, in units (its query rows, the
-// join), and P::kSums, whether row sums can be asked for.
+// join), and P::kSums, whether row sums can be asked for (then also more_blocks() and, with
+// MORE, more(): blocks behind those of the join for other work that waits for the first kernel).
 struct ListParams {
   const void* q;
   void* out;
@@ -35,6 +36,7 @@ struct ListParams {
   int rows, entries;          // T * group; entries of this launch
   Divisor group, seqs;        // H / Hkv; sequences in this launch
   Divisor heads, joined;      // Hkv, and the second kernel's blocks for a tile's rows
+  int joins;                  // the second kernel's blocks that join
   float scale_log2, unit;     // of the scores, in powers of two; of the output
   unsigned* err;
   float* parts;               // workspace: slots of partial sums
@@ -258,25 +260,19 @@ __device__ __forceinline__ bool run_start(const P& p, ListShared& sh, int& at, i
   return true;
 }
 
-// A block has 128 columns of one row (GROUPS warps that take the parts in turn, in the
-// blocks' order, each with a running maximum) or, with GROUPS 1, of all rows of a
-// tile, a warp each.  It joins the parts of its head, and writes the zeros of rows
-// that see nothing.
-template <typename P, typename E, int NW, int RM, int GROUPS>
-__global__ void __launch_bounds__(512) join_kernel(const P p, int blocks) {
-  constexpr int D = NW * 128, TEAMS = kWarps / NW;
-  __shared__ float4 s_sum[GROUPS > 1 ? GROUPS - 1 : 1][32];
-  __shared__ float2 s_ml[GROUPS];
-  __shared__ int s_units[16][2];
+// The parts of a head: blocks c0 .. c0 + n - 1 have one each, the first of them in its slot `first`.  None
+// (n 0): nothing is seen.  One: the block has stored the output.
+struct Parts {
+  int c0, n, first;
+};
+
+// The list of units, as the first kernel counts it, while that one runs.  Its blocks let this
+// grid start behind their own wait: whatever wrote the lengths has ended, and its writes are in
+// L2.  (The first kernel's own results are read behind a wait of the caller's.)
+template <int RM, int TEAMS, typename P>
+__device__ __forceinline__ Parts parts_of(const P& p, int e, int h, const Entry<P::kHeadCost>& x,
+                                          int blocks, int (*s_units)[2]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int grp = warp % GROUPS;
-  const int id = blockIdx.x / NW, d = blockIdx.x % NW * 128 + lane * 4;
-  const int eh = id / p.joined, r = id - eh * (int)p.joined.by + warp / GROUPS;
-  const int e = eh / p.heads, h = eh - e * p.Hkv;
-  asm volatile("griddepcontrol.launch_dependents;");
-  // The list of units, as the first kernel counts it, while that one runs.  Its blocks let this
-  // grid start behind their own wait: whatever wrote the lengths has ended, and its writes are in
-  // L2.  (The first kernel's own results are read behind the wait below.)
   int before = 0, total = 0;
 #pragma unroll 1
   for (int i = tid; i < p.entries; i += blockDim.x) {
@@ -298,16 +294,48 @@ __global__ void __launch_bounds__(512) join_kernel(const P p, int blocks) {
     before += s_units[w][0];
     total += s_units[w][1];
   }
-  const auto x = entry_of<RM, true>(p, e);
   const int run = run_of<TEAMS>(total, blocks);
   const int s0 = before + h * x.listed();
-  int c0 = 0, n = 0, first = 0;
+  Parts y = {};
   if (x.n > 0) {
-    c0 = (int)((uint32_t)(s0 + P::kHeadCost) / (uint32_t)run);
-    n = (int)((uint32_t)(s0 + x.listed() - 1) / (uint32_t)run) - c0 + 1;
+    y.c0 = (int)((uint32_t)(s0 + P::kHeadCost) / (uint32_t)run);
+    y.n = (int)((uint32_t)(s0 + x.listed() - 1) / (uint32_t)run) - y.c0 + 1;
     // the first block's part is its run's last piece unless its run starts in this head
-    first = c0 * run >= s0 ? 0 : 1;
+    y.first = y.c0 * run >= s0 ? 0 : 1;
   }
+  return y;
+}
+
+// Where part i of a head is.
+template <int RM, int D, typename P>
+__device__ __forceinline__ const float* part_at(const P& p, const Parts& y, int i) {
+  return p.parts + (int64_t)(2 * (y.c0 + i) + (i == 0 ? y.first : 0)) * slot_floats<RM, D>();
+}
+
+// A block has 128 columns of one row (GROUPS warps that take the parts in turn, in the
+// blocks' order, each with a running maximum) or, with GROUPS 1, of all rows of a
+// tile, a warp each.  It joins the parts of its head, and writes the zeros of rows
+// that see nothing.
+template <typename P, typename E, int NW, int RM, int GROUPS, bool MORE = false>
+__global__ void __launch_bounds__(512) join_kernel(const P p, int blocks) {
+  constexpr int D = NW * 128, TEAMS = kWarps / NW;
+  __shared__ float4 s_sum[GROUPS > 1 ? GROUPS - 1 : 1][32];
+  __shared__ float2 s_ml[GROUPS];
+  __shared__ int s_units[16][2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int grp = warp % GROUPS;
+  if constexpr (MORE)
+    if ((int)blockIdx.x >= p.joins) {
+      p.template more<RM, NW>((int)blockIdx.x - p.joins, blocks, s_units);
+      return;
+    }
+  const int id = blockIdx.x / NW, d = blockIdx.x % NW * 128 + lane * 4;
+  const int eh = id / p.joined, r = id - eh * (int)p.joined.by + warp / GROUPS;
+  const int e = eh / p.heads, h = eh - e * p.Hkv;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const auto x = entry_of<RM, true>(p, e);
+  const Parts head = parts_of<RM, TEAMS>(p, e, h, x, blocks, s_units);
+  const int n = head.n;
   // Every block waits, also one with nothing to do: this grid must not end before the first.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (r >= x.nr || x.bad || n == 1) return;   // n 1: stored whole
@@ -330,8 +358,7 @@ __global__ void __launch_bounds__(512) join_kernel(const P p, int blocks) {
       ml[j] = make_float2(-INFINITY, 0.f);
       v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
-        const float* slot =
-            p.parts + (int64_t)(2 * (c0 + i) + (i == 0 ? first : 0)) * slot_floats<RM, D>();
+        const float* slot = part_at<RM, D>(p, head, i);
         ml[j] = *reinterpret_cast<const float2*>(slot + RM * D + 2 * r);
         v[j] = *reinterpret_cast<const float4*>(slot + r * D + d);
       }
@@ -430,14 +457,21 @@ int launch_list(const Kernels<P>& k, P p, int64_t B, int num_sms, cudaStream_t s
       const bool many = (int64_t)p.entries * p.Hkv * 8 <= blocks;
       p.joined = divisor(many ? rows : 1);
       const int64_t joins = (int64_t)p.entries * p.Hkv * p.joined.by * k.nw;
-      if (joins > 0x7fffffff) return kErrShape;
+      int threads = many ? 256 : rows * 32;
+      int64_t more = 0;
+      if constexpr (P::kSums) {
+        threads = std::max(threads, p.more_threads());
+        more = p.more_blocks(threads);
+      }
+      if (joins + more > 0x7fffffff) return kErrShape;
+      p.joins = (int)joins;
       cfg.gridDim = dim3((unsigned)blocks);
       cfg.blockDim = dim3(kThreads);
       cfg.dynamicSmemBytes = k.smem;
       cudaError_t err = cudaLaunchKernelEx(&cfg, k.decode, p);
       if (err == cudaSuccess) {
-        cfg.gridDim = dim3((unsigned)joins);
-        cfg.blockDim = dim3(many ? 256 : rows * 32);
+        cfg.gridDim = dim3((unsigned)(joins + more));
+        cfg.blockDim = dim3((unsigned)threads);
         cfg.dynamicSmemBytes = 0;
         err = cudaLaunchKernelEx(&cfg, many ? k.join_many : k.join_few, p, blocks);
       }

@@ -49,12 +49,83 @@ namespace {
 constexpr int kBlocksPerSm = 2;
 constexpr float kLag = 4.f, kUp = 11.f;        // powers of two: of a score above the base; of weights
 
+struct Scores;
+Divisor chunks_of(const Scores& p, int threads);
+
+// What the accumulated weights need.
 struct Scores : ListParams {
   float* scores;       // null, or [head][keys of whole units][row_pad]
   float* weights;      // [head][cap]
   int64_t score_head;  // floats of a head
-  int row_pad;
+  int row_pad, lanes;  // a multiple of 4; lanes to a key
+  Divisor chunks;      // of a head's keys, blocks
+  bool fused;          // weights are added beside the join
 };
+
+constexpr int kWeightThreads = 256, kMaxRows = PFA_DECODE_MAX_ROWS;
+constexpr int kWeightKeys = 4, kWeightRounds = 2;   // keys of a thread in flight, rounds of them
+
+// Largest score, 1 / sum and position of four rows each; rows behind the last see nothing.
+struct RowSums {
+  float4 m, inv;
+  int4 pos;
+};
+
+// LANES lanes (0: p.lanes) take a key's rows four at a time and add up their weights: this block's keys of
+// a head, chunk `chunk`, between rows lo and end.
+template <int LANES>
+__device__ __forceinline__ void add_weights(const Scores& p, int64_t bh, int chunk, int lo, int end,
+                                            const RowSums* rows) {
+  const int lanes = LANES > 0 ? LANES : p.lanes, sub = threadIdx.x & (lanes - 1), quads = p.row_pad / 4;
+  const int step = blockDim.x / lanes, block = step * kWeightKeys * kWeightRounds;   // keys
+  const float* const scores = p.scores + bh * p.score_head;
+  float* const weights = p.weights + bh * p.cap;
+#pragma unroll 1
+  for (int64_t at = lo + (int64_t)chunk * block; at < end; at += (int64_t)p.chunks.by * block)
+#pragma unroll 1
+    for (int round = 0; round < kWeightRounds; ++round) {
+      const int64_t j0 = at + round * (step * kWeightKeys) + threadIdx.x / lanes;
+      float sum[kWeightKeys], was[kWeightKeys];
+#pragma unroll
+      for (int i = 0; i < kWeightKeys; ++i) {
+        sum[i] = was[i] = 0.f;
+        if (sub == 0 && j0 + i * step < end) was[i] = weights[j0 + i * step];
+      }
+#pragma unroll 1
+      for (int q = sub; q < quads; q += lanes) {
+        float4 v[kWeightKeys];
+#pragma unroll
+        for (int i = 0; i < kWeightKeys; ++i)
+          if (j0 + i * step < end)
+            v[i] = *reinterpret_cast<const float4*>(scores + (j0 + i * step) * p.row_pad + 4 * q);
+        const RowSums r = rows[q];
+#pragma unroll
+        for (int i = 0; i < kWeightKeys; ++i) {
+          const int64_t j = j0 + i * step;
+          // (what a row does not see may not have been written)
+          auto add = [&](float s, float m, float inv, int pos) {
+            if (j <= pos && (p.window <= 0 || j > pos - p.window)) sum[i] += exp2_fast(s - m) * inv;
+          };
+          add(v[i].x, r.m.x, r.inv.x, r.pos.x);
+          add(v[i].y, r.m.y, r.inv.y, r.pos.y);
+          add(v[i].z, r.m.z, r.inv.z, r.pos.z);
+          add(v[i].w, r.m.w, r.inv.w, r.pos.w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kWeightKeys; ++i) {
+#pragma unroll
+        for (int d = 1; d < lanes; d <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+        if (sub == 0 && j0 + i * step < end) weights[j0 + i * step] = was[i] + sum[i];
+      }
+    }
+}
+
+__device__ __forceinline__ void set_row(RowSums* rows, int r, float2 ml, int pos) {
+  reinterpret_cast<float*>(&rows[r / 4].m)[r % 4] = ml.x;
+  reinterpret_cast<float*>(&rows[r / 4].inv)[r % 4] = ml.y;
+  reinterpret_cast<int*>(&rows[r / 4].pos)[r % 4] = pos;
+}
 
 // UNIT: keys of a unit, in products of 16.  A ring holds 128 keys a warp.
 template <int UNIT>
@@ -62,6 +133,48 @@ struct Params : Scores {
   static constexpr int kUnit = UNIT, kHeadCost = 512 / UNIT;
   static constexpr bool kSums = true;
   const uint8_t *k4, *v4, *k_scale, *v_scale;
+
+  int more_threads() const { return fused ? kWeightThreads : 0; }
+  int64_t more_blocks(int threads) {
+    if (!fused) return 0;
+    chunks = chunks_of(*this, threads);
+    return (int64_t)entries * Hkv * chunks.by;
+  }
+  // Weights beside the join, where a head's rows are one tile: their sums from the parts once more.
+  template <int RM, int NW>
+  __device__ __forceinline__ void more(int id, int blocks, int (*s_units)[2]) const {
+    __shared__ RowSums s_rows[RM / 4];
+    const int eh = id / chunks, chunk = id - eh * (int)chunks.by, e = eh / heads, h = eh - e * Hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const auto x = entry_of<RM, true>(*this, e);
+    const Parts head = parts_of<RM, kWarps / NW>(*this, e, h, x, blocks, s_units);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t bh = x.b * Hkv + h;
+    if (head.n == 0 || x.lo + (int64_t)chunk * (blockDim.x / lanes * (kWeightKeys * kWeightRounds)) >= x.end) return;
+    for (int r = warp; r < RM; r += warps) {
+      float2 ml = make_float2(0.f, 0.f);
+      if (r < x.nr && head.n == 1) {
+        ml = sums[bh * rows + r];
+      } else if (r < x.nr) {
+        float m = -INFINITY, l = 0.f;
+        for (int i = lane; i < head.n; i += 32) {
+          const float2 v = *reinterpret_cast<const float2*>(part_at<RM, NW * 128>(*this, head, i) + RM * NW * 128 + 2 * r);
+          const float to = fmaxf(m, v.x), base = to == -INFINITY ? 0.f : to;
+          l = l * exp2_fast(m - base) + v.y * exp2_fast(v.x - base);
+          m = to;
+        }
+        float most = m;
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        l *= exp2_fast(m - (most == -INFINITY ? 0.f : most));
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        ml = row_sums(most, l);
+      }
+      if (lane == 0) set_row(s_rows, r, ml, r < x.nr ? x.end - (int)T + r / group : -1);
+    }
+    __syncthreads();
+    add_weights<0>(*this, bh, chunk, x.lo, x.end, s_rows);
+  }
 };
 
 // Key of row i of a product, in its eight.
@@ -637,92 +750,49 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// G lanes for each key of a head, four of its rows' scores at a time: their weights, added up.
-constexpr int kWeightThreads = 256, kMaxRows = PFA_DECODE_MAX_ROWS;
-constexpr int kWeightKeys = 4, kWeightRounds = 2;   // keys of a thread in flight, rounds of them
-
-template <int G>
-__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const Scores p, const Divisor chunks) {
-  constexpr int kStep = kWeightThreads / G, kBlock = kStep * kWeightKeys * kWeightRounds;   // keys
-  __shared__ float4 s_m[kMaxRows / 4], s_inv[kMaxRows / 4];   // of each row, 0 and 0 behind the last
-  __shared__ int4 s_pos[kMaxRows / 4];
+// Weights behind the join, from its row sums.
+template <int LANES>
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const Scores p) {
+  __shared__ RowSums s_rows[kMaxRows / 4];
   asm volatile("griddepcontrol.launch_dependents;");
-  const int bh = blockIdx.x / chunks, chunk = blockIdx.x - bh * (int)chunks.by, b = bh / p.heads;
+  const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x - bh * (int)p.chunks.by, b = bh / p.heads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t len = p.lengths[b];
   if (len < 0 || len > p.cap) return;
   const int end = (int)len, first = end - (int)p.T;
   const int lo = p.window > 0 ? max(0, max(first, 0) - p.window + 1) : 0;
-  if (lo + (int64_t)chunk * kBlock >= end) return;
-  for (int r = threadIdx.x; r < p.row_pad; r += kWeightThreads) {
-    const float2 ml = r < p.rows ? p.sums[(int64_t)bh * p.rows + r] : make_float2(0.f, 0.f);
-    reinterpret_cast<float*>(s_m)[r] = ml.x;
-    reinterpret_cast<float*>(s_inv)[r] = ml.y;
-    reinterpret_cast<int*>(s_pos)[r] = r < p.rows ? first + r / p.group : -1;   // -1 sees nothing
-  }
+  if (lo + (int64_t)chunk * (kWeightThreads / LANES * (kWeightKeys * kWeightRounds)) >= end) return;
+  for (int r = threadIdx.x; r < p.row_pad; r += kWeightThreads)
+    set_row(s_rows, r, r < p.rows ? p.sums[(int64_t)bh * p.rows + r] : make_float2(0.f, 0.f),
+            r < p.rows ? first + r / p.group : -1);
   __syncthreads();
-  const int sub = threadIdx.x % G, quads = p.row_pad / 4;
-  const float* const scores = p.scores + bh * p.score_head;
-  float* const weights = p.weights + (int64_t)bh * p.cap;
-#pragma unroll 1
-  for (int64_t at = lo + (int64_t)chunk * kBlock; at < end; at += (int64_t)chunks.by * kBlock)
-#pragma unroll 1
-    for (int round = 0; round < kWeightRounds; ++round) {
-      const int64_t j0 = at + round * (kStep * kWeightKeys) + threadIdx.x / G;
-      float sum[kWeightKeys], was[kWeightKeys];
-#pragma unroll
-      for (int i = 0; i < kWeightKeys; ++i) {
-        sum[i] = was[i] = 0.f;
-        if (sub == 0 && j0 + i * kStep < end) was[i] = weights[j0 + i * kStep];
-      }
-#pragma unroll 1
-      for (int q = sub; q < quads; q += G) {
-        float4 v[kWeightKeys];
-#pragma unroll
-        for (int i = 0; i < kWeightKeys; ++i)
-          if (j0 + i * kStep < end)
-            v[i] = *reinterpret_cast<const float4*>(scores + (j0 + i * kStep) * p.row_pad + 4 * q);
-        const float4 m = s_m[q], inv = s_inv[q];
-        const int4 pos = s_pos[q];
-#pragma unroll
-        for (int i = 0; i < kWeightKeys; ++i) {
-          const int64_t j = j0 + i * kStep;
-          // (what a row does not see may not have been written)
-          auto add = [&](float s, float m, float inv, int pos) {
-            if (j <= pos && (p.window <= 0 || j > pos - p.window)) sum[i] += exp2_fast(s - m) * inv;
-          };
-          add(v[i].x, m.x, inv.x, pos.x);
-          add(v[i].y, m.y, inv.y, pos.y);
-          add(v[i].z, m.z, inv.z, pos.z);
-          add(v[i].w, m.w, inv.w, pos.w);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kWeightKeys; ++i) {
-#pragma unroll
-        for (int d = 1; d < G; d <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
-        if (sub == 0 && j0 + i * kStep < end) weights[j0 + i * kStep] = was[i] + sum[i];
-      }
-    }
+  add_weights<LANES>(p, bh, chunk, lo, end, s_rows);
 }
 
-template <int G>
-int launch_weights(Scores p, int64_t heads, cudaStream_t stream) {
-  constexpr int kBlock = kWeightThreads / G * kWeightKeys * kWeightRounds;
+// Blocks of `threads` for a head's keys.
+Divisor chunks_of(const Scores& p, int threads) {
+  const int64_t block = threads / p.lanes * kWeightKeys * kWeightRounds;
   const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
-  const int64_t chunks = std::min<int64_t>((keys + kBlock - 1) / kBlock, 0x7fffffff / heads);
+  return divisor((uint32_t)((keys + block - 1) / block));
+}
+
+int launch_weights(Scores p, int64_t heads, cudaStream_t stream) {
+  p.chunks = chunks_of(p, kWeightThreads);
+  if (heads * p.chunks.by > 0x7fffffff)   // (then each takes several)
+    p.chunks = divisor((uint32_t)(0x7fffffff / heads));
   p.heads = divisor(p.Hkv);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(heads * chunks));
+  cfg.gridDim = dim3((unsigned)(heads * p.chunks.by));
   cfg.blockDim = dim3(kWeightThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, weights_kernel<G>, p, divisor((uint32_t)chunks)) == cudaSuccess)
-    return kOk;
+  auto* const kernel = p.lanes == 1 ? weights_kernel<1> : p.lanes == 2 ? weights_kernel<2>
+                       : p.lanes == 4 ? weights_kernel<4> : weights_kernel<8>;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return kOk;
   cudaGetLastError();
   return kErrLaunch;
 }
@@ -732,6 +802,11 @@ int launch(const Params<64>& all, const DecodeQ4Call& c) {
   using P = Params<UNIT>;
   P p;
   static_cast<Scores&>(p) = all;
+  // Beside the join the weights save a launch, but each of their blocks finds its head's sums for
+  // itself (us, beside / behind): 16 sequences of 1024 keys, 32/8 heads 13.8 / 15.4, one of 16384 12.8 / 14.0, of
+  // 131072 42.8 / 40.2; 32 of up to 8192 42.2 / 38.3.
+  p.fused = c.weights && p.rows <= 8 * NT &&
+            c.span.B * p.Hkv * chunks_of(p, kWeightThreads).by <= (int64_t)2 * c.num_sms;
   p.k4 = all.k4; p.v4 = all.v4; p.k_scale = all.k_scale; p.v_scale = all.v_scale;
   static DeviceOnce once;
   const int rc = once.run(c.device, [] {
@@ -739,10 +814,12 @@ int launch(const Params<64>& all, const DecodeQ4Call& c) {
                                 (int)sizeof(Shared<UNIT>)) == cudaSuccess ? kOk : kErrLaunch;
   });
   if (rc != kOk) return rc;
-  const Kernels<P> k = {decode_kernel<E, NW, NT, UNIT>, join_kernel<P, E, NW, 8 * NT, 8>,
-                        join_kernel<P, E, NW, 8 * NT, 1>, 8 * NT, NW, kBlocksPerSm,
-                        sizeof(Shared<UNIT>)};
-  return launch_list(k, p, c.span.B, c.num_sms, c.stream);
+  const Kernels<P> k = {decode_kernel<E, NW, NT, UNIT>,
+                        p.fused ? join_kernel<P, E, NW, 8 * NT, 8, true> : join_kernel<P, E, NW, 8 * NT, 8>,
+                        p.fused ? join_kernel<P, E, NW, 8 * NT, 1, true> : join_kernel<P, E, NW, 8 * NT, 1>,
+                        8 * NT, NW, kBlocksPerSm, sizeof(Shared<UNIT>)};
+  const int r = launch_list(k, p, c.span.B, c.num_sms, c.stream);
+  return r != kOk || !c.weights || p.fused ? r : launch_weights(p, c.span.B * p.Hkv, c.stream);
 }
 
 // Workspace: partial sums, two slots a run; with weights each row's sums and each score.
@@ -797,6 +874,9 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   p.score_head = w.score_head;
   p.row_pad = w.row_pad;
   p.weights = c.weights;
+  // Lanes to a key: as many as it has four rows, or four or eight that take turns.
+  const int quads = p.row_pad / 4;
+  p.lanes = quads <= 1 ? 1 : quads <= 3 ? 2 : quads % 8 == 0 || quads >= 24 ? 8 : 4;
   // With tiles of 16 rows a converted code serves two products; with 8 there are twice as many units
   // to spread, and less code to fetch.  16 rows, bf16 (us, tiles of 8 / of 16):
   //   one sequence, 32/8 heads of 128, 512 / 4096 / 16384 keys     7.0 / 8.5   8.3 / 10.1   13.2 / 13.2
@@ -814,13 +894,7 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   else   // (16 fp32 rows and units of 64 keys need more registers than there are: 16.7 us for 14.9)
     rc = c.D == 128 ? (few ? launch<float, 1, 1, 64>(p, c) : launch<float, 1, 2, 32>(p, c))
                     : (few ? launch<float, 4, 1, 64>(p, c) : launch<float, 4, 2, 32>(p, c));
-  if (rc != kOk || !c.weights) return rc;
-  // Lanes to a key: as many as it has four rows, or four or eight that take turns.
-  const int quads = p.row_pad / 4;
-  return quads <= 1                      ? launch_weights<1>(p, heads, c.stream)
-         : quads <= 3                    ? launch_weights<2>(p, heads, c.stream)
-         : quads % 8 == 0 || quads >= 24 ? launch_weights<8>(p, heads, c.stream)
-                                         : launch_weights<4>(p, heads, c.stream);
+  return rc;
 }
 
 }  // namespace pfa
