@@ -803,8 +803,8 @@ int launch(const Params<64>& all, const DecodeQ4Call& c) {
   P p;
   static_cast<Scores&>(p) = all;
   // Beside the join the weights save a launch, but each of their blocks finds its head's sums for
-  // itself (us, beside / behind): 16 sequences of 1024 keys, 32/8 heads 13.8 / 15.4, one of 16384 12.8 / 14.0, of
-  // 131072 42.8 / 40.2; 32 of up to 8192 42.2 / 38.3.
+  // itself (us, beside / behind): 16 sequences of 1024 keys, 32/8 heads 13.8 / 15.4, one of 16384 12.9 / 14.0, of
+  // 131072 42.8 / 41.2; 32 of up to 8192 42.2 / 38.9.
   p.fused = c.weights && p.rows <= 8 * NT &&
             c.span.B * p.Hkv * chunks_of(p, kWeightThreads).by <= (int64_t)2 * c.num_sms;
   p.k4 = all.k4; p.v4 = all.v4; p.k_scale = all.k_scale; p.v_scale = all.v_scale;

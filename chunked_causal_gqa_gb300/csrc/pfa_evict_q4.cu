@@ -114,32 +114,32 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sums, int64_t&
 }
 
 // Rows `rows` of width.by pieces move to 0 .. keep - 1, in place.  `rank` of `size` blocks; barrier(): theirs.
-template <typename T, typename B>
+template <int THREADS, typename T, typename B>
 __device__ __forceinline__ void move_rows(T* base, const int32_t* rows, int keep, const Divisor& width, int rank,
                                           int size, B&& barrier) {
-  const int w = (int)width.by, per_round = size * (kThreads * kPieces) / width;   // rows of a round
+  const int w = (int)width.by, per_round = size * (THREADS * kPieces) / width;   // rows of a round
 #pragma unroll 1
   for (int at = 0; at < keep;) {
     const int here = min(per_round, keep - at), pieces = here * w;
-    // consecutive pieces for the threads of a block, runs of kThreads for the blocks in turn
-    const int e0 = rank * kThreads + (int)threadIdx.x;
+    // consecutive pieces for the threads of a block, runs of THREADS for the blocks in turn
+    const int e0 = rank * THREADS + (int)threadIdx.x;
     T x[kPieces];
     int from[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int e = e0 + i * size * kThreads;
+      const int e = e0 + i * size * THREADS;
       if (e < pieces) from[i] = rows[at + e / width];
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int e = e0 + i * size * kThreads;
+      const int e = e0 + i * size * THREADS;
       if (e < pieces) x[i] = base[(int64_t)from[i] * w + (e - e / width * w)];
     }
     barrier();
     T* const to = base + (int64_t)at * w;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int e = e0 + i * size * kThreads;
+      const int e = e0 + i * size * THREADS;
       if (e < pieces) to[e] = x[i];
     }
     at += here;
@@ -305,13 +305,14 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Params p) {
   cluster_wait();
   if (tiles > 1) {
     cluster_barrier();   // the list is whole
-    move_rows(w, rows, p.keep, p.one, (int)rank, (int)size, [] { cluster_barrier(); });
+    move_rows<kThreads>(w, rows, p.keep, p.one, (int)rank, (int)size, [] { cluster_barrier(); });
   }
   for (int64_t j = p.keep + (int64_t)rank * kThreads + tid; j < n; j += size * kThreads)
     w[j] = 0.f;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) move_kernel(const Params p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) move_kernel(const Params p) {
   asm volatile("griddepcontrol.launch_dependents;");
   const int rank = (int)cluster_rank(), size = (int)cluster_size();
   const int id = blockIdx.x / size, part = id / p.heads;
@@ -329,15 +330,15 @@ __global__ void __launch_bounds__(kThreads, 2) move_kernel(const Params p) {
   const Divisor& pieces = part < 2 ? p.code_pieces : p.scale_pieces;
   auto barrier = [] { cluster_barrier(); };
   switch (bytes / (int)pieces.by) {
-    case 16: move_rows(reinterpret_cast<uint4*>(base), rows, p.keep, pieces, rank, size, barrier); break;
-    case 8: move_rows(reinterpret_cast<uint2*>(base), rows, p.keep, pieces, rank, size, barrier); break;
-    case 4: move_rows(reinterpret_cast<uint32_t*>(base), rows, p.keep, pieces, rank, size, barrier); break;
-    case 2: move_rows(reinterpret_cast<uint16_t*>(base), rows, p.keep, pieces, rank, size, barrier); break;
-    default: move_rows(base, rows, p.keep, pieces, rank, size, barrier);
+    case 16: move_rows<THREADS>(reinterpret_cast<uint4*>(base), rows, p.keep, pieces, rank, size, barrier); break;
+    case 8: move_rows<THREADS>(reinterpret_cast<uint2*>(base), rows, p.keep, pieces, rank, size, barrier); break;
+    case 4: move_rows<THREADS>(reinterpret_cast<uint32_t*>(base), rows, p.keep, pieces, rank, size, barrier); break;
+    case 2: move_rows<THREADS>(reinterpret_cast<uint16_t*>(base), rows, p.keep, pieces, rank, size, barrier); break;
+    default: move_rows<THREADS>(base, rows, p.keep, pieces, rank, size, barrier);
   }
 }
 
-int launch(void (*kernel)(const Params), int64_t clusters, int size, size_t smem, const Params& p,
+int launch(void (*kernel)(const Params), int64_t clusters, int size, int threads, size_t smem, const Params& p,
            cudaStream_t stream) {
   if (clusters * size > 0x7fffffff) return kErrShape;
   cudaLaunchAttribute attr[2];
@@ -348,7 +349,7 @@ int launch(void (*kernel)(const Params), int64_t clusters, int size, size_t smem
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * size));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -370,6 +371,15 @@ Divisor pieces_of(int n) {
   int size = 16;
   while (n % size) size /= 2;
   return divisor((uint32_t)(n / size));
+}
+
+// Threads of a moving block.  Blocks of 256, four to an SM, are in different phases of their rounds; where
+// the heads are too few to fill the SMs with them, larger ones take fewer rounds.  Whole call, us,
+// 256 / 512 threads: 63488 -> 16384 rows of 8 heads of 128 27.3 / 23.2, 120000 -> 65536 90.8 / 67.2; 32768 ->
+// 16384 rows of 32 heads 37.5 / 41.6, 16384 -> 8192 of 64 39.6 / 49.8, 8192 -> 6000 of 256 127 / 170.  (1024
+// threads, one block an SM: 27.3, 68.3, 60.1, 53.9, 184.)
+int move_threads(int64_t heads, int num_sms) {
+  return heads * 2 * kMaxCluster < (int64_t)2 * num_sms ? 512 : 256;
 }
 
 }  // namespace
@@ -396,10 +406,12 @@ int launch_cache_evict_q4(const EvictQ4Call& c) {
   const int64_t heads = c.B * c.Hkv;
   if (4 * heads * kMaxCluster > 0x7fffffff) return kErrShape;
   p.heads = (int)heads;
-  rc = launch(select_kernel, heads, blocks_for(p.cap, kTile), sizeof(Select), p, c.stream);
+  rc = launch(select_kernel, heads, blocks_for(p.cap, kTile), kThreads, sizeof(Select), p, c.stream);
   if (rc != kOk) return rc;
-  const int mov = blocks_for(c.keep * p.code_bytes, (int64_t)kThreads * kPieces * 16);
-  return launch(move_kernel, 4 * heads, mov, 0, p, c.stream);
+  const int64_t bytes = c.keep * p.code_bytes;
+  const int threads = move_threads(heads, c.num_sms);
+  return launch(threads == 512 ? move_kernel<512> : move_kernel<256>, 4 * heads,
+                blocks_for(bytes, (int64_t)threads * kPieces * 16), threads, 0, p, c.stream);
 }
 
 }  // namespace pfa

@@ -284,6 +284,7 @@ struct EvictQ4Call {
   int64_t* lengths_out;
   int32_t* rows_out;
   unsigned* err;
+  int num_sms;
   int device;
   cudaStream_t stream;
 };

@@ -406,7 +406,7 @@ int pfa_cache_evict_q4(void* k4, void* v4, void* k_scale, void* v_scale, float* 
   c.Hkv = num_kv_heads; c.D = head_dim;
   c.keep = keep; c.recent = recent;
   c.lengths_out = lengths_out; c.rows_out = rows_out;
-  c.err = d.err; c.device = d.device;
+  c.err = d.err; c.num_sms = d.num_sms; c.device = d.device;
   c.stream = static_cast<cudaStream_t>(stream);
   return launch_cache_evict_q4(c);
 }
