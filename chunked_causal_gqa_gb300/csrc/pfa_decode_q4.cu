@@ -887,14 +887,23 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
   const int64_t units = heads * ((p.rows + 7) / 8) * (keys / 64 + 1);
   const bool few = p.rows <= 8 || units < (int64_t)12 * c.num_sms * kBlocksPerSm;
-  int rc;
-  if (c.dtype == PFA_BF16)
-    rc = c.D == 128 ? (few ? launch<__nv_bfloat16, 1, 1, 64>(p, c) : launch<__nv_bfloat16, 1, 2, 64>(p, c))
-                    : (few ? launch<__nv_bfloat16, 4, 1, 64>(p, c) : launch<__nv_bfloat16, 4, 2, 64>(p, c));
-  else   // (16 fp32 rows and units of 64 keys need more registers than there are: 16.7 us for 14.9)
-    rc = c.D == 128 ? (few ? launch<float, 1, 1, 64>(p, c) : launch<float, 1, 2, 32>(p, c))
-                    : (few ? launch<float, 4, 1, 64>(p, c) : launch<float, 4, 2, 32>(p, c));
-  return rc;
+  // Units of 64 keys need fewer instructions a key, units of 32 spread further and their code is fetched
+  // sooner.  8 rows or less (us, 32 / 64 keys): one sequence, 32/8 heads of 128, 128 / 4096 / 16384 keys 4.8 / 5.4,
+  // 7.2 / 7.8, 10.1 / 9.8, 32 sequences of 8192 59.7 / 54.4; 8/2 heads of 512, fp32, one sequence of 4096 keys
+  // 9.7 / 10.8.  (16 fp32 rows and units of 64 keys need more registers than there are.)
+  const bool small = units < (int64_t)2 * c.num_sms * kBlocksPerSm;
+  if (c.dtype == PFA_BF16) {
+    if (c.D == 128)
+      return !few ? launch<__nv_bfloat16, 1, 2, 64>(p, c)
+             : small ? launch<__nv_bfloat16, 1, 1, 32>(p, c) : launch<__nv_bfloat16, 1, 1, 64>(p, c);
+    return !few ? launch<__nv_bfloat16, 4, 2, 64>(p, c)
+           : small ? launch<__nv_bfloat16, 4, 1, 32>(p, c) : launch<__nv_bfloat16, 4, 1, 64>(p, c);
+  }
+  if (c.D == 128)
+    return !few ? launch<float, 1, 2, 32>(p, c)
+           : small ? launch<float, 1, 1, 32>(p, c) : launch<float, 1, 1, 64>(p, c);
+  return !few ? launch<float, 4, 2, 32>(p, c)
+         : small ? launch<float, 4, 1, 32>(p, c) : launch<float, 4, 1, 64>(p, c);
 }
 
 }  // namespace pfa
