@@ -4,6 +4,7 @@
 #include "pfa_checks.h"
 
 #include <algorithm>
+#include <cmath>
 
 namespace pfa {
 namespace {
@@ -53,6 +54,11 @@ CacheQ4 cache_of(const void* k4, const void* v4, const void* k_scale, const void
                  int64_t cap, int k_exp, int v_exp) {
   return CacheQ4{const_cast<void*>(k4), const_cast<void*>(v4), const_cast<void*>(k_scale),
                  const_cast<void*>(v_scale), cap, k_exp, v_exp};
+}
+
+// The scores' factor with K's exponent has to be a float.
+int check_scale(float scale, int k_exp) {
+  return std::isfinite(std::ldexp(scale * 1.4426950408889634f, k_exp)) ? PFA_OK : PFA_ERR_VALUE;
 }
 
 // How a chunk of one sequence runs: few rows, and all of fp32, by the decode kernel; else the
@@ -227,6 +233,7 @@ int pfa_decode_attention_q4(const void* q, const void* k4, const void* v4, const
   if (B > kMaxLen || T > kMaxLen || T * (num_heads / num_kv_heads) > PFA_DECODE_MAX_ROWS)
     return PFA_ERR_SHAPE;
   if ((rc = check_cache(B * num_kv_heads, head_dim, max_seq_len, k_exp, v_exp)) != PFA_OK) return rc;
+  if ((rc = check_scale(scale, k_exp)) != PFA_OK) return rc;
   if (B == 0 || T == 0) return PFA_OK;
   if (!lengths) return PFA_ERR_NULL;
   if ((rc = check_span(B, T, 0, lengths)) != PFA_OK) return rc;
@@ -308,6 +315,7 @@ int pfa_prefill_attention_q4(const void* q, const void* k4, const void* v4, cons
   if (rc != PFA_OK) return rc;
   if ((rc = check_span(1, T, start_pos, nullptr)) != PFA_OK) return rc;
   if ((rc = check_cache(num_kv_heads, head_dim, max_seq_len, k_exp, v_exp)) != PFA_OK) return rc;
+  if ((rc = check_scale(scale, k_exp)) != PFA_OK) return rc;
   if (start_pos + T > max_seq_len) return PFA_ERR_SHAPE;
   if (T == 0) return PFA_OK;
   const CacheQ4 cache = cache_of(k4, v4, k_scale, v_scale, max_seq_len, k_exp, v_exp);

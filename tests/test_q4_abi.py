@@ -93,7 +93,7 @@ def test_decode_refusals(lib, last):
     for bad in (dict(H=6, Hkv=4), dict(H=0), dict(D=64), dict(D=256), dict(H=258, Hkv=2), dict(B=-1),
                 dict(T=-1), dict(T=257), dict(cap=0), dict(qs=1000), dict(os=1000)):
         assert decode(lib, **bad) == SHAPE, bad
-    for bad in (dict(scale=float("nan")), dict(ke=65), dict(ve=-65)):
+    for bad in (dict(scale=float("nan")), dict(ke=65), dict(ve=-65), dict(scale=1e30, ke=64)):
         assert decode(lib, **bad) == VALUE, bad
     for bad in (dict(q=None), dict(o=None), dict(ln=None), dict(k4=None), dict(vs=None)):
         assert decode(lib, **bad) == NULL, bad
@@ -128,7 +128,7 @@ def test_prefill_refusals(lib, last):
     for bad in (dict(H=6, Hkv=4), dict(D=64), dict(T=-1), dict(sp=-1), dict(sp=157), dict(cap=100),
                 dict(row=1000), dict(H=258, Hkv=2)):
         assert prefill(lib, **bad) == SHAPE, bad
-    for bad in (dict(scale=float("inf")), dict(ke=99)):
+    for bad in (dict(scale=float("inf")), dict(ke=99), dict(scale=-1e25, ke=64)):
         assert prefill(lib, **bad) == VALUE, bad
     for bad in (dict(q=None), dict(o=None), dict(ks=None)):
         assert prefill(lib, **bad) == NULL, bad

@@ -294,6 +294,38 @@ def test_decode_one_heavy_key_and_a_tail(dt):
     ok()
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_decode_rows_that_are_not_finite_leave_the_others_right(dt, what):
+    case = ([700, 130], 2, 8, 2, 128, 0, 704, dt)
+    cache, q, k, v = attention_case(case, 31)
+    clean = pkg.decode_attention_q4(q, cache, lengths(case[0]))
+    check_attention(clean, None, None, q, k, v, case)
+    q[0, 1, 2, 5] = what
+    q[1, 0, 7] = what
+    out = pkg.decode_attention_q4(q, cache, lengths(case[0]))
+    bad = torch.zeros(2, 2, 8, dtype=torch.bool, device=G.dev())
+    bad[0, 1, 2] = bad[1, 0, 7] = True
+    assert not torch.isfinite(out[bad]).any() and torch.equal(out[~bad], clean[~bad])
+    ok()
+
+
+def test_decode_keys_that_some_tokens_do_not_see():
+    """NaN rows behind a sequence, and before every token's window, touch nothing; the cut runs through a unit."""
+    for n, T, window in ((100, 1, 0), (100, 3, 40), (129, 5, 64), (64, 1, 1), (1000, 2, 300)):
+        for dt in (BF16, F32):
+            case = ([n], T, 8, 2, 128, window, 1100, dt)
+            cache, q, k, v = attention_case(case, n + T)
+            lo = max(0, n - T - window + 1) if window else 0
+            for s in (cache.k_scale, cache.v_scale):
+                s.view(torch.uint8)[:, :, :lo] = 0x7f
+            w = torch.zeros(1, 2, 1100, device=G.dev())
+            out = pkg.decode_attention_q4(q, cache, lengths([n]), weights=w, window=window)
+            k[:, :, :lo] = v[:, :, :lo] = 0
+            check_attention(out, w, torch.zeros_like(w), q, k, v, case)
+    ok()
+
+
 def test_decode_reports_lengths_and_leaves_the_others_right():
     case = ([50, 60, 70], 2, 8, 2, 128, 0, 64, BF16)
     cache, q, k, v = attention_case(case, 9)
