@@ -1,5 +1,5 @@
 """Build libpfa.so (the C-ABI library) for sm_103a with nvcc, and _pfa_torch.so
-(the operators of the 8-bit cache on torch tensors, over that library) with g++, in-tree.
+(the operators of the 8-bit and 4-bit caches on torch tensors, over that library) with g++, in-tree.
 
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 chunked_causal_gqa_gb300/_build/libpfa.so with the CUDA runtime linked
@@ -135,7 +135,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile and link libpfa.so, then _pfa_torch.so; returns libpfa.so's path.
 
     Where _pfa_torch.so cannot be compiled (no g++, no headers of Python or torch) that is a
-    warning: only the operators of the 8-bit cache need it, and only from Python."""
+    warning: only the operators of the 8-bit and 4-bit caches need it, and only from Python."""
     if not force and not extra_flags and up_to_date():
         _extension_or_warning(force)
         return LIB

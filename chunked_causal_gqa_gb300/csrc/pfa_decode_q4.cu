@@ -29,13 +29,29 @@
 // The exponent's base rises only when a score passes it by 2^4, so that most units need no
 // maximum across lanes and no rescaling: a weight is 2^(s - base) 2^11, at most 2^15.
 //
-// Work split and join: pfa_decode.cuh.  Four warps take a run's units of 64 keys in turn, each with
-// its own ring filled by cp.async; head_dim 512: four warps share a unit, each with 128 channels, and
-// exchange partial scores.
+// Work split and join: pfa_decode.cuh.  Four warps take a run's units of 64 (or 32) keys in turn, each with
+// its own ring of 128 keys filled by cp.async; head_dim 512: four warps share a unit, each with 128
+// channels, and exchange partial scores.  Two blocks an SM: the unit's 64 keys want the registers.
 //
 // Accumulated weights: the scores go to the workspace as they are made (4 bytes a row and key beside
-// the 144 of the cache); the join leaves each row's maximum and sum, and a third kernel adds up
-// 2^(s - m) / l over the rows of a key.
+// the 144 of the cache); the join leaves each row's maximum and sum, and 2^(s - m) / l, added up over
+// the rows of a key, follows beside the join or in a kernel behind it.  (Making the scores again would
+// read K again: 72 bytes a key, where 16 are written and 16 read for four rows.)
+//
+// Measured on GB300, all kernels of a call, one pass among others:
+//   1 sequence of 131072 keys, 32/8 heads of 128, bf16 (151 MB)      32.1 us (floor 22.2): streaming at
+//     7.1 TB/s (each further sequence takes 21.3 us), and 9 us of start, uneven ends and join
+//   32 sequences up to 8192 keys with weights (144 MB)               39.9 us (floor 21.2): the same, 8 us
+//     of which are the scores, written and read, and the third launch
+//   32 tokens at 16384 keys with weights                             69 us (floor 4.4): eight tiles of rows
+//     convert the codes anew, 44 us; 67 MB of scores, written and read, the rest
+//   4 sequences, 3 tokens, window 1024, 8/2 heads of 512, fp32       12.1 us: two launches and some ten
+//     latencies (floor 0.6)
+// Steps (the first two cases): units of 32 keys, three blocks an SM, each copy with its own addresses
+// and bounds 38.6 / 49.1; running offsets, score factor and base in one fused multiply-add, units of 64
+// keys and two blocks 32.2 / 39.4 (512 instructions for 32 keys of a warp, 715 before).  128 registers
+// and four blocks with two stages lost (42.8 / 50.2), and so did making the next unit's scores beside this
+// one's sum (33.0 / 40.8): it is HBM that streams, not the products that wait.
 #include "pfa_decode.cuh"
 #include "pfa_q4.cuh"
 

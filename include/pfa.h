@@ -63,10 +63,11 @@ typedef enum {
     PFA_ERR_ALIAS = -9,      /* out overlaps q, k_cache or v_cache                  */
     PFA_ERR_SCRATCH = -10,   /* the shape needs more scratch than
                                 pfa_prefill_attention_noalloc holds, or than the
-                                workspace given to an 8-bit cache's attention       */
+                                workspace given to an 8-bit or 4-bit cache's
+                                attention                                           */
     PFA_ERR_LENGTHS = -11    /* lengths read on the device ({T, start_pos} of
-                                pfa_prefill_attention_graph, the 8-bit cache's
-                                lengths) did not fit the capacities (reported
+                                pfa_prefill_attention_graph, the 8-bit and 4-bit
+                                caches' lengths) did not fit the capacities (reported
                                 after a sync by pfa_last_device_error)              */
 } pfa_status;
 
@@ -603,8 +604,9 @@ PFA_API int pfa_cache_read_q4(const void *k4, const void *v4, const void *k_scal
  *             A key's total is what pfa_cache_evict_q4 goes by.
  *   workspace of pfa_decode_workspace_bytes_q4 bytes: with weights it holds each score
  *             (4 bytes for each row of the T * num_heads / num_kv_heads and cache row).
- * Weights of the sum over V are rounded to 11 bits (bf16) or 21 (fp32); the accumulated ones
- * are not rounded below fp32.
+ * Weights of the sum over V are rounded to 11 bits (bf16) or 21 (fp32), small ones to 2^-36 of the
+ * row's largest; the accumulated ones are not rounded below fp32.  Two calls that add to the
+ * same weights must not run at the same time.
  */
 PFA_API int pfa_decode_attention_q4(const void *q, const void *k4, const void *v4,
                                     const void *k_scale, const void *v_scale, void *out,
@@ -620,9 +622,10 @@ PFA_API int pfa_decode_workspace_bytes_q4(int64_t B, int64_t T, int num_heads, i
 /*
  * pfa_prefill_attention_q4 -- pfa_prefill_attention_cache (linear) on one
  * sequence's 4-bit cache: T tokens at start_pos .., whose own rows have been
- * written.  q and out rows are qkv_dim elements apart.  Few rows T * num_heads /
- * num_kv_heads, and all of fp32, run the kernel of pfa_decode_attention_q4; longer bf16 chunks
- * read the visible rows back into the workspace and run the 16-bit kernels on them.
+ * written.  q and out rows are qkv_dim elements apart.  By the rows T * num_heads /
+ * num_kv_heads, kv heads and keys it runs the kernel of pfa_decode_attention_q4 (few of them, and all of
+ * fp32), or it reads the visible rows back into the workspace and runs the 16-bit kernels on them
+ * (the softmax weights are then rounded to bf16 as those kernels do).
  * workspace: pfa_prefill_workspace_bytes_q4 bytes, 256-byte aligned, not shared by calls that
  * can run at the same time.
  */
@@ -646,7 +649,7 @@ PFA_API int pfa_prefill_workspace_bytes_q4(int64_t T, int64_t start_pos, int num
  * are.  Sequences of at most `keep` rows are not changed.
  *
  *   weights      device fp32 [B][num_kv_heads][max_seq_len], updated in place.  NaN counts as
- *                larger than any number.
+ *                larger than any number, and -0 as 0, which it becomes.
  *   lengths      device, B int64.
  *   keep, recent 1 <= keep <= max_seq_len, 0 <= recent <= keep.
  *   lengths_out  device, B int64: min(lengths[b], keep); may be lengths.  (A length out of
