@@ -34,7 +34,6 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 256;
-constexpr int kLane = 16, kTile = kThreads * kLane;   // rows of a lane and of a block at a time
 constexpr int kPieces = 8;       // of a thread in a round
 constexpr int kMaxCluster = 8;
 
@@ -155,18 +154,22 @@ __device__ __forceinline__ void move_rows(T* base, const int32_t* rows, int keep
   }
 }
 
+template <int LANE>
 struct Select {
   int hist[4][kBins];                // a pass each: other blocks may still read the last one
   int sums[32];                      // of the warps; zero behind the last
   int64_t pairs[32], total;          // rows that stay for sure, and 2^32 times those at the border
   int digit, count, left;
-  uint32_t keys[kWarps][32][kLane + 1];   // a lane's rows, one word apart from the next lane's
-  uint16_t kept[kWarps][32 * kLane];      // of a warp, in order
+  uint32_t keys[kWarps][32][LANE + 1];   // a lane's rows, one word apart from the next lane's
+  uint16_t kept[kWarps][32 * LANE];      // of a warp, in order
 };
 
+// LANE: rows of a lane at a time.
+template <int LANE>
 __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Params p) {
+  constexpr int kLane = LANE, kTile = kThreads * LANE;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Select& sm = *reinterpret_cast<Select*>(smem_raw);
+  Select<LANE>& sm = *reinterpret_cast<Select<LANE>*>(smem_raw);
   asm volatile("griddepcontrol.launch_dependents;");
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const int bh = blockIdx.x / size, b = bh / p.Hkv;
@@ -391,15 +394,21 @@ int move_threads(int64_t heads, int num_sms) {
   return heads * 2 * kMaxCluster < (int64_t)2 * num_sms ? 512 : 256;
 }
 
+template <int LANE>
+int launch_select(const Params& p, const EvictQ4Call& c) {
+  static DeviceOnce once;
+  const int rc = once.run(c.device, [] {
+    return cudaFuncSetAttribute(select_kernel<LANE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(Select<LANE>)) == cudaSuccess ? kOk : kErrLaunch;
+  });
+  if (rc != kOk) return rc;
+  return launch(select_kernel<LANE>, p.heads, blocks_for(p.cap, kThreads * LANE), kThreads, sizeof(Select<LANE>), p,
+                c.stream);
+}
+
 }  // namespace
 
 int launch_cache_evict_q4(const EvictQ4Call& c) {
-  static DeviceOnce once;
-  int rc = once.run(c.device, [] {
-    return cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(Select)) == cudaSuccess ? kOk : kErrLaunch;
-  });
-  if (rc != kOk) return rc;
   Params p;
   p.part[0] = (uint8_t*)c.cache.k4; p.part[1] = (uint8_t*)c.cache.v4;
   p.part[2] = (uint8_t*)c.cache.k_scale; p.part[3] = (uint8_t*)c.cache.v_scale;
@@ -415,7 +424,12 @@ int launch_cache_evict_q4(const EvictQ4Call& c) {
   const int64_t heads = c.B * c.Hkv;
   if (4 * heads * kMaxCluster > 0x7fffffff) return kErrShape;
   p.heads = (int)heads;
-  rc = launch(select_kernel, heads, blocks_for(p.cap, kTile), kThreads, sizeof(Select), p, c.stream);
+  // With 4 rows a lane a pass is shorter and a head has more blocks: gains where they are all there at once
+  // (16 / 4 rows, us: 16000 rows of 8 heads 17 / 15, 8000 of 16 17 / 15; 8192 of 256 48 / 60, 1000 of 256 23 / 21).
+  const bool thin = p.cap <= 4 * kThreads ||
+                    (p.cap <= 4 * kThreads * kMaxCluster &&
+                     heads * blocks_for(p.cap, 4 * kThreads) <= (int64_t)2 * c.num_sms);
+  const int rc = thin ? launch_select<4>(p, c) : launch_select<16>(p, c);
   if (rc != kOk) return rc;
   const int64_t bytes = c.keep * p.code_bytes;
   const int threads = move_threads(heads, c.num_sms);
