@@ -1,0 +1,126 @@
+"""The 4-bit cache's attention on paths that sizes alone reach: chunks that read the cache back, batches of
+more sequences than one list of work holds, calls side by side, graphs that share a workspace."""
+import pytest
+import torch
+
+import chunked_causal_gqa_gb300 as pkg
+from tests import gpu_util as G
+from tests import q4_reference as R
+from tests import q8_reference as R8
+from tests.test_q4_gpu import BF16, F32, attention_case, check_attention, lengths, ok, randn, within
+
+pytestmark = pytest.mark.gpu
+
+
+READ_BACK = [  # T, start, H, Hkv, D, window
+    (1100, 117, 8, 2, 128, 0),
+    (1100, 117, 8, 2, 128, 200),
+    (2000, 0, 4, 1, 128, 0),
+    (700, 1333, 16, 8, 128, 0),
+    (700, 1333, 16, 8, 128, 64),
+    (400, 640, 8, 2, 512, 0),
+]
+
+
+@pytest.mark.parametrize("case", READ_BACK, ids=str)
+def test_a_chunk_that_reads_the_cache_back(case):
+    T, start, H, Hkv, D, window = case
+    n = start + T
+    seen = T + (min(start, window - 1) if window else start)       # rows that the chunk sees
+    assert pkg.prefill_workspace_bytes_q4(T, start, H, Hkv, D, window) >= 2 * Hkv * seen * D * 2
+    cache = pkg.Q4Cache(*R.make_cache(Hkv, n + 9, D, seed=16, device=G.dev(), batch=1, dead=[n])).slot(0)
+    cache = cache._replace(k_exponent=1, v_exponent=-2)
+    q = randn((T, H, D), BF16, 14, 0.5)
+    out = pkg.prefill_attention_q4(q, cache, start_pos=start, window=window)
+    k, v = R.values(cache.k, cache.k_scale, 1), R.values(cache.v, cache.v_scale, -2)
+    want, tol, _, _ = R.attention(q, k, v, n, window, R8.default_scale(D), BF16)
+    # the 16-bit kernels round the weights to bf16
+    j, pos = torch.arange(n, device=G.dev()), torch.arange(start, n, device=G.dev())[:, None]
+    hidden = (j > pos) | (j <= pos - window if window else torch.zeros_like(j, dtype=torch.bool))
+    for h in range(H):
+        kv = h // (H // Hkv)
+        p = torch.softmax((q[:, h].double() @ k[kv, :n].T * R8.default_scale(D)).masked_fill(hidden, float("-inf")), -1)
+        tol[:, h] += 2.0 ** -8 * (p @ v[kv, :n].abs()) * (1 + 2.0 ** -8)
+    within(out, want, tol)
+    ok()
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_more_sequences_than_one_list_of_work_holds(T):
+    B, H, Hkv, D, cap = 16500, 2, 1, 128, 6
+    cache = pkg.Q4Cache(*R.make_cache(Hkv, cap, D, batch=B, seed=21, device=G.dev()))
+    q = randn((B, T, H, D), BF16, 22)
+    ns = [(7 * b + b // 100) % (cap + 1) for b in range(B)]
+    w0 = torch.rand(B, Hkv, cap, device=G.dev())
+    w = w0.clone()
+    out = pkg.decode_attention_q4(q, cache, lengths(ns), weights=w)
+    some = [0, 1, 2, 3, 4, 5, 6, 4095, 5460, 5461, 8191, 8192, 16383, 16384, 16385, 16386, 16387, B - 2, B - 1]
+    at = torch.tensor(some, device=G.dev())
+    k, v = (R.values(c[at], s[at]) for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    check_attention(out[at], w[at], w0[at], q[at], k, v, ([ns[b] for b in some], T, H, Hkv, D, 0, cap, BF16))
+    # the others: what each gives in a batch of its own
+    for b0 in range(0, B, 1500):
+        z = slice(b0, b0 + 1500)
+        w1 = w0[z].clone()
+        one = pkg.decode_attention_q4(q[z], pkg.Q4Cache(cache.k[z], cache.v[z], cache.k_scale[z], cache.v_scale[z]),
+                                      lengths(ns[z]), weights=w1)
+        assert torch.equal(one, out[z])
+        # sums and scores are equal; the order of the tokens' and heads' weights may be another
+        within(w1, w[z].double(), 2.0 ** -20 * w[z].double())
+    ok()
+
+
+def test_calls_at_the_same_time():
+    """Four streams, each with weights and workspaces of its own, over one cache."""
+    case = ([3000, 17, 2999, 0], 2, 8, 2, 128, 0, 3001, BF16)
+    cache, _, _, _ = attention_case(case, 31)
+    n = lengths(case[0])
+    qs = [randn((4, 2, 8, 128), BF16, 40 + i) for i in range(4)]
+    want = []
+    for q in qs:
+        w = torch.zeros(4, 2, 3001, device=G.dev())
+        want.append((pkg.decode_attention_q4(q, cache, n, weights=w), w))
+    ws = [torch.zeros(4, 2, 3001, device=G.dev()) for _ in qs]
+    outs = [torch.empty_like(q) for q in qs]
+    need = pkg.decode_workspace_bytes_q4(4, 2, 8, 2, 128, 3001, weights=True)
+    scratch = [torch.empty(need, dtype=torch.uint8, device=G.dev()) for _ in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for w in ws:
+            w.zero_()
+        torch.cuda.synchronize()
+        for q, w, out, s, z in zip(qs, ws, outs, streams, scratch):
+            pkg.decode_attention_q4(q, cache, n, out, weights=w, stream=s, workspace=z)
+        torch.cuda.synchronize()
+        for (o, w), out, w1 in zip(want, outs, ws):
+            assert torch.equal(o, out) and torch.equal(w, w1)
+    ok()
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_graphs_that_share_a_workspace(dt):
+    """Two calls of different shapes, captured over one workspace that held NaN, replayed in turn."""
+    a, b = ([2000, 5], 1, 8, 2, 128, 0, 2001, dt), ([300], 9, 8, 2, 128, 50, 300, dt)
+    calls, need = [], 0
+    for i, case in enumerate((a, b)):
+        cache, q, _, _ = attention_case(case, 50 + i)
+        n, w = lengths(case[0]), torch.zeros(len(case[0]), 2, case[6], device=G.dev())
+        need = max(need, pkg.decode_workspace_bytes_q4(len(case[0]), case[1], 8, 2, 128, case[6], weights=True, dtype=dt))
+        out = pkg.decode_attention_q4(q, cache, n, weights=w, window=case[5])
+        calls.append((q, cache, n, case[5], out, w.clone(), torch.zeros_like(out), w.zero_()))
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=G.dev())
+    graphs = []
+    for q, cache, n, window, _, _, out, w in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pkg.decode_attention_q4(q, cache, n, out, weights=w, window=window, workspace=ws)
+        graphs.append(graph)
+    for _ in range(3):
+        for graph, (*_, want, acc, out, w) in zip(graphs, calls):
+            w.zero_()
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(w, acc)
+    ok()
