@@ -900,7 +900,8 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   //   one sequence of 131072 keys                                  51.0 / 43.4
   //   8/2 heads of 512, 16 sequences of 2048, 4 of 32768 keys      26.3 / 31.6   65.9 / 53.7
   // fp32: 9.5 / 11.9 at 4096 keys, 23.2 / 23.8 at 32768, 8 sequences of 8192 keys 43.8 / 38.9.
-  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
+  const int64_t rows = c.span.lengths ? p.cap : c.span.start_pos + p.T;   // most that a sequence can have
+  const int64_t keys = p.window > 0 ? std::min<int64_t>(rows, p.window + p.T) : rows;
   const int64_t units = heads * ((p.rows + 7) / 8) * (keys / 64 + 1);
   const bool few = p.rows <= 8 || units < (int64_t)12 * c.num_sms * kBlocksPerSm;
   // Units of 64 keys need fewer instructions a key, units of 32 spread further and their code is fetched
