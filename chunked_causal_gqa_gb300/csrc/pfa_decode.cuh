@@ -313,7 +313,7 @@ __device__ __forceinline__ const float* part_at(const P& p, const Parts& y, int 
 }
 
 // A block has 128 columns of one row (GROUPS warps that take the parts in turn, in the
-// blocks' order, each with a running maximum) or, with GROUPS 1, of all rows of a
+// blocks' order, each with a running maximum) or, with GROUPS 1, of up to 16 rows of a
 // tile, a warp each.  It joins the parts of its head, and writes the zeros of rows
 // that see nothing.
 template <typename P, typename E, int NW, int RM, int GROUPS, bool MORE = false>
@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(512) join_kernel(const P p, int blocks) {
       return;
     }
   const int id = blockIdx.x / NW, d = blockIdx.x % NW * 128 + lane * 4;
-  const int eh = id / p.joined, r = id - eh * (int)p.joined.by + warp / GROUPS;
+  const int eh = id / p.joined;
+  const int r = (id - eh * (int)p.joined.by) * ((int)(blockDim.x >> 5) / GROUPS) + warp / GROUPS;
   const int e = eh / p.heads, h = eh - e * p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;");
   const auto x = entry_of<RM, true>(p, e);
@@ -410,7 +411,7 @@ template <typename P>
 struct Kernels {
   void (*decode)(const P);
   void (*join_many)(const P, int);   // eight warps a row
-  void (*join_few)(const P, int);    // a warp a row, all rows of a tile
+  void (*join_few)(const P, int);    // a warp a row, up to 16 rows of a tile
   int rm, nw, blocks_per_sm;         // rows of a tile, head_dim / 128
   size_t smem;
 };
@@ -455,14 +456,15 @@ int launch_list(const Kernels<P>& k, P p, int64_t B, int num_sms, cudaStream_t s
       // few a warp (32 sequences of 8 heads: 49.7 us for both kernels with eight, 46.3 with one).
       const int rows = std::min(k.rm, p.rows);
       const bool many = (int64_t)p.entries * p.Hkv * 8 <= blocks;
-      p.joined = divisor(many ? rows : 1);
-      const int64_t joins = (int64_t)p.entries * p.Hkv * p.joined.by * k.nw;
-      int threads = many ? 256 : rows * 32;
+      int threads = many ? 256 : std::min(rows, 16) * 32;
       int64_t more = 0;
       if constexpr (P::kSums) {
         threads = std::max(threads, p.more_threads());
         more = p.more_blocks(threads);
       }
+      const int block_rows = many ? 1 : threads / 32;
+      p.joined = divisor((rows + block_rows - 1) / block_rows);
+      const int64_t joins = (int64_t)p.entries * p.Hkv * p.joined.by * k.nw;
       if (joins + more > 0x7fffffff) return kErrShape;
       p.joins = (int)joins;
       cfg.gridDim = dim3((unsigned)blocks);

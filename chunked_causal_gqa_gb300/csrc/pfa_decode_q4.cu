@@ -51,7 +51,9 @@
 // and bounds 38.6 / 49.1; running offsets, score factor and base in one fused multiply-add, units of 64
 // keys and two blocks 32.2 / 39.4 (512 instructions for 32 keys of a warp, 715 before).  128 registers
 // and four blocks with two stages lost (42.8 / 50.2), and so did making the next unit's scores beside this
-// one's sum (33.0 / 40.8): it is HBM that streams, not the products that wait.
+// one's sum (33.0 / 40.8): it is HBM that streams, not the products that wait.  More than 8 rows (16 of 63488
+// keys 28.4 -> 24.4 us in the kernel, issuing 40 -> 45 % of the cycles, the tensor pipe 34 %): second operands shared
+// through shared memory, and the scores of all keys of a unit side by side.
 #include "pfa_decode.cuh"
 #include "pfa_q4.cuh"
 
@@ -229,8 +231,13 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   return b;
 }
 
-template <int UNIT>
+// Whether the warps of a block share the second operands of the scores (see decode_kernel).
+template <typename E, int NW, int NT>
+constexpr bool kWide = NT > 1 && NW == 1 && sizeof(E) == 2;
+
+template <int UNIT, int NT, bool WIDE>
 struct Shared {
+  static constexpr int kProducts = WIDE ? NT : 0;
   static constexpr int kStages = 128 / UNIT;
   static constexpr int kHalf = UNIT * 64;        // bytes of a warp's K (or V) codes of a stage
   static constexpr int kScales = UNIT * 8;       // and of its scales
@@ -239,11 +246,13 @@ struct Shared {
   static constexpr int kJoinBytes = kWarps * UNIT * 128;
   alignas(128) uint8_t ring[kWarps][kStages][kStageBytes];
   alignas(16) uint8_t join[kJoinBytes];
-  float2 ml[kWarps][16];                         // a warp's {m, l} of each row
+  float2 ml[kWarps][8 * NT];                     // a warp's {m, l} of each row
+  uint2 query[kProducts * 8 + 1][32];            // [product][k16 step][lane]
+  float factor[kProducts * 8 + 2];               // of a row's scores
   ListShared list;
   static_assert(kJoinBytes >= kWarps * 8 * 128 * 4, "join area");
 };
-static_assert(kBlocksPerSm * (sizeof(Shared<64>) + 1024) <= 228 * 1024, "shared memory of an SM");
+static_assert(kBlocksPerSm * (sizeof(Shared<64, 2, true>) + 1024) <= 228 * 1024, "shared memory of an SM");
 
 // NW: warps of a unit (head_dim / 128).  NT: products a tile, tiles of 8 NT rows.
 template <typename E, int NW, int NT, int UNIT>
@@ -254,11 +263,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   constexpr int D = NW * 128, TEAMS = kWarps / NW, RM = 8 * NT;
   constexpr bool F32 = sizeof(E) == 4;
   constexpr int SETS = F32 ? 2 : 1;   // high and low halves
-  constexpr int kUnit = UNIT, kTiles = UNIT / 16, kStages = Shared<UNIT>::kStages;
-  constexpr int kHalf = Shared<UNIT>::kHalf, kScales = Shared<UNIT>::kScales, kStageBytes = Shared<UNIT>::kStageBytes;
-  static_assert(NW == 1 || Shared<UNIT>::kJoinBytes >= 2 * NW * kTiles * NT * 32 * 16, "score exchange");
+  // More rows than a product's eight: the scores' second operands are in shared memory, each warp having
+  // made those of one product, and what can be made anew is not held.  That leaves registers for
+  // the products of all keys of a unit at once, NT * UNIT / 16 chains of them that do not wait for one another.
+  constexpr bool WIDE = kWide<E, NW, NT>;
+  static_assert(!WIDE || NT <= kWarps, "a warp for each product");
+  using Sh = Shared<UNIT, NT, WIDE>;
+  constexpr int kUnit = UNIT, kTiles = UNIT / 16, kStages = Sh::kStages;
+  constexpr int kHalf = Sh::kHalf, kScales = Sh::kScales, kStageBytes = Sh::kStageBytes;
+  static_assert(NW == 1 || Sh::kJoinBytes >= 2 * NW * kTiles * NT * 32 * 16, "score exchange");
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  Shared<UNIT>& sm = *reinterpret_cast<Shared<UNIT>*>(smem_raw);
+  Sh& sm = *reinterpret_cast<Sh*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, qd = lane & 3;
   const int team = warp / NW, part = warp % NW;
@@ -278,9 +293,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
   // Query rows of a piece as they are stored, this warp's columns: the lane's 32
   // elements of its rows.  Rows past the tile repeat its last.
   // They are asked for under the prologue or the join before, but for two fp32 rows, which
-  // would need 64 registers across the join.
+  // would need 64 registers across the join.  (WIDE: those of the product that is this warp's.)
   constexpr int RV = F32 ? 8 : 4;   // 16-byte vectors of a row
-  constexpr bool EARLY = NT * RV <= 8;
+  constexpr bool EARLY = !WIDE && NT * RV <= 8;
   uint4 raw[EARLY ? NT * RV : RV];
   auto load_row = [&](int i) {
     const int r = cu.x.r0 + min(g + 8 * i, cu.x.nr - 1);
@@ -292,10 +307,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
       raw[(EARLY ? i * RV : 0) + j] = *reinterpret_cast<const uint4*>(row + j * (16 / (int)sizeof(E)));
   };
   auto load_early = [&]() {
+    if (cu.done()) return;
     if constexpr (EARLY) {
-      if (cu.done()) return;
 #pragma unroll
       for (int i = 0; i < NT; ++i) load_row(i);
+    } else if constexpr (WIDE) {
+      if (warp < NT) load_row(warp);
     }
   };
   load_early();
@@ -380,10 +397,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 
   while (!cu.done()) {
     const auto x = cu.x;
-    // ---- the piece's query rows, scaled by a power of two each
-    uint32_t qf[NT][SETS][8][2];
-    float srow[NT][2];     // rows 2 qd, 2 qd + 1 of each product
-    int hi[NT][2], lo[NT][2];
+    // ---- the piece's query rows, scaled by a power of two each (WIDE: one product's, for all warps)
+    constexpr int QT = WIDE ? 1 : NT;
+    uint32_t qf[QT][SETS][8][2];
+    float srow[QT][2];     // rows 2 qd, 2 qd + 1 of each product
+    int hi[QT][2], lo[QT][2];
     auto raw_at = [&](int i, int j) -> float {   // element j of the lane's 32 of row i
       const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
       if constexpr (F32) {
@@ -393,9 +411,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
         return __uint_as_float(j % 2 ? v & 0xffff0000u : v << 16);
       }
     };
+    auto seen_to = [&](int r) { return x.end - (int)p.T + (x.r0 + min(r, x.nr - 1)) / p.group; };
+    auto seen_from = [&](int to) { return p.window > 0 ? to - p.window + 1 : 0; };
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      if constexpr (!EARLY) load_row(i);
+    for (int i = 0; i < QT; ++i) {
+      if constexpr (!EARLY && !WIDE) load_row(i);
       float amax = 0.f;
 #pragma unroll
       for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(raw_at(i, j)));
@@ -422,12 +442,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
           else
             qf[i][0][s][c] = half2_of(w0, w1);
         }
+      if constexpr (WIDE) {
+        if (warp < NT) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        srow[i][c] = __shfl_sync(0xffffffffu, down, (2 * qd + c) * 4);
-        const int r = x.r0 + min(8 * i + 2 * qd + c, x.nr - 1);
-        hi[i][c] = x.end - (int)p.T + r / p.group;
-        lo[i][c] = p.window > 0 ? hi[i][c] - p.window + 1 : 0;
+          for (int s = 0; s < 8; ++s) sm.query[warp * 8 + s][lane] = make_uint2(qf[0][0][s][0], qf[0][0][s][1]);
+          if (qd == 0) sm.factor[warp * 8 + g] = down;
+        }
+        __syncthreads();   // (the join's last barrier is behind what used them before)
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          srow[i][c] = __shfl_sync(0xffffffffu, down, (2 * qd + c) * 4);
+          hi[i][c] = seen_to(8 * i + 2 * qd + c);
+          lo[i][c] = seen_from(hi[i][c]);
+        }
       }
     }
     // keys that every row of the tile sees need no mask
@@ -445,11 +473,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
         for (int c = 0; c < 4; ++c) o[i][t][c] = 0.f;
     // Base, kUp - base (0 for none), this lane's part of the sum; what an exponent may be before
     // the bases are looked at.
-    float m[NT][2], up[NT][2], l[NT][2], limit = -INFINITY;
+    float m[NT][2], ups[QT][2], l[NT][2], limit = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) m[i][c] = -INFINITY, up[i][c] = l[i][c] = 0.f;
+      for (int c = 0; c < 2; ++c) m[i][c] = -INFINITY, l[i][c] = 0.f;
+#pragma unroll
+    for (int i = 0; i < QT; ++i) ups[i][0] = ups[i][1] = 0.f;
+    auto up = [&](int i, int c) {
+      if constexpr (WIDE)
+        return m[i][c] == -INFINITY ? 0.f : kUp - m[i][c];
+      else
+        return ups[i][c];
+    };
 
 #pragma unroll 1
     for (; cu.k < cu.kend; cu.k += TEAMS) {
@@ -458,41 +494,80 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
       const uint32_t kb = ring + stage * kStageBytes, vb = kb + kHalf + kScales;
       // ---- scores: [product of 16 keys][tile]{key g, row 2 qd, + 1; key g + 8, the same rows}
       float s[kTiles][NT][4];
+      auto k_factors = [&](int h, uint32_t& sa, uint32_t& sc) {
+        sa = e4m3x2_to_half(lds2(kb + kHalf + (h * 16 + k_row) * 8 + 2 * qd));
+        sc = e4m3x2_to_half(lds2(kb + kHalf + (h * 16 + 8 + k_row) * 8 + 2 * qd));
+      };
+      // k16 steps 2 w, 2 w + 1
+      auto k_fragments = [&](int w, uint32_t wa, uint32_t wc, uint32_t sa, uint32_t sc, uint32_t (&a)[2][4]) {
+        const uint32_t fa = __byte_perm(sa, sa, w < 2 ? 0x1010 : 0x3232);
+        const uint32_t fc = __byte_perm(sc, sc, w < 2 ? 0x1010 : 0x3232);
+        a[0][0] = mul2(e2m1x2_to_half<0>(wa), fa);
+        a[0][1] = mul2(e2m1x2_to_half<0>(wc), fc);
+        a[0][2] = mul2(e2m1x2_to_half<1>(wa), fa);
+        a[0][3] = mul2(e2m1x2_to_half<1>(wc), fc);
+        a[1][0] = mul2(e2m1x2_to_half<2>(wa), fa);
+        a[1][1] = mul2(e2m1x2_to_half<2>(wc), fc);
+        a[1][2] = mul2(e2m1x2_to_half<3>(wa), fa);
+        a[1][3] = mul2(e2m1x2_to_half<3>(wc), fc);
+      };
+      if constexpr (WIDE) {
+        uint4 ka[kTiles], kc[kTiles];
+        uint32_t sa[kTiles], sc[kTiles];
 #pragma unroll
-      for (int h = 0; h < kTiles; ++h) {
-        float acc[NT][SETS][4];
+        for (int h = 0; h < kTiles; ++h) {
+          ka[h] = lds16(kb + h * 1024 + k_at);
+          kc[h] = lds16(kb + h * 1024 + 512 + k_at);
+          k_factors(h, sa[h], sc[h]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int b = 0; b < SETS; ++b) acc[i][b][0] = acc[i][b][1] = acc[i][b][2] = acc[i][b][3] = 0.f;
-        const uint4 ka = lds16(kb + h * 1024 + k_at), kc = lds16(kb + h * 1024 + 512 + k_at);
-        const uint32_t sa = e4m3x2_to_half(lds2(kb + kHalf + (h * 16 + k_row) * 8 + 2 * qd));
-        const uint32_t sc = e4m3x2_to_half(lds2(kb + kHalf + (h * 16 + 8 + k_row) * 8 + 2 * qd));
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t fa = __byte_perm(sa, sa, w < 2 ? 0x1010 : 0x3232);
-          const uint32_t fc = __byte_perm(sc, sc, w < 2 ? 0x1010 : 0x3232);
-          uint32_t a[2][4];
-          a[0][0] = mul2(e2m1x2_to_half<0>(wa[w]), fa);
-          a[0][1] = mul2(e2m1x2_to_half<0>(wc[w]), fc);
-          a[0][2] = mul2(e2m1x2_to_half<1>(wa[w]), fa);
-          a[0][3] = mul2(e2m1x2_to_half<1>(wc[w]), fc);
-          a[1][0] = mul2(e2m1x2_to_half<2>(wa[w]), fa);
-          a[1][1] = mul2(e2m1x2_to_half<2>(wc[w]), fc);
-          a[1][2] = mul2(e2m1x2_to_half<3>(wa[w]), fa);
-          a[1][3] = mul2(e2m1x2_to_half<3>(wc[w]), fc);
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-              for (int b = 0; b < SETS; ++b) mma(acc[i][b], a[c], qf[i][b][2 * w + c][0], qf[i][b][2 * w + c][1]);
+          for (int i = 0; i < NT; ++i) s[h][i][0] = s[h][i][1] = s[h][i][2] = s[h][i][3] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int w = 0; w < 4; ++w) {
+          uint2 qw[NT][2];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[h][i][c] = F32 ? acc[i][0][c] + acc[i][SETS - 1][c] : acc[i][0][c];
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) qw[i][c] = sm.query[i * 8 + 2 * w + c][lane];
+#pragma unroll
+          for (int h = 0; h < kTiles; ++h) {
+            uint32_t a[2][4];
+            k_fragments(w, reinterpret_cast<const uint32_t*>(&ka[h])[w], reinterpret_cast<const uint32_t*>(&kc[h])[w],
+                        sa[h], sc[h], a);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < NT; ++i) mma(s[h][i], a[c], qw[i][c].x, qw[i][c].y);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < kTiles; ++h) {
+          float acc[NT][SETS][4];
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int b = 0; b < SETS; ++b) acc[i][b][0] = acc[i][b][1] = acc[i][b][2] = acc[i][b][3] = 0.f;
+          const uint4 ka = lds16(kb + h * 1024 + k_at), kc = lds16(kb + h * 1024 + 512 + k_at);
+          uint32_t sa, sc;
+          k_factors(h, sa, sc);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a[2][4];
+            k_fragments(w, wa[w], wc[w], sa, sc, a);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int b = 0; b < SETS; ++b) mma(acc[i][b], a[c], qf[i][b][2 * w + c][0], qf[i][b][2 * w + c][1]);
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[h][i][c] = F32 ? acc[i][0][c] + acc[i][SETS - 1][c] : acc[i][0][c];
+        }
       }
       __syncwarp();
       copy_k(stage);
@@ -524,21 +599,37 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
       const bool masked = key0 < all_lo || key0 + kUnit - 1 > all_hi;
       // ---- scores become exponents over the base, up = kUp - base; hidden ones -infinity
 #pragma unroll
-      for (int h = 0; h < kTiles; ++h)
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[h][i][c] = fmaf(s[h][i][c], srow[i][c & 1], up[i][c & 1]);
-      if (masked) {
+      for (int i = 0; i < NT; ++i) {
+        float2 f;
+        if constexpr (WIDE)
+          f = *reinterpret_cast<const float2*>(&sm.factor[8 * i + 2 * qd]);
+        else
+          f = make_float2(srow[i][0], srow[i][1]);
+        const float u0 = up(i, 0), u1 = up(i, 1);
 #pragma unroll
         for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+          for (int c = 0; c < 4; ++c) s[h][i][c] = fmaf(s[h][i][c], c & 1 ? f.y : f.x, c & 1 ? u1 : u0);
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          int to[2], from[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if constexpr (WIDE)
+              to[c] = seen_to(8 * i + 2 * qd + c), from[c] = seen_from(to[c]);
+            else
+              to[c] = hi[i][c], from[c] = lo[i][c];
+          }
+#pragma unroll
+          for (int h = 0; h < kTiles; ++h)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int key = key0 + h * 16 + (c >> 1) * 8 + (int)k_row;
-              if (key < lo[i][c & 1] || key > hi[i][c & 1]) s[h][i][c] = -INFINITY;
+              if (key < from[c & 1] || key > to[c & 1]) s[h][i][c] = -INFINITY;
             }
+        }
       }
       if (scores && part == 0) {
 #pragma unroll
@@ -551,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 #pragma unroll
               for (int c = 0; c < 2; ++c)
                 *reinterpret_cast<float2*>(to + (h * 16 + c * 8) * p.row_pad) =
-                    make_float2(s[h][i][2 * c] - up[i][0], s[h][i][2 * c + 1] - up[i][1]);
+                    make_float2(s[h][i][2 * c] - up(i, 0), s[h][i][2 * c + 1] - up(i, 1));
           }
         }
       }
@@ -574,14 +665,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
             float mx = largest(i, c);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            mx = fmaxf(mx - up[i][c], m[i][c]);
+            mx = fmaxf(mx - up(i, c), m[i][c]);
             if (mx == -INFINITY) {   // nothing seen yet: the next unit asks again
               limit = -INFINITY;
               continue;
             }
-            const float a = exp2_fast(m[i][c] - mx), by = kUp - mx - up[i][c];
+            const float a = exp2_fast(m[i][c] - mx), by = kUp - mx - up(i, c);
             m[i][c] = mx;
-            up[i][c] = kUp - mx;
+            if constexpr (!WIDE) ups[i][c] = kUp - mx;
 #pragma unroll
             for (int h = 0; h < kTiles; ++h) {
               s[h][i][c] += by;
@@ -827,13 +918,13 @@ int launch(const Params<64>& all, const DecodeQ4Call& c) {
   static DeviceOnce once;
   const int rc = once.run(c.device, [] {
     return cudaFuncSetAttribute(decode_kernel<E, NW, NT, UNIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(Shared<UNIT>)) == cudaSuccess ? kOk : kErrLaunch;
+                                (int)sizeof(Shared<UNIT, NT, kWide<E, NW, NT>>)) == cudaSuccess ? kOk : kErrLaunch;
   });
   if (rc != kOk) return rc;
   const Kernels<P> k = {decode_kernel<E, NW, NT, UNIT>,
                         p.fused ? join_kernel<P, E, NW, 8 * NT, 8, true> : join_kernel<P, E, NW, 8 * NT, 8>,
                         p.fused ? join_kernel<P, E, NW, 8 * NT, 1, true> : join_kernel<P, E, NW, 8 * NT, 1>,
-                        8 * NT, NW, kBlocksPerSm, sizeof(Shared<UNIT>)};
+                        8 * NT, NW, kBlocksPerSm, sizeof(Shared<UNIT, NT, kWide<E, NW, NT>>)};
   const int r = launch_list(k, p, c.span.B, c.num_sms, c.stream);
   return r != kOk || !c.weights || p.fused ? r : launch_weights(p, c.span.B * p.Hkv, c.stream);
 }
@@ -846,7 +937,7 @@ struct Layout {
 };
 Layout layout(int64_t heads, int rows, int D, int dtype, int64_t cap, bool weights, int num_sms) {
   Layout w = {};
-  const int rm = rows <= 8 ? 8 : 16;   // most rows of a tile
+  const int rm = rows <= 8 ? 8 : rows > 16 && rows <= 24 && D == 128 && dtype == PFA_BF16 ? 24 : 16;   // most of a tile
   const size_t parts = 2 * (size_t)num_sms * kBlocksPerSm * (rm * D + rm * 2) * sizeof(float);
   w.sums = (parts + 255) & ~(size_t)255;
   w.scores = w.total = w.sums;
@@ -895,11 +986,14 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   p.lanes = quads <= 1 ? 1 : quads <= 3 ? 2 : quads % 8 == 0 || quads >= 24 ? 8 : 4;
   // With tiles of 16 rows a converted code serves two products; with 8 there are twice as many units
   // to spread, and less code to fetch.  16 rows, bf16 (us, tiles of 8 / of 16):
-  //   one sequence, 32/8 heads of 128, 512 / 4096 / 16384 keys     7.0 / 8.5   8.3 / 10.1   13.2 / 13.2
-  //   16 sequences of 512 / 2048 keys                              11.2 / 12.7   19.9 / 19.6
-  //   one sequence of 131072 keys                                  51.0 / 43.4
-  //   8/2 heads of 512, 16 sequences of 2048, 4 of 32768 keys      26.3 / 31.6   65.9 / 53.7
+  //   one sequence, 32/8 heads of 128, 1024 / 4096 / 16384 / 32768 keys   7.4 / 8.4   8.5 / 9.7   13.2 / 12.3   18.0 / 16.7
+  //   16 sequences of 512 / 2048 keys                                     11.4 / 12.2   20.0 / 18.2
+  //   8/2 heads of 512, 16 sequences of 2048, 4 of 32768 keys             26.3 / 31.6   65.9 / 53.7
   // fp32: 9.5 / 11.9 at 4096 keys, 23.2 / 23.8 at 32768, 8 sequences of 8192 keys 43.8 / 38.9.
+  // 17 to 24 rows are one tile of 24 in place of two of 16 (24 rows, of 16 / of 24): one sequence, 32/8 heads,
+  // 16384 / 63488 keys 16.4 / 15.1, 37.7 / 30.4, 16 of 2048 26.0 / 22.8; 8/1 heads, 131072 keys 19.3 / 20.0.  Two
+  // or more such tiles are no faster than their rows in tiles of 16 (48 rows, 63488 keys 52.1 / 52.0), and
+  // one of 32 spills (47 for 32 rows, 38 with two of 16).
   const int64_t rows = c.span.lengths ? p.cap : c.span.start_pos + p.T;   // most that a sequence can have
   const int64_t keys = p.window > 0 ? std::min<int64_t>(rows, p.window + p.T) : rows;
   const int64_t units = heads * ((p.rows + 7) / 8) * (keys / 64 + 1);
@@ -911,7 +1005,8 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   const bool small = units < (int64_t)2 * c.num_sms * kBlocksPerSm;
   if (c.dtype == PFA_BF16) {
     if (c.D == 128)
-      return !few ? launch<__nv_bfloat16, 1, 2, 64>(p, c)
+      return !few ? (p.rows > 16 && p.rows <= 24 ? launch<__nv_bfloat16, 1, 3, 32>(p, c)
+                                                 : launch<__nv_bfloat16, 1, 2, 64>(p, c))
              : small ? launch<__nv_bfloat16, 1, 1, 32>(p, c) : launch<__nv_bfloat16, 1, 1, 64>(p, c);
     return !few ? launch<__nv_bfloat16, 4, 2, 64>(p, c)
            : small ? launch<__nv_bfloat16, 4, 1, 32>(p, c) : launch<__nv_bfloat16, 4, 1, 64>(p, c);

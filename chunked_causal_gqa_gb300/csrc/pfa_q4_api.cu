@@ -72,15 +72,15 @@ struct PrefillPlan {
   Call call;              // on the read-back rows
 };
 
-// Which is faster.  The decode kernel takes some 9 us and, at head_dim 128, 1.86e-6 us for each row, kv
+// Which is faster.  The decode kernel takes some 9 us and, at head_dim 128, 1.74e-6 us for each row, kv
 // head and key; the other reads the cache back (656 bytes a key and kv head) and walks the keys with
 // 128-row tiles, about 13 us and (0.1e-3 Hkv + 0.6e-3) us a key.  Measured on GB300 (us, decode / read back):
-//   8 kv heads, rows                     96 / 128 / 192 / 384
-//     1024 keys        10.3 / 15.9   12.4 / 15.9   12.7 / 16.3   18.8 / 16.9
-//     16384 keys       35.7 / 43.2   41.1 / 43.1   58.7 / 43.4
-//     63488 keys      101.9 / 113   131.9 / 113
-//   2 kv heads, 63488 keys, rows 128 / 192 / 256    40 / 65   55 / 66   72 / 66
-//   1 kv head, 63488 keys, rows 256 / 384 / 512     40 / 88   56 / 58   72 / 59
+//   8 kv heads, rows                     96 / 112 / 128 / 192 / 384
+//     1024 keys         9.7 / 15.9                11.6 / 15.9   12.9 / 16.3   17.5 / 16.9
+//     16384 keys       33.7 / 43.2   36.7 / 43    38.5 / 43.1   54.8 / 43.4
+//     63488 keys       95.5 / 113    111 / 113    123 / 113
+//   2 kv heads, 63488 keys, rows 128 / 192 / 256    37 / 65   51 / 66   67 / 66
+//   1 kv head, 63488 keys, rows 256 / 384 / 512     38 / 88   52 / 58   66 / 59
 // head_dim 512: 9.6e-6 us for each row, kv head and key against 13e-3 us a key in each wave of the other's tiles
 //   2 kv heads, 16384 keys, rows 128 / 512   55 / 222   178 / 223
 // fp32 always runs the decode kernel: the bf16 parts of the fp32 kernel would leave some 6e-5 of the
@@ -88,7 +88,7 @@ struct PrefillPlan {
 bool prefill_by_decode(int64_t T, int64_t keys, int H, int Hkv, int D, int dtype, int num_sms) {
   if (dtype == PFA_F32) return true;
   const int64_t rows = T * (H / Hkv);
-  if (D == 128) return rows * Hkv <= 2000000 / keys + 52 * Hkv + 323;
+  if (D == 128) return rows * Hkv <= 2300000 / keys + 57 * Hkv + 345;
   const int64_t blocks = (rows + 255) / 256 * 4 * Hkv;
   return rows * Hkv <= 1300 * ((blocks + num_sms - 1) / num_sms);
 }

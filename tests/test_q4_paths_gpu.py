@@ -124,3 +124,36 @@ def test_graphs_that_share_a_workspace(dt):
             torch.cuda.synchronize()
             assert torch.equal(out, want) and torch.equal(w, acc)
     ok()
+
+
+MANY = [  # T, H, Hkv, D, window, dtype: 40 sequences, enough units for the larger tiles
+    (2, 30, 6, 128, 0, BF16),      # 10 rows
+    (4, 32, 8, 128, 0, BF16),      # 16
+    (4, 32, 8, 128, 70, BF16),
+    (17, 6, 6, 128, 0, BF16),      # 17
+    (5, 32, 8, 128, 0, BF16),      # 20
+    (3, 64, 8, 128, 33, BF16),     # 24
+    (5, 25, 5, 128, 0, BF16),      # 25
+    (12, 32, 8, 128, 0, BF16),     # 48
+    (11, 30, 6, 128, 100, BF16),   # 55
+    (4, 32, 8, 128, 0, F32),
+    (5, 32, 8, 128, 65, F32),
+    (3, 30, 6, 512, 0, BF16),
+    (2, 60, 6, 512, 60, F32),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=str)
+@pytest.mark.parametrize("with_weights", [False, True])
+def test_many_rows_and_sequences(case, with_weights):
+    T, H, Hkv, D, window, dt = case
+    lens, cap = [1000, 999, 1, 0, 64, 333, 17, 2, 512, 961] * 4, 1000
+    full = (lens, T, H, Hkv, D, window, cap, dt)
+    cache, q, k, v = attention_case(full, 61, (2, -3))
+    w0 = torch.rand(len(lens), Hkv, cap, device=G.dev()) if with_weights else None
+    w = w0.clone() if with_weights else None
+    out = pkg.decode_attention_q4(q, cache, lengths(lens), weights=w, window=window)
+    check_attention(out, w, w0, q, k, v, full)
+    again = pkg.decode_attention_q4(q, cache, lengths(lens), weights=None if w0 is None else w0.clone(), window=window)
+    assert torch.equal(out, again)
+    ok()
