@@ -665,6 +665,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
             float mx = largest(i, c);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            // (a row's own scores alone raise its base: its result does not depend on its tile's others)
+            if (m[i][c] != -INFINITY && !(mx > kUp + kLag)) continue;
             mx = fmaxf(mx - up(i, c), m[i][c]);
             if (mx == -INFINITY) {   // nothing seen yet: the next unit asks again
               limit = -INFINITY;

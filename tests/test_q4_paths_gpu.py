@@ -157,3 +157,28 @@ def test_many_rows_and_sequences(case, with_weights):
     again = pkg.decode_attention_q4(q, cache, lengths(lens), weights=None if w0 is None else w0.clone(), window=window)
     assert torch.equal(out, again)
     ok()
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_many_rows_one_of_them_not_finite(what):
+    """A row of a tile that is not finite leaves the tile's others right, and keys that are not finite leave
+    those right that do not see them."""
+    lens, cap, T, H, Hkv, D = [1000, 700] * 20, 1000, 6, 32, 8, 128
+    full = (lens, T, H, Hkv, D, 0, cap, BF16)
+    cache, q, k, v = attention_case(full, 71)
+    n = lengths(lens)
+    good = pkg.decode_attention_q4(q, cache, n)
+    bad = q.clone()
+    bad[3, 2, 5, 7] = what
+    out = pkg.decode_attention_q4(bad, cache, n)
+    assert out[3, 2, 5].isnan().all()
+    rest = torch.ones(q.shape[:3], dtype=torch.bool, device=G.dev())
+    rest[3, 2, 5] = False
+    assert torch.equal(out[rest], good[rest])
+    cache.k_scale.view(torch.uint8)[4, 1, 999, 0] = 0x7f       # the last token's own key
+    out = pkg.decode_attention_q4(q, cache, n)
+    assert out[4, 5, 4:8].isnan().all()
+    rest = torch.ones(q.shape[:3], dtype=torch.bool, device=G.dev())
+    rest[4, 5, 4:8] = False
+    assert not out[rest].isnan().any() and torch.equal(out[rest], good[rest])
+    ok()
