@@ -33,18 +33,19 @@
 // its own ring of 128 keys filled by cp.async; head_dim 512: four warps share a unit, each with 128
 // channels, and exchange partial scores.  Two blocks an SM: the unit's 64 keys want the registers.
 //
-// Accumulated weights: the scores go to the workspace as they are made (4 bytes a row and key beside
-// the 144 of the cache); the join leaves each row's maximum and sum, and 2^(s - m) / l, added up over
-// the rows of a key, follows beside the join or in a kernel behind it.  (Making the scores again would
-// read K again: 72 bytes a key, where 16 are written and 16 read for four rows.)
+// Accumulated weights: the join leaves each row's maximum and sum, and 2^(s - m) / l, added up over
+// the rows of a key, follows beside the join or in a kernel behind it.  With few rows the scores go to the
+// workspace as they are made (4 bytes a row and key beside the 144 of the cache; making them again would
+// read K again, 72 bytes a key, where 16 are written and 16 read for four rows); with many they are made
+// again (scores_again).
 //
 // Measured on GB300, all kernels of a call, one pass among others:
 //   1 sequence of 131072 keys, 32/8 heads of 128, bf16 (151 MB)      32.1 us (floor 22.2): streaming at
 //     7.1 TB/s (each further sequence takes 21.3 us), and 9 us of start, uneven ends and join
 //   32 sequences up to 8192 keys with weights (144 MB)               39.9 us (floor 21.2): the same, 8 us
 //     of which are the scores, written and read, and the third launch
-//   32 tokens at 16384 keys with weights                             69 us (floor 4.4): eight tiles of rows
-//     convert the codes anew, 44 us; 67 MB of scores, written and read, the rest
+//   32 tokens at 16384 keys with weights                             57 us (floor 4.4): eight tiles of rows
+//     convert the codes anew, 38 us; the weights 16
 //   4 sequences, 3 tokens, window 1024, 8/2 heads of 512, fp32       12.1 us: two launches and some ten
 //     latencies (floor 0.6)
 // Steps (the first two cases): units of 32 keys, three blocks an SM, each copy with its own addresses
@@ -60,6 +61,7 @@
 #include "../../include/pfa.h"
 
 #include <cmath>
+#include <type_traits>
 
 namespace pfa {
 namespace {
@@ -224,6 +226,25 @@ __device__ __forceinline__ uint32_t lds1(uint32_t a) {
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// K's fragments of the k16 steps 2 w, 2 w + 1: words w of the two keys' 32 channels, their two scales each.
+__device__ __forceinline__ void k_fragments(int w, uint32_t wa, uint32_t wc, uint32_t sa, uint32_t sc,
+                                            uint32_t (&a)[4], uint32_t (&b)[4]) {
+  const uint32_t fa = __byte_perm(sa, sa, w < 2 ? 0x1010 : 0x3232);
+  const uint32_t fc = __byte_perm(sc, sc, w < 2 ? 0x1010 : 0x3232);
+  a[0] = mul2(e2m1x2_to_half<0>(wa), fa);
+  a[1] = mul2(e2m1x2_to_half<0>(wc), fc);
+  a[2] = mul2(e2m1x2_to_half<1>(wa), fa);
+  a[3] = mul2(e2m1x2_to_half<1>(wc), fc);
+  b[0] = mul2(e2m1x2_to_half<2>(wa), fa);
+  b[1] = mul2(e2m1x2_to_half<2>(wc), fc);
+  b[2] = mul2(e2m1x2_to_half<3>(wa), fa);
+  b[3] = mul2(e2m1x2_to_half<3>(wc), fc);
+}
+// The power of two that brings a row with this largest element to 2^13 .. 2^14.
+__device__ __forceinline__ int row_exponent(float amax) {
+  if (amax == 0.f || !(amax <= 3.402823466e38f)) return 0;
+  return min(13 + 127 - (int)(__float_as_uint(amax) >> 23), 120);
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   uint32_t b;
@@ -427,11 +448,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 #pragma unroll
         for (int w = 0; w < NW; ++w) amax = fmaxf(amax, sm.ml[team * NW + w][g + 8 * i].x);
       }
-      int ex = 13 + 127 - (int)(__float_as_uint(amax) >> 23);
-      if (amax == 0.f || !(amax <= 3.402823466e38f)) ex = 0;
-      ex = min(ex, 120);
-      const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
-      const float down = __uint_as_float((uint32_t)(127 - ex) << 23) * p.scale_log2;
+      const int ex = row_exponent(amax);
+      const float up = pow2(ex), down = pow2(-ex) * p.scale_log2;
 #pragma unroll
       for (int s = 0; s < 8; ++s)
 #pragma unroll
@@ -498,19 +516,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
         sa = e4m3x2_to_half(lds2(kb + kHalf + (h * 16 + k_row) * 8 + 2 * qd));
         sc = e4m3x2_to_half(lds2(kb + kHalf + (h * 16 + 8 + k_row) * 8 + 2 * qd));
       };
-      // k16 steps 2 w, 2 w + 1
-      auto k_fragments = [&](int w, uint32_t wa, uint32_t wc, uint32_t sa, uint32_t sc, uint32_t (&a)[2][4]) {
-        const uint32_t fa = __byte_perm(sa, sa, w < 2 ? 0x1010 : 0x3232);
-        const uint32_t fc = __byte_perm(sc, sc, w < 2 ? 0x1010 : 0x3232);
-        a[0][0] = mul2(e2m1x2_to_half<0>(wa), fa);
-        a[0][1] = mul2(e2m1x2_to_half<0>(wc), fc);
-        a[0][2] = mul2(e2m1x2_to_half<1>(wa), fa);
-        a[0][3] = mul2(e2m1x2_to_half<1>(wc), fc);
-        a[1][0] = mul2(e2m1x2_to_half<2>(wa), fa);
-        a[1][1] = mul2(e2m1x2_to_half<2>(wc), fc);
-        a[1][2] = mul2(e2m1x2_to_half<3>(wa), fa);
-        a[1][3] = mul2(e2m1x2_to_half<3>(wc), fc);
-      };
       if constexpr (WIDE) {
         uint4 ka[kTiles], kc[kTiles];
         uint32_t sa[kTiles], sc[kTiles];
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
           for (int h = 0; h < kTiles; ++h) {
             uint32_t a[2][4];
             k_fragments(w, reinterpret_cast<const uint32_t*>(&ka[h])[w], reinterpret_cast<const uint32_t*>(&kc[h])[w],
-                        sa[h], sc[h], a);
+                        sa[h], sc[h], a[0], a[1]);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_kernel(const Pa
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t a[2][4];
-            k_fragments(w, wa[w], wc[w], sa, sc, a);
+            k_fragments(w, wa[w], wc[w], sa, sc, a[0], a[1]);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -906,6 +911,184 @@ int launch_weights(Scores p, int64_t heads, cudaStream_t stream) {
   return kErrLaunch;
 }
 
+// Weights behind the join without stored scores: a warp converts 32 keys once and makes their scores with all
+// rows again, 128 rows at a time, whose second operands the block's warps share; each lane has the sums of
+// four keys over a quarter of the rows.  128 rows at 16384 keys: 16 us, where storing and reading 67 MB of
+// scores took 25; 43 % of the tensor pipe, the rest the exponentials beside it and the start.  (Three blocks an SM
+// 55.9 us for the whole call, two 54.0; four products at once 54.5.)
+constexpr int kAgainRows = 128, kAgainBlocks = 2;
+
+__global__ void __launch_bounds__(kThreads, kAgainBlocks) weights_again_kernel(const Params<64> p) {
+  __shared__ uint2 s_query[kAgainRows / 8][8][32];   // [product][k16 step][lane]
+  __shared__ float2 s_factor[kAgainRows / 2], s_minus[kAgainRows / 2], s_inv[kAgainRows / 2];   // two rows each
+  __shared__ int2 s_pos[kAgainRows / 2];
+  constexpr int D = 128;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x - bh * (int)p.chunks.by;
+  const int b = bh / p.heads, h = bh - b * p.Hkv;
+  // (what the first kernel reads may be read before the wait, past this SM's own cache)
+  const int64_t len = __ldcg((const long long*)p.lengths + b);
+  const int end = len < 0 || len > p.cap ? 0 : (int)len, first = end - (int)p.T;
+  const int lo = p.window > 0 ? max(0, max(first, 0) - p.window + 1) : 0;
+  const int steps = (int)(((int64_t)end - lo + kThreads - 1) / kThreads);   // a key a thread
+  if (chunk >= steps) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const uint8_t* const codes = p.k4 + (int64_t)bh * p.cap * (D / 2) + qd * 16;
+  const uint8_t* const scales = p.k_scale + (int64_t)bh * p.cap * (D / 16) + qd * 2;
+  float* const weights = p.weights + (int64_t)bh * p.cap;
+  const int k_row = key_at(g);
+  uint4 w[4];          // keys k_row, + 8, + 16, + 24: 32 channels each
+  uint32_t scale[4];   // and their two scales
+  auto load = [&](int step) {
+    const int64_t key0 = lo + (int64_t)step * kThreads + warp * 32 + k_row;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool on = key0 + 8 * i < end;
+      w[i] = on ? __ldcg(reinterpret_cast<const uint4*>(codes + (key0 + 8 * i) * (D / 2))) : make_uint4(0, 0, 0, 0);
+      scale[i] = on ? __ldcg(reinterpret_cast<const unsigned short*>(scales + (key0 + 8 * i) * (D / 16))) : 0u;
+    }
+  };
+#pragma unroll 1
+  for (int r0 = 0; r0 < p.rows; r0 += kAgainRows) {
+    const int nr = min(kAgainRows, p.rows - r0), products = (nr + 7) / 8;
+    if (r0 > 0) __syncthreads();   // the rows before are done with
+    load(chunk);
+    uint4 x[kAgainRows / 8 / kWarps][4];   // this warp's rows, all asked for at once
+#pragma unroll
+    for (int n = 0; n < kAgainRows / 8 / kWarps; ++n) {
+      const int i = warp + kWarps * n;
+      if (i >= products) break;
+      const int r = r0 + min(8 * i + g, nr - 1), t = r / p.group;
+      const uint4* row = reinterpret_cast<const uint4*>(
+          (const __nv_bfloat16*)p.q + (b * p.T + t) * p.q_row +
+          (int64_t)(h * (int)p.group.by + r - t * (int)p.group.by) * D + qd * 32);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[n][j] = __ldcg(row + j);
+    }
+#pragma unroll
+    for (int n = 0; n < kAgainRows / 8 / kWarps; ++n) {
+      const int i = warp + kWarps * n;
+      if (i >= products) break;
+      const uint32_t* const u = reinterpret_cast<const uint32_t*>(x[n]);
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xffff0000u))));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int ex = row_exponent(amax);
+      const float up = pow2(ex);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        uint32_t f[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          f[c] = half2_of(__uint_as_float(u[2 * s + c] << 16) * up, __uint_as_float(u[2 * s + c] & 0xffff0000u) * up);
+        s_query[i][s][lane] = make_uint2(f[0], f[1]);
+      }
+      if (qd == 0) reinterpret_cast<float*>(s_factor)[8 * i + g] = pow2(-ex) * p.scale_log2;
+    }
+    if (r0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = tid; i < 8 * products; i += kThreads) {
+      const int r = r0 + min(i, nr - 1), pos = first + r / p.group;
+      // (rows at negative positions may have no sums)
+      const float2 ml = pos >= 0 ? p.sums[(int64_t)bh * p.rows + r] : make_float2(0.f, 0.f);
+      reinterpret_cast<float*>(s_minus)[i] = -ml.x;
+      reinterpret_cast<float*>(s_inv)[i] = i < nr ? ml.y : 0.f;
+      reinterpret_cast<int*>(s_pos)[i] = pos;
+    }
+    __syncthreads();
+    const int all_hi = first + r0 / p.group;   // keys that every row sees: up to here, and from
+    const int all_lo = p.window > 0 ? first + (r0 + nr - 1) / p.group - p.window + 1 : 0;
+#pragma unroll 1
+    for (int step = chunk; step < steps; step += (int)p.chunks.by) {
+      const int64_t key0 = lo + (int64_t)step * kThreads + warp * 32;
+      uint32_t a[2][8][4];   // keys 16 h .. + 15
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t sa = e4m3x2_to_half(scale[2 * i]), sc = e4m3x2_to_half(scale[2 * i + 1]);
+        const uint32_t wa[4] = {w[2 * i].x, w[2 * i].y, w[2 * i].z, w[2 * i].w};
+        const uint32_t wc[4] = {w[2 * i + 1].x, w[2 * i + 1].y, w[2 * i + 1].z, w[2 * i + 1].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k_fragments(j, wa[j], wc[j], sa, sc, a[i][2 * j], a[i][2 * j + 1]);
+      }
+      if (step + (int)p.chunks.by < steps) load(step + (int)p.chunks.by);
+      if (key0 >= end) continue;
+      const int64_t mine = key0 + k_row + 8 * qd;   // (four lanes have the same sums)
+      const float was = mine < end ? weights[mine] : 0.f;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};   // keys k_row, + 8, + 16, + 24
+      // N products at once, N * 2 chains of eight
+      auto add = [&](int i, auto count, auto masked) {
+        constexpr int N = decltype(count)::value;
+        float acc[N][2][4] = {};
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            const uint2 q = s_query[i + n][s][lane];
+            mma(acc[n][0], a[0][s], q.x, q.y);
+            mma(acc[n][1], a[1][s], q.x, q.y);
+          }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const int at = 4 * (i + n) + qd;
+          const float2 f = s_factor[at], minus = s_minus[at], inv = s_inv[at];
+          int2 pos;
+          if constexpr (decltype(masked)::value) pos = s_pos[at];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if constexpr (decltype(masked)::value) {
+              const int64_t key = key0 + k_row + 8 * (j / 2);
+              const int to = j % 2 ? pos.y : pos.x;
+              if (key > to || (p.window > 0 && key <= to - p.window)) continue;
+            }
+            sum[j / 2] = fmaf(exp2_fast(fmaf(acc[n][j / 4][j % 4], j % 2 ? f.y : f.x, j % 2 ? minus.y : minus.x)),
+                              j % 2 ? inv.y : inv.x, sum[j / 2]);
+          }
+        }
+      };
+      int i = 0;
+      if (key0 < all_lo || key0 + 31 > all_hi) {
+#pragma unroll 1
+        for (; i < products; ++i) add(i, std::integral_constant<int, 1>(), std::true_type());
+      } else {
+#pragma unroll 1
+        for (; i + 2 <= products; i += 2) add(i, std::integral_constant<int, 2>(), std::false_type());
+        if (i < products) add(i, std::integral_constant<int, 1>(), std::false_type());
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
+        sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+      }
+      if (mine < end) weights[mine] = was + (qd & 2 ? (qd & 1 ? sum[3] : sum[2]) : qd & 1 ? sum[1] : sum[0]);
+    }
+  }
+}
+
+int launch_weights_again(Params<64> p, int64_t heads, int num_sms, cudaStream_t stream) {
+  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.cap, p.window + p.T) : p.cap;
+  const int64_t slots = ((int64_t)num_sms * kAgainBlocks + heads - 1) / heads;   // of a head, at once
+  p.chunks = divisor((uint32_t)std::min<int64_t>((keys + kThreads - 1) / kThreads, slots));
+  p.heads = divisor(p.Hkv);
+  if (heads * p.chunks.by > 0x7fffffff) return kErrShape;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(heads * p.chunks.by));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, weights_again_kernel, p) == cudaSuccess) return kOk;
+  cudaGetLastError();
+  return kErrLaunch;
+}
+
 template <typename E, int NW, int NT, int UNIT>
 int launch(const Params<64>& all, const DecodeQ4Call& c) {
   using P = Params<UNIT>;
@@ -914,7 +1097,7 @@ int launch(const Params<64>& all, const DecodeQ4Call& c) {
   // Beside the join the weights save a launch, but each of their blocks finds its head's sums for
   // itself (us, beside / behind): 16 sequences of 1024 keys, 32/8 heads 13.8 / 15.4, one of 16384 12.9 / 14.0, of
   // 131072 42.8 / 41.2; 32 of up to 8192 42.2 / 38.9.
-  p.fused = c.weights && p.rows <= 8 * NT &&
+  p.fused = p.scores && p.rows <= 8 * NT &&
             c.span.B * p.Hkv * chunks_of(p, kWeightThreads).by <= (int64_t)2 * c.num_sms;
   p.k4 = all.k4; p.v4 = all.v4; p.k_scale = all.k_scale; p.v_scale = all.v_scale;
   static DeviceOnce once;
@@ -928,10 +1111,21 @@ int launch(const Params<64>& all, const DecodeQ4Call& c) {
                         p.fused ? join_kernel<P, E, NW, 8 * NT, 1, true> : join_kernel<P, E, NW, 8 * NT, 1>,
                         8 * NT, NW, kBlocksPerSm, sizeof(Shared<UNIT, NT, kWide<E, NW, NT>>)};
   const int r = launch_list(k, p, c.span.B, c.num_sms, c.stream);
-  return r != kOk || !c.weights || p.fused ? r : launch_weights(p, c.span.B * p.Hkv, c.stream);
+  if (r != kOk || !c.weights || p.fused) return r;
+  return p.scores ? launch_weights(p, c.span.B * p.Hkv, c.stream)
+                  : launch_weights_again(all, c.span.B * p.Hkv, c.num_sms, c.stream);
 }
 
-// Workspace: partial sums, two slots a run; with weights each row's sums and each score.
+// Whether accumulated weights come from scores that are made again, not stored: for many rows, as K's codes
+// are converted once for all of them, and for few heads, whose blocks then have few keys each and wait little.
+// bf16, head_dim 128 (us, again / stored): one sequence of 8 kv heads, 16384 keys, 16 / 24 / 32 / 128 rows
+// 17.0 / 18.0, 20.6 / 23.4, 22.4 / 25.7, 54 / 63, 8 rows 14.6 / 14.0; 63488 keys, 32 / 256 rows 54 / 66, 325 / 384;
+// 16 sequences of 2048 keys, 16 / 24 / 32 / 128 rows 29 / 27, 36 / 34, 41 / 42, 124 / 137.
+bool scores_again(int64_t heads, int rows, int D, int dtype) {
+  return D == 128 && dtype == PFA_BF16 && (rows > 24 || (rows > 8 && heads <= 16));
+}
+
+// Workspace: partial sums, two slots a run; with weights each row's sums and each score, where scores are stored.
 struct Layout {
   size_t sums, scores, total;
   int64_t score_head;
@@ -944,9 +1138,11 @@ Layout layout(int64_t heads, int rows, int D, int dtype, int64_t cap, bool weigh
   w.sums = (parts + 255) & ~(size_t)255;
   w.scores = w.total = w.sums;
   if (!weights) return w;
+  w.scores += ((size_t)heads * rows * sizeof(float2) + 255) & ~(size_t)255;
+  w.total = w.scores;
+  if (scores_again(heads, rows, D, dtype)) return w;
   w.row_pad = (rows + 3) & ~3;
   w.score_head = (cap + 63) / 64 * 64 * w.row_pad;
-  w.scores += ((size_t)heads * rows * sizeof(float2) + 255) & ~(size_t)255;
   w.total = w.scores + (((size_t)heads * w.score_head * sizeof(float) + 255) & ~(size_t)255);
   return w;
 }
@@ -979,7 +1175,7 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   char* ws = static_cast<char*>(c.ws);
   p.parts = reinterpret_cast<float*>(ws);
   p.sums = c.weights ? reinterpret_cast<float2*>(ws + w.sums) : nullptr;
-  p.scores = c.weights ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
+  p.scores = w.score_head > 0 ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
   p.score_head = w.score_head;
   p.row_pad = w.row_pad;
   p.weights = c.weights;

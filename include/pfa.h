@@ -602,8 +602,9 @@ PFA_API int pfa_cache_read_q4(const void *k4, const void *v4, const void *k_scal
  *             softmax weights, summed over the call's tokens and the query heads of the kv
  *             head, are added to it in place.  Rows that no token sees are not touched.
  *             A key's total is what pfa_cache_evict_q4 goes by.
- *   workspace of pfa_decode_workspace_bytes_q4 bytes: with weights it holds each score
- *             (4 bytes for each row of the T * num_heads / num_kv_heads and cache row).
+ *   workspace of pfa_decode_workspace_bytes_q4 bytes: with weights it can hold each score
+ *             (4 bytes for each row of the T * num_heads / num_kv_heads and cache row; for bf16 at
+ *             head_dim 128 not for more than 24 rows, nor for more than 8 of at most 16 heads in all).
  * Weights of the sum over V are rounded to 11 bits (bf16) or 21 (fp32), small ones to 2^-36 of the
  * row's largest; the accumulated ones are not rounded below fp32.  Two calls that add to the
  * same weights must not run at the same time.

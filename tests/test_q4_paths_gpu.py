@@ -182,3 +182,49 @@ def test_many_rows_one_of_them_not_finite(what):
     rest[4, 5, 4:8] = False
     assert not out[rest].isnan().any() and torch.equal(out[rest], good[rest])
     ok()
+
+
+AGAIN = [  # lens, T, H, Hkv, window: few heads, or many rows
+    ([3001], 3, 8, 2, 0),              # 12 rows
+    ([3001, 64], 9, 8, 8, 70),         # 9
+    ([3001, 1, 0, 7], 16, 4, 4, 0),    # 16
+    ([3001, 129], 16, 16, 2, 0),       # 128
+    ([3001, 129], 43, 6, 2, 0),        # 129
+    ([300, 5, 260], 100, 20, 2, 33),   # 1000
+    ([2000] * 12, 26, 8, 8, 0),        # 26 rows of many heads
+    ([32, 33], 32, 8, 2, 0),           # chunks that are all or nearly all of a sequence
+]
+
+
+@pytest.mark.parametrize("case", AGAIN, ids=lambda c: f"B{len(c[0])}x{c[0][0]}-T{c[1]}-{c[2]}/{c[3]}-w{c[4]}")
+def test_weights_without_stored_scores(case):
+    lens, T, H, Hkv, window = case
+    cap, rows = max(lens) + 2, T * H // Hkv
+    extra = (pkg.decode_workspace_bytes_q4(len(lens), T, H, Hkv, 128, cap, weights=True) -
+             pkg.decode_workspace_bytes_q4(len(lens), T, H, Hkv, 128, cap))
+    assert extra < len(lens) * Hkv * rows * 8 + 512               # the rows' sums, no scores
+    full = (lens, T, H, Hkv, 128, window, cap, BF16)
+    cache, q, k, v = attention_case(full, 81, (3, -1))
+    w0 = torch.rand(len(lens), Hkv, cap, device=G.dev())
+    w = w0.clone()
+    out = pkg.decode_attention_q4(q, cache, lengths(lens), weights=w, window=window)
+    check_attention(out, w, w0, q, k, v, full)
+    assert torch.equal(out, pkg.decode_attention_q4(q, cache, lengths(lens), window=window))
+    again = w0.clone()
+    pkg.decode_attention_q4(q, cache, lengths(lens), weights=again, window=window)
+    assert torch.equal(w, again)
+    ok()
+
+
+def test_weights_without_stored_scores_report_lengths():
+    case = ([700, 701, 700], 10, 8, 2, 128, 0, 700, BF16)
+    cache, q, k, v = attention_case(([700, 700, 700], *case[1:]), 91)
+    w = torch.zeros(3, 2, 700, device=G.dev())
+    out = torch.full_like(q, 3.0)
+    pkg.decode_attention_q4(q, cache, lengths(case[0]), out, weights=w)
+    ok(-11)
+    for b in (0, 2):
+        want, tol, acc, acc_tol = R.attention(q[b], k[b], v[b], 700, 0, R8.default_scale(128), BF16)
+        within(out[b], want, tol)
+        within(w[b], acc, acc_tol + 2.0 ** -24 * acc)
+    assert (out[1] == 3).all() and not w[1].any()
