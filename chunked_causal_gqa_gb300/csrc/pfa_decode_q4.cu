@@ -44,7 +44,7 @@
 //     7.1 TB/s (each further sequence takes 21.3 us), and 9 us of start, uneven ends and join
 //   32 sequences up to 8192 keys with weights (144 MB)               39.9 us (floor 21.2): the same, 8 us
 //     of which are the scores, written and read, and the third launch
-//   32 tokens at 16384 keys with weights                             57 us (floor 4.4): eight tiles of rows
+//   32 tokens at 16384 keys with weights                             56 us (floor 4.4): eight tiles of rows
 //     convert the codes anew, 38 us; the weights 16
 //   4 sequences, 3 tokens, window 1024, 8/2 heads of 512, fp32       12.1 us: two launches and some ten
 //     latencies (floor 0.6)
@@ -914,7 +914,7 @@ int launch_weights(Scores p, int64_t heads, cudaStream_t stream) {
 // Weights behind the join without stored scores: a warp converts 32 keys once and makes their scores with all
 // rows again, 128 rows at a time, whose second operands the block's warps share; each lane has the sums of
 // four keys over a quarter of the rows.  128 rows at 16384 keys: 16 us, where storing and reading 67 MB of
-// scores took 25; 43 % of the tensor pipe, the rest the exponentials beside it and the start.  (Three blocks an SM
+// scores took 25; 49 % of the tensor pipe, the rest the exponentials beside it and the start.  (Three blocks an SM
 // 55.9 us for the whole call, two 54.0; four products at once 54.5.)
 constexpr int kAgainRows = 128, kAgainBlocks = 2;
 
