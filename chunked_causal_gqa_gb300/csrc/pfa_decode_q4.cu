@@ -1121,37 +1121,47 @@ int launch(const Params<64>& all, const DecodeQ4Call& c) {
 // bf16, head_dim 128 (us, again / stored): one sequence of 8 kv heads, 16384 keys, 16 / 24 / 32 / 128 rows
 // 17.0 / 18.0, 20.6 / 23.4, 22.4 / 25.7, 54 / 63, 8 rows 14.6 / 14.0; 63488 keys, 32 / 256 rows 54 / 66, 325 / 384;
 // 16 sequences of 2048 keys, 16 / 24 / 32 / 128 rows 29 / 27, 36 / 34, 41 / 42, 124 / 137.
-bool scores_again(int64_t heads, int rows, int D, int dtype) {
-  return D == 128 && dtype == PFA_BF16 && (rows > 24 || (rows > 8 && heads <= 16));
+bool scores_again(int64_t heads, int rows) { return rows > 24 || (rows > 8 && heads <= 16); }
+
+// Partial sums, two slots a run.  (Slots for the most rows that a tile may have at this many rows or fewer.)
+size_t parts_bytes(int rows, int D, int dtype, int num_sms) {
+  const int rm = rows <= 8 ? 8 : D == 128 && dtype == PFA_BF16 ? 24 : 16;
+  const size_t parts = 2 * (size_t)num_sms * kBlocksPerSm * (rm * D + rm * 2) * sizeof(float);
+  return (parts + 255) & ~(size_t)255;
 }
 
-// Workspace: partial sums, two slots a run; with weights each row's sums and each score, where scores are stored.
+// Workspace: partial sums; with weights each row's sums and each score, where scores are stored.  `total` is the
+// size that callers are told, `least` what a call makes do with: where scores can be made again, no call of fewer
+// rows, sequences or keys needs more than a call that makes them again is told, so a workspace for the largest
+// call holds every smaller one.
 struct Layout {
-  size_t sums, scores, total;
+  size_t sums, scores, total, least;
   int64_t score_head;
   int row_pad;
 };
 Layout layout(int64_t heads, int rows, int D, int dtype, int64_t cap, bool weights, int num_sms) {
   Layout w = {};
-  const int rm = rows <= 8 ? 8 : rows > 16 && rows <= 24 && D == 128 && dtype == PFA_BF16 ? 24 : 16;   // most of a tile
-  const size_t parts = 2 * (size_t)num_sms * kBlocksPerSm * (rm * D + rm * 2) * sizeof(float);
-  w.sums = (parts + 255) & ~(size_t)255;
-  w.scores = w.total = w.sums;
+  w.sums = parts_bytes(rows, D, dtype, num_sms);
+  w.scores = w.total = w.least = w.sums;
   if (!weights) return w;
-  w.scores += ((size_t)heads * rows * sizeof(float2) + 255) & ~(size_t)255;
-  w.total = w.scores;
-  if (scores_again(heads, rows, D, dtype)) return w;
+  const size_t sums = ((size_t)heads * rows * sizeof(float2) + 255) & ~(size_t)255;
+  w.scores += sums;
+  const bool again = D == 128 && dtype == PFA_BF16;
+  w.total = w.least = parts_bytes(kMaxRows, D, dtype, num_sms) + sums;
+  if (again && scores_again(heads, rows)) return w;
   w.row_pad = (rows + 3) & ~3;
   w.score_head = (cap + 63) / 64 * 64 * w.row_pad;
   w.total = w.scores + (((size_t)heads * w.score_head * sizeof(float) + 255) & ~(size_t)255);
+  w.least = again ? std::min(w.total, w.least) : w.total;
   return w;
 }
 
 }  // namespace
 
-size_t decode_q4_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int64_t cap,
-                           bool weights, int num_sms) {
-  return layout(B * Hkv, (int)std::min<int64_t>(T * (H / Hkv), 1 << 30), D, dtype, cap, weights, num_sms).total;
+DecodeQ4Sizes decode_q4_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int64_t cap,
+                                  bool weights, int num_sms) {
+  const Layout w = layout(B * Hkv, (int)std::min<int64_t>(T * (H / Hkv), 1 << 30), D, dtype, cap, weights, num_sms);
+  return DecodeQ4Sizes{w.total, w.least};
 }
 
 int launch_decode_q4(const DecodeQ4Call& c) {
@@ -1175,7 +1185,7 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   char* ws = static_cast<char*>(c.ws);
   p.parts = reinterpret_cast<float*>(ws);
   p.sums = c.weights ? reinterpret_cast<float2*>(ws + w.sums) : nullptr;
-  p.scores = w.score_head > 0 ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
+  p.scores = w.score_head > 0 && c.ws_bytes >= w.total ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
   p.score_head = w.score_head;
   p.row_pad = w.row_pad;
   p.weights = c.weights;

@@ -267,11 +267,16 @@ struct DecodeQ4Call {
   int num_sms;
   int device;
   void* ws;
+  size_t ws_bytes;
   cudaStream_t stream;
 };
-// Workspace bytes of launch_decode_q4 for T tokens of each of B sequences.
-size_t decode_q4_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int64_t cap,
-                           bool weights, int num_sms);
+// Workspace bytes of launch_decode_q4 for T tokens of each of B sequences: with `total` it runs as it is
+// fastest; it needs `least`.
+struct DecodeQ4Sizes {
+  size_t total, least;
+};
+DecodeQ4Sizes decode_q4_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int64_t cap,
+                                  bool weights, int num_sms);
 int launch_decode_q4(const DecodeQ4Call& c);
 
 struct EvictQ4Call {

@@ -66,7 +66,7 @@ int check_scale(float scale, int k_exp) {
 struct PrefillPlan {
   bool decode;
   int window;             // 0: none
-  size_t total;           // workspace
+  size_t total, least;    // workspace: what callers are told; what the call needs
   int64_t lo, rows;       // read back: cache rows [lo, lo + rows) are visible
   size_t v_at, ws_at;
   Call call;              // on the read-back rows
@@ -100,8 +100,10 @@ int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window
   p->window = window;
   p->decode = prefill_by_decode(
       T, window > 0 ? std::min<int64_t>(start_pos + T, window + T) : start_pos + T, H, Hkv, D, dtype, num_sms);
+  // (the decode kernel's slots grow with the rows: those of T hold any shorter chunk's)
+  const size_t parts = decode_q4_workspace(1, T, H, Hkv, D, dtype, start_pos + T, false, num_sms).total;
   if (p->decode) {
-    p->total = decode_q4_workspace(1, T, H, Hkv, D, dtype, start_pos + T, false, num_sms);
+    p->total = p->least = parts;
     return PFA_OK;
   }
   p->lo = window > 0 ? std::max<int64_t>(0, start_pos - window + 1) : 0;
@@ -114,8 +116,8 @@ int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window
   if (rc != PFA_OK) return rc;
   p->v_at = kv;
   p->ws_at = 2 * kv;
-  p->call.ws_bytes = workspace_bytes_bf16(p->call);
-  p->total = p->ws_at + round256(p->call.ws_bytes);
+  p->least = p->ws_at;   // without more the plain schedule runs
+  p->total = std::max(parts, p->ws_at + round256(workspace_bytes_bf16(p->call)));
   return PFA_OK;
 }
 
@@ -218,7 +220,7 @@ int pfa_decode_workspace_bytes_q4(int64_t B, int64_t T, int num_heads, int num_k
   DeviceInfo d;
   if ((rc = current_device(&d)) != kOk) return rc;
   *bytes = decode_q4_workspace(B, T, num_heads, num_kv_heads, head_dim, dtype, max_seq_len,
-                               weights != 0, d.num_sms);
+                               weights != 0, d.num_sms).total;
   return PFA_OK;
 }
 
@@ -260,17 +262,16 @@ int pfa_decode_attention_q4(const void* q, const void* k4, const void* v4, const
     return PFA_ERR_ALIAS;
   DeviceInfo d;
   if ((rc = current_device(&d)) != kOk) return rc;
-  const size_t need = decode_q4_workspace(B, T, num_heads, num_kv_heads, head_dim, dtype,
-                                          max_seq_len, weights != nullptr, d.num_sms);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return PFA_ERR_SCRATCH;
-    if (overlaps(workspace, need, q, rq.span()) || overlaps(workspace, need, out, ro.span()) ||
-        overlaps(workspace, need, lengths, (size_t)B * 8) ||
-        (weights && overlaps(workspace, need, weights, wbytes)) ||
-        cache_shares(c.cache, heads, head_dim, workspace, need))
-      return PFA_ERR_ALIAS;
-    if (!device_accessible(workspace, d.device)) return PFA_ERR_DEVICE;
-  }
+  const DecodeQ4Sizes need = decode_q4_workspace(B, T, num_heads, num_kv_heads, head_dim, dtype,
+                                                 max_seq_len, weights != nullptr, d.num_sms);
+  if (!workspace || workspace_bytes < need.least) return PFA_ERR_SCRATCH;
+  const size_t used = std::min(workspace_bytes, need.total);
+  if (overlaps(workspace, used, q, rq.span()) || overlaps(workspace, used, out, ro.span()) ||
+      overlaps(workspace, used, lengths, (size_t)B * 8) ||
+      (weights && overlaps(workspace, used, weights, wbytes)) ||
+      cache_shares(c.cache, heads, head_dim, workspace, used))
+    return PFA_ERR_ALIAS;
+  if (!device_accessible(workspace, d.device)) return PFA_ERR_DEVICE;
   if (!device_accessible(q, d.device) || !device_accessible(out, d.device) ||
       !device_accessible(lengths, d.device) || !accessible(c.cache, d.device) ||
       (weights && !device_accessible(weights, d.device)))
@@ -283,7 +284,7 @@ int pfa_decode_attention_q4(const void* q, const void* k4, const void* v4, const
   c.dtype = dtype; c.scale = scale;
   c.q_row = q_stride; c.out_row = out_stride;
   c.err = d.err; c.num_sms = d.num_sms; c.device = d.device;
-  c.ws = workspace;
+  c.ws = workspace; c.ws_bytes = workspace_bytes;
   c.stream = static_cast<cudaStream_t>(stream);
   return launch_decode_q4(c);
 }
@@ -336,14 +337,12 @@ int pfa_prefill_attention_q4(const void* q, const void* k4, const void* v4, cons
   rc = prefill_plan(T, start_pos, num_heads, num_kv_heads, head_dim, window, scale, dtype, qkv_dim,
                     d.num_sms, stream, &plan);
   if (rc != PFA_OK) return rc;
-  if (plan.total > 0) {
-    if (!workspace || workspace_bytes < plan.total) return PFA_ERR_SCRATCH;
-    if (overlaps(workspace, plan.total, q, rq.span()) ||
-        overlaps(workspace, plan.total, out, ro.span()) ||
-        cache_shares(cache, num_kv_heads, head_dim, workspace, plan.total))
-      return PFA_ERR_ALIAS;
-    if (!device_accessible(workspace, d.device)) return PFA_ERR_DEVICE;
-  }
+  if (!workspace || workspace_bytes < plan.least) return PFA_ERR_SCRATCH;
+  const size_t used = std::min(workspace_bytes, plan.total);
+  if (overlaps(workspace, used, q, rq.span()) || overlaps(workspace, used, out, ro.span()) ||
+      cache_shares(cache, num_kv_heads, head_dim, workspace, used))
+    return PFA_ERR_ALIAS;
+  if (!device_accessible(workspace, d.device)) return PFA_ERR_DEVICE;
   if (!device_accessible(q, d.device) || !device_accessible(out, d.device) ||
       !accessible(cache, d.device))
     return PFA_ERR_DEVICE;
@@ -355,7 +354,7 @@ int pfa_prefill_attention_q4(const void* q, const void* k4, const void* v4, cons
     c.window = plan.window; c.dtype = dtype; c.scale = scale;
     c.q_row = qkv_dim; c.out_row = qkv_dim;
     c.err = d.err; c.num_sms = d.num_sms; c.device = d.device;
-    c.ws = workspace;
+    c.ws = workspace; c.ws_bytes = workspace_bytes;
     c.stream = static_cast<cudaStream_t>(stream);
     return launch_decode_q4(c);
   }
@@ -370,6 +369,7 @@ int pfa_prefill_attention_q4(const void* q, const void* k4, const void* v4, cons
   if ((rc = launch_cache_read_q4(r)) != kOk) return rc;
   plan.call.q = q; plan.call.out = out;
   plan.call.k = r.k_out; plan.call.v = r.v_out;
+  plan.call.ws_bytes = used - plan.ws_at;
   plan.call.ws = plan.call.ws_bytes ? base + plan.ws_at : nullptr;
   return dispatch(plan.call, PFA_BF16);
 }

@@ -115,7 +115,8 @@ def decode_attention_q4(q: torch.Tensor, cache: Q4Cache, lengths: torch.Tensor,
 def decode_workspace_bytes_q4(B: int, T: int, num_heads: int, num_kv_heads: int, head_dim: int,
                               max_seq_len: int, *, weights: bool = False,
                               dtype: torch.dtype = torch.bfloat16) -> int:
-    """Workspace bytes of decode_attention_q4 for a shape, on the current device."""
+    """Workspace bytes of decode_attention_q4 for a shape, on the current device: they also serve every
+    call of fewer tokens or sequences, of a smaller cache or without weights."""
     return _bytes("pfa_decode_workspace_bytes_q4", B, T, num_heads, num_kv_heads, head_dim,
                   _DTYPES[dtype], max_seq_len, 1 if weights else 0)
 
@@ -140,7 +141,8 @@ def prefill_attention_q4(q: torch.Tensor, cache: Q4Cache, out: torch.Tensor | No
 def prefill_workspace_bytes_q4(T: int, start_pos: int, num_heads: int, num_kv_heads: int,
                                head_dim: int, window: int = 0,
                                dtype: torch.dtype = torch.bfloat16) -> int:
-    """Workspace bytes of prefill_attention_q4 for a shape, on the current device."""
+    """Workspace bytes of prefill_attention_q4 for a shape, on the current device: they also serve every
+    call of fewer tokens, an earlier start_pos, or both."""
     return _bytes("pfa_prefill_workspace_bytes_q4", T, start_pos, num_heads, num_kv_heads, head_dim,
                   window, _DTYPES[dtype])
 

@@ -605,6 +605,10 @@ PFA_API int pfa_cache_read_q4(const void *k4, const void *v4, const void *k_scal
  *   workspace of pfa_decode_workspace_bytes_q4 bytes: with weights it can hold each score
  *             (4 bytes for each row of the T * num_heads / num_kv_heads and cache row; for bf16 at
  *             head_dim 128 not for more than 24 rows, nor for more than 8 of at most 16 heads in all).
+ *             That size also serves every call of fewer tokens or sequences, of a smaller cache or without
+ *             weights, so one for the largest call can be kept for all.  A call that finds less than its own
+ *             size in it makes its scores again instead of storing them (bf16, head_dim 128): out is the
+ *             same, the accumulated weights are within their rounding.
  * Weights of the sum over V are rounded to 11 bits (bf16) or 21 (fp32), small ones to 2^-36 of the
  * row's largest; the accumulated ones are not rounded below fp32.  Two calls that add to the
  * same weights must not run at the same time.
@@ -628,7 +632,9 @@ PFA_API int pfa_decode_workspace_bytes_q4(int64_t B, int64_t T, int num_heads, i
  * fp32), or it reads the visible rows back into the workspace and runs the 16-bit kernels on them
  * (the softmax weights are then rounded to bf16 as those kernels do).
  * workspace: pfa_prefill_workspace_bytes_q4 bytes, 256-byte aligned, not shared by calls that
- * can run at the same time.
+ * can run at the same time.  That size also serves every call of fewer tokens, an earlier start_pos, or both; the
+ * 16-bit kernels then run the schedule of pfa_prefill_attention_ws where what is left holds its workspace, and
+ * the plain one where it does not.
  */
 PFA_API int pfa_prefill_attention_q4(const void *q, const void *k4, const void *v4,
                                      const void *k_scale, const void *v_scale, void *out,
