@@ -1134,13 +1134,23 @@ size_t parts_bytes(int rows, int D, int dtype, int num_sms) {
 // size that callers are told, `least` what a call makes do with: where scores can be made again, no call of fewer
 // rows, sequences or keys needs more than a call that makes them again is told, so a workspace for the largest
 // call holds every smaller one.
+//
+// Scores go by the capacity, whatever the sequences hold of it, so no more than kMaxScores bytes of them (or one
+// sequence's) are kept: beyond that the sequences take turns, as many at a time as fit.  32 sequences of 32 fp32
+// tokens, 32/8 heads, caches of 131072 rows (us, 4 GiB / all 17 GB): up to 8192 keys used 1120 / 1062, 65536 7285 / 7326;
+// head_dim 512, bf16, 8192 used (4 GiB / 8.6 GB) 1285 / 1262.  (Making them again instead is no way out for few
+// rows: 96 sequences of one token, 32/8 heads, up to 60000 keys, stored / again 971 / 1699.)
+constexpr int64_t kMaxScores = (int64_t)1 << 32;
 struct Layout {
   size_t sums, scores, total, least;
   int64_t score_head;
+  int64_t at_once;     // sequences whose scores are kept at a time
   int row_pad;
 };
-Layout layout(int64_t heads, int rows, int D, int dtype, int64_t cap, bool weights, int num_sms) {
+Layout layout(int64_t B, int Hkv, int rows, int D, int dtype, int64_t cap, bool weights, int num_sms) {
   Layout w = {};
+  const int64_t heads = B * Hkv;
+  w.at_once = B;
   w.sums = parts_bytes(rows, D, dtype, num_sms);
   w.scores = w.total = w.least = w.sums;
   if (!weights) return w;
@@ -1148,10 +1158,15 @@ Layout layout(int64_t heads, int rows, int D, int dtype, int64_t cap, bool weigh
   w.scores += sums;
   const bool again = D == 128 && dtype == PFA_BF16;
   w.total = w.least = parts_bytes(kMaxRows, D, dtype, num_sms) + sums;
+  const int row_pad = (rows + 3) & ~3;
+  const int64_t head = (cap + 63) / 64 * 64 * row_pad, sequence = Hkv * head * (int64_t)sizeof(float);
+  const bool all = sequence <= kMaxScores / B;
   if (again && scores_again(heads, rows)) return w;
-  w.row_pad = (rows + 3) & ~3;
-  w.score_head = (cap + 63) / 64 * 64 * w.row_pad;
-  w.total = w.scores + (((size_t)heads * w.score_head * sizeof(float) + 255) & ~(size_t)255);
+  w.row_pad = row_pad;
+  w.score_head = head;
+  if (!all) w.at_once = std::max<int64_t>(1, kMaxScores / sequence);
+  // (the bound itself where sequences take turns: the size is not to fall as a sequence's grows)
+  w.total = w.scores + (all ? B * sequence : std::max(sequence, kMaxScores));
   w.least = again ? std::min(w.total, w.least) : w.total;
   return w;
 }
@@ -1160,7 +1175,7 @@ Layout layout(int64_t heads, int rows, int D, int dtype, int64_t cap, bool weigh
 
 DecodeQ4Sizes decode_q4_workspace(int64_t B, int64_t T, int H, int Hkv, int D, int dtype, int64_t cap,
                                   bool weights, int num_sms) {
-  const Layout w = layout(B * Hkv, (int)std::min<int64_t>(T * (H / Hkv), 1 << 30), D, dtype, cap, weights, num_sms);
+  const Layout w = layout(B, Hkv, (int)std::min<int64_t>(T * (H / Hkv), 1 << 30), D, dtype, cap, weights, num_sms);
   return DecodeQ4Sizes{w.total, w.least};
 }
 
@@ -1181,11 +1196,30 @@ int launch_decode_q4(const DecodeQ4Call& c) {
   p.err = c.err;
   const int64_t heads = c.span.B * c.Hkv;
   if (c.weights && heads > 0x7fffffff) return kErrShape;
-  const Layout w = layout(heads, p.rows, c.D, c.dtype, p.cap, c.weights != nullptr, c.num_sms);
+  const Layout w = layout(c.span.B, c.Hkv, p.rows, c.D, c.dtype, p.cap, c.weights != nullptr, c.num_sms);
+  const bool stored = w.score_head > 0 && c.ws_bytes >= w.total;
+  if (stored && w.at_once < c.span.B) {   // (each call's first kernel waits for the one before it to end)
+    const int64_t es = c.dtype == PFA_F32 ? 4 : 2, cache_rows = c.Hkv * c.cache.max_seq_len;
+    for (int64_t b = 0; b < c.span.B; b += w.at_once) {
+      DecodeQ4Call s = c;
+      s.span.B = std::min(w.at_once, c.span.B - b);
+      s.span.lengths += b;
+      s.q = (const char*)c.q + b * c.span.T * c.q_row * es;
+      s.out = (char*)c.out + b * c.span.T * c.out_row * es;
+      s.weights += b * cache_rows;
+      s.cache.k4 = (char*)c.cache.k4 + b * cache_rows * (c.D / 2);
+      s.cache.v4 = (char*)c.cache.v4 + b * cache_rows * (c.D / 2);
+      s.cache.k_scale = (char*)c.cache.k_scale + b * cache_rows * (c.D / 16);
+      s.cache.v_scale = (char*)c.cache.v_scale + b * cache_rows * (c.D / 16);
+      const int rc = launch_decode_q4(s);
+      if (rc != kOk) return rc;
+    }
+    return kOk;
+  }
   char* ws = static_cast<char*>(c.ws);
   p.parts = reinterpret_cast<float*>(ws);
   p.sums = c.weights ? reinterpret_cast<float2*>(ws + w.sums) : nullptr;
-  p.scores = w.score_head > 0 && c.ws_bytes >= w.total ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
+  p.scores = stored ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
   p.score_head = w.score_head;
   p.row_pad = w.row_pad;
   p.weights = c.weights;

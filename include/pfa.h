@@ -604,11 +604,13 @@ PFA_API int pfa_cache_read_q4(const void *k4, const void *v4, const void *k_scal
  *             A key's total is what pfa_cache_evict_q4 goes by.
  *   workspace of pfa_decode_workspace_bytes_q4 bytes: with weights it can hold each score
  *             (4 bytes for each row of the T * num_heads / num_kv_heads and cache row; for bf16 at
- *             head_dim 128 not for more than 24 rows, nor for more than 8 of at most 16 heads in all).
+ *             head_dim 128 not for more than 24 rows, nor for more than 8 of at most 16 heads in all;
+ *             of as many sequences at a time as fit in 4 GiB, or of one).
  *             That size also serves every call of fewer tokens or sequences, of a smaller cache or without
  *             weights, so one for the largest call can be kept for all.  A call that finds less than its own
  *             size in it makes its scores again instead of storing them (bf16, head_dim 128): out is the
- *             same, the accumulated weights are within their rounding.
+ *             same, the accumulated weights are within their rounding, and a call of few rows may take
+ *             almost twice the time.
  * Weights of the sum over V are rounded to 11 bits (bf16) or 21 (fp32), small ones to 2^-36 of the
  * row's largest; the accumulated ones are not rounded below fp32.  Two calls that add to the
  * same weights must not run at the same time.
