@@ -121,10 +121,11 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sums, int64_t&
   return __shfl_sync(0xffffffffu, all - sums[lane], warp) + up - x;
 }
 
-// Rows `rows` of width.by pieces move to 0 .. keep - 1, in place.  `rank` of `size` blocks; barrier(): theirs.
-template <int THREADS, typename T, typename B>
+// Rows `rows` of width.by pieces move to 0 .. keep - 1, in place, each piece x as as(x).  `rank` of `size` blocks;
+// barrier(): theirs.
+template <int THREADS, typename T, typename B, typename F>
 __device__ __forceinline__ void move_rows(T* base, const int32_t* rows, int keep, const Divisor& width, int rank,
-                                          int size, B&& barrier) {
+                                          int size, B&& barrier, F&& as) {
   const int w = (int)width.by, per_round = size * (THREADS * kPieces) / width;   // rows of a round
 #pragma unroll 1
   for (int at = 0; at < keep;) {
@@ -148,7 +149,7 @@ __device__ __forceinline__ void move_rows(T* base, const int32_t* rows, int keep
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int e = e0 + i * size * THREADS;
-      if (e < pieces) to[e] = x[i];
+      if (e < pieces) to[e] = as(x[i]);
     }
     at += here;
   }
@@ -317,7 +318,9 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Params p) {
   cluster_wait();
   if (tiles > 1) {
     cluster_barrier();   // the list is whole
-    move_rows<kThreads>(w, rows, p.keep, p.one, (int)rank, (int)size, [] { cluster_barrier(); });
+    // (as what its key stands for, as with one tile)
+    move_rows<kThreads>(w, rows, p.keep, p.one, (int)rank, (int)size, [] { cluster_barrier(); },
+                        [](float x) { return weight_of(key_of(x)); });
   }
   for (int64_t j = p.keep + (int64_t)rank * kThreads + tid; j < n; j += size * kThreads)
     w[j] = 0.f;
@@ -341,12 +344,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) move_kernel(const Par
                         bh * p.cap * bytes;
   const Divisor& pieces = part < 2 ? p.code_pieces : p.scale_pieces;
   auto barrier = [] { cluster_barrier(); };
+  auto as = [](auto x) { return x; };
   switch (bytes / (int)pieces.by) {
-    case 16: move_rows<THREADS>(reinterpret_cast<uint4*>(base), rows, p.keep, pieces, rank, size, barrier); break;
-    case 8: move_rows<THREADS>(reinterpret_cast<uint2*>(base), rows, p.keep, pieces, rank, size, barrier); break;
-    case 4: move_rows<THREADS>(reinterpret_cast<uint32_t*>(base), rows, p.keep, pieces, rank, size, barrier); break;
-    case 2: move_rows<THREADS>(reinterpret_cast<uint16_t*>(base), rows, p.keep, pieces, rank, size, barrier); break;
-    default: move_rows<THREADS>(base, rows, p.keep, pieces, rank, size, barrier);
+    case 16: move_rows<THREADS>(reinterpret_cast<uint4*>(base), rows, p.keep, pieces, rank, size, barrier, as); break;
+    case 8: move_rows<THREADS>(reinterpret_cast<uint2*>(base), rows, p.keep, pieces, rank, size, barrier, as); break;
+    case 4: move_rows<THREADS>(reinterpret_cast<uint32_t*>(base), rows, p.keep, pieces, rank, size, barrier, as); break;
+    case 2: move_rows<THREADS>(reinterpret_cast<uint16_t*>(base), rows, p.keep, pieces, rank, size, barrier, as); break;
+    default: move_rows<THREADS>(base, rows, p.keep, pieces, rank, size, barrier, as);
   }
 }
 

@@ -658,7 +658,8 @@ PFA_API int pfa_prefill_workspace_bytes_q4(int64_t T, int64_t start_pos, int num
  * are.  Sequences of at most `keep` rows are not changed.
  *
  *   weights      device fp32 [B][num_kv_heads][max_seq_len], updated in place.  NaN counts as
- *                larger than any number, and -0 as 0, which it becomes.
+ *                larger than any number, and -0 as 0, which it becomes where rows are cut (a
+ *                NaN stays one, of bits 0x7fffffff).
  *   lengths      device, B int64.
  *   keep, recent 1 <= keep <= max_seq_len, 0 <= recent <= keep.
  *   lengths_out  device, B int64: min(lengths[b], keep); may be lengths.  (A length out of
