@@ -72,25 +72,41 @@ struct PrefillPlan {
   Call call;              // on the read-back rows
 };
 
-// Which is faster.  The decode kernel takes some 9 us and, at head_dim 128, 1.74e-6 us for each row, kv
+// Which is faster.  The decode kernel takes some 11 us and, at head_dim 128, 1.7e-6 us for each row, kv
 // head and key; the other reads the cache back (656 bytes a key and kv head) and walks the keys with
-// 128-row tiles, about 13 us and (0.1e-3 Hkv + 0.6e-3) us a key.  Measured on GB300 (us, decode / read back):
-//   8 kv heads, rows                     96 / 112 / 128 / 192 / 384
-//     1024 keys         9.7 / 15.9                11.6 / 15.9   12.9 / 16.3   17.5 / 16.9
-//     16384 keys       33.7 / 43.2   36.7 / 43    38.5 / 43.1   54.8 / 43.4
-//     63488 keys       95.5 / 113    111 / 113    123 / 113
-//   2 kv heads, 63488 keys, rows 128 / 192 / 256    37 / 65   51 / 66   67 / 66
-//   1 kv head, 63488 keys, rows 256 / 384 / 512     38 / 88   52 / 58   66 / 59
-// head_dim 512: 9.6e-6 us for each row, kv head and key against 13e-3 us a key in each wave of the other's tiles
-//   2 kv heads, 16384 keys, rows 128 / 512   55 / 222   178 / 223
+// 128-row tiles: some 20 us (less below 1000 keys) and (0.1e-3 Hkv + 0.8e-3) us a key.  The constants are those of
+// the least time lost over 669 shapes (256 to 63488 keys, 1 to 16 kv heads, groups of 1 to 8): 0.1 % on average, 11 %
+// at most.  Measured on GB300 (us, decode / read back, the rule's last rows of decode and the next):
+//   8 kv heads,  4096 keys, rows 192 / 256     21.5 / 25.3   26.7 / 25.5
+//               16384 keys, rows 128 / 160     38.9 / 43.6   48.6 / 44.0
+//               63488 keys, rows 112 / 128      112 / 114     123 / 114
+//   2 kv heads,  4096 keys, rows 768 / 1024    22.8 / 22.9   26.8 / 23.4
+//               16384 keys, rows 384 / 512     33.1 / 35.7   39.8 / 36.4
+//               63488 keys, rows 256 / 384     67.0 / 67.2   94.9 / 61.3
+//   1 kv head,  16384 keys, rows 768 / 1024    34.6 / 39.3   40.6 / 34.9
+// head_dim 512: some 14 us and 1.1e-5 us for each row, kv head and key, against 11 us and 13e-3 us a key in each wave
+// of the other's tiles; below some 500 keys it is the launches that count (438 shapes: 0.2 % and 17 %, at 64 keys)
+//   2 kv heads,  1024 keys, rows 256 / 320     20.5 / 24.0   23.0 / 22.9
+//                4096 keys, rows 512 / 640     61.9 / 64.2   73.5 / 63.4
+//               16384 keys, rows 512 / 640      188 / 224     233 / 223
 // fp32 always runs the decode kernel: the bf16 parts of the fp32 kernel would leave some 6e-5 of the
 // output, and at head_dim 512 that attention runs on the CUDA cores.
+constexpr int64_t kWave512 = 1300, kKeys512 = 650000;
+int64_t waves_512(int64_t rows, int Hkv, int num_sms) {
+  return ((rows + 255) / 256 * 4 * Hkv + num_sms - 1) / num_sms;
+}
 bool prefill_by_decode(int64_t T, int64_t keys, int H, int Hkv, int D, int dtype, int num_sms) {
   if (dtype == PFA_F32) return true;
   const int64_t rows = T * (H / Hkv);
-  if (D == 128) return rows * Hkv <= 2300000 / keys + 57 * Hkv + 345;
-  const int64_t blocks = (rows + 255) / 256 * 4 * Hkv;
-  return rows * Hkv <= 1300 * ((blocks + num_sms - 1) / num_sms);
+  if (D == 128) return rows * Hkv <= std::min<int64_t>(4250000 / keys, 2100) + 60 * Hkv + 450;
+  return rows * Hkv <= std::max(kWave512 * waves_512(rows, Hkv, num_sms) - kKeys512 / keys, 60000 / keys + 400);
+}
+// The most keys, up to `keys`, at which T tokens or fewer may be read back.
+int64_t most_read_back(int64_t T, int64_t keys, int H, int Hkv, int D, int dtype, int num_sms) {
+  if (!prefill_by_decode(T, keys, H, Hkv, D, dtype, num_sms)) return keys;
+  if (dtype == PFA_F32 || D == 128) return 0;   // fewer rows and fewer keys run the decode kernel all the more
+  const int64_t rows = T * (H / Hkv), more = kWave512 * waves_512(rows, Hkv, num_sms) - rows * Hkv;
+  return rows * Hkv <= 400 ? 0 : more > 0 ? std::min(keys, kKeys512 / more + 1) : keys;
 }
 
 int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window, float scale,
@@ -98,12 +114,15 @@ int prefill_plan(int64_t T, int64_t start_pos, int H, int Hkv, int D, int window
   // a window of all keys is none, and the kernels' 32-bit positions stay in range
   if (window < 0 || window >= start_pos + T) window = 0;
   p->window = window;
-  p->decode = prefill_by_decode(
-      T, window > 0 ? std::min<int64_t>(start_pos + T, window + T) : start_pos + T, H, Hkv, D, dtype, num_sms);
+  const int64_t keys = window > 0 ? std::min<int64_t>(start_pos + T, window + T) : start_pos + T;
+  p->decode = prefill_by_decode(T, keys, H, Hkv, D, dtype, num_sms);
   // (the decode kernel's slots grow with the rows: those of T hold any shorter chunk's)
   const size_t parts = decode_q4_workspace(1, T, H, Hkv, D, dtype, start_pos + T, false, num_sms).total;
   if (p->decode) {
-    p->total = p->least = parts;
+    p->least = parts;
+    // (an earlier start may read back where this one does not)
+    const int64_t back = most_read_back(T, keys, H, Hkv, D, dtype, num_sms);
+    p->total = std::max(parts, 2 * round256((size_t)Hkv * back * D * elem(PFA_BF16)));
     return PFA_OK;
   }
   p->lo = window > 0 ? std::max<int64_t>(0, start_pos - window + 1) : 0;
