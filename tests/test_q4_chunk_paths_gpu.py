@@ -6,7 +6,7 @@ import chunked_causal_gqa_gb300 as pkg
 from tests import gpu_util as G
 from tests import q4_reference as R
 from tests import q8_reference as R8
-from tests.test_q4_gpu import BF16, F32, ok, randn, within
+from tests.test_q4_gpu import BF16, PREFILL, ok, randn, within
 
 pytestmark = pytest.mark.gpu
 
@@ -62,4 +62,22 @@ def test_a_size_for_a_late_chunk_serves_the_earlier_ones_of_another_path():
         paths.add(reads_back(q, cache, start))
         pkg.prefill_attention_q4(q, cache, start_pos=start, workspace=ws)
     assert len(paths) == 2
+    ok()
+
+
+@pytest.mark.parametrize("case", PREFILL, ids=str)
+def test_chunks_on_the_codes_round_their_weights_to_halves(case):
+    """The codes' own bound (weights of 11 bits) for each chunk that does not read the cache back."""
+    T, start, H, Hkv, D, window, dt = case
+    n = start + T
+    cache = pkg.Q4Cache(*R.make_cache(Hkv, n + 9, D, seed=6, device=G.dev()), 1, -2)
+    q = randn((T, H, D), dt, 4, 0.5)
+    assert reads_back(q, cache, start, window) == (case == (300, 77, 8, 2, 512, 128, BF16))
+    out = pkg.prefill_attention_q4(q, cache, start_pos=start, window=window)
+    k, v = R.values(cache.k, cache.k_scale, 1), R.values(cache.v, cache.v_scale, -2)
+    want, tol, _, _ = R.attention(q, k, v, n, window, R8.default_scale(D), dt)
+    if reads_back(q, cache, start, window):    # the 16-bit kernels round the weights to bf16
+        a, _, _, _ = R.attention(q, k, v.abs(), n, window, R8.default_scale(D), dt)
+        tol = tol + 2.0 ** -8 * a * (1 + 2.0 ** -8)
+    within(out, want, tol)
     ok()
