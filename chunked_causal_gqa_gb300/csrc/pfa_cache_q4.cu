@@ -12,11 +12,11 @@
 // (a border among them) and on the right side of every border elsewhere.
 //
 // Measured on GB300, one pass among others (GPU: in a graph):
-//   write 1 token of 32 sequences, 8 heads of 128         4.1 us, the host's call (GPU 1.9)
-//   write 2048 tokens of 8 heads of 128, bf16 (10.7 MB)   4.5 us (GPU 3.9; floor 1.6): one launch, position,
+//   write 1 token of 32 sequences, 8 heads of 128         3.9 to 4.2 us, the host's call (GPU 1.9)
+//   write 2048 tokens of 8 heads of 128, bf16 (10.7 MB)   4.3 us (GPU 3.9; floor 1.6): one launch, position,
 //     row and codes follow one another
 //   read 63488 rows of 8 heads of 128 as bf16 (333 MB)    51.0 us, 6.5 TB/s (floor 49.1): HBM
-//   read 3188 rows of 2 heads of 512 as fp32 (30 MB)      6.8 us, the host's call (GPU 5.5; floor 4.4)
+//   read 3188 rows of 2 heads of 512 as fp32 (30 MB)      6.8 to 7.4 us, the host's call (GPU 5.6; floor 4.4)
 // Reading back, a lane makes 16 output bytes at a time, so that both sides of a warp's pieces are contiguous.
 #include "pfa_internal.h"
 #include "pfa_ptx.cuh"

@@ -1,7 +1,7 @@
 // pfa_decode_q4.cu -- attention of few tokens of a batch of sequences over
 // their 4-bit caches, on the tensor cores.
 //
-// For each sequence and kv head the T * group query rows form tiles of 8 or 16 rows,
+// For each sequence and kv head the T * group query rows form tiles of 8, 16 or 24 rows,
 // and for each tile
 //   s_j = scale * <q, k_j>,  out = sum_j 2^(s_j log2 e - m) v_j / sum_j 2^(s_j log2 e - m)
 // with the maximum, the sum and the output in fp32.  A cache byte is read once for all rows of a

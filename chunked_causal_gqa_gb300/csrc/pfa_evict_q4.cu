@@ -16,7 +16,7 @@
 // writes.
 //
 // Measured on GB300, one pass among others:
-//   63488 -> 16384 rows of 8 heads of 128 (42 MB)               24.1 us (floor 6.2): 11 us of selection, a
+//   63488 -> 16384 rows of 8 heads of 128 (42 MB)               23.9 us (floor 6.2): 11 us of selection, a
 //     chain of some fifteen latencies in each of four passes and a list; 9 us for two rounds of moving
 //   32 sequences of up to 8192 rows -> 2048, 8 heads (119 MB)   39.0 us (floor 17.6): moving reads 94 MB (rows
 //     of scales are a quarter of a 32-byte sector) in 27 us

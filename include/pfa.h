@@ -533,7 +533,8 @@ PFA_API int pfa_decode_workspace_bytes_q8(int64_t B, int64_t T, int num_heads, i
  * those kernels do).  On the codes the tensor-core kernel rounds weights to 11 bits, small
  * ones to 2^-32 of the row's largest.  workspace: pfa_prefill_workspace_bytes_q8 bytes
  * (PFA_ERR_SCRATCH otherwise), 256-byte aligned, not shared by calls that can run
- * at the same time.  head_dim, heads, and what a key that only some rows see may
+ * at the same time (it goes by the path that a shape takes: a larger chunk's size does not always
+ * serve a smaller one).  head_dim, heads, and what a key that only some rows see may
  * hold: as for pfa_decode_attention_q8.
  */
 PFA_API int pfa_prefill_attention_q8(const void *q, const void *k8, const void *v8,
@@ -561,8 +562,8 @@ PFA_API int pfa_prefill_workspace_bytes_q8(int64_t T, int64_t start_pos, int num
  * scale is a full three bits fine from 2^-6 up to 448; the exponent puts the values of a layer there.
  * Rows do not depend on one another: appending one changes no other, and a row can be
  * moved as it is.  Scale pointers are aligned to the largest power of two in head_dim / 16 (up
- * to 16 bytes), code pointers to eight times that (up to 16 bytes).  Everything said above of the 8-bit cache's lengths, token rows, streams and
- * errors holds here too.
+ * to 16 bytes), code pointers to eight times that (up to 16 bytes).  Everything said above of the
+ * 8-bit cache's lengths, token rows, streams and errors holds here too.
  */
 
 /*
